@@ -26,7 +26,8 @@ EXPORTS = ("sfx_status_str", "sfx_abi_version", "sfx_predict_ws", "sfx_predict",
            "sfx_ffn_pipeline_ws", "sfx_ffn_pipeline", "sfx_stream_read", "sfx_predict_q4",
            "sfx_topk_now_update", "sfx_hot_update", "sfx_count_active", "sfx_select_kth_ws",
            "sfx_select_kth", "sfx_hot_first_order_ws", "sfx_hot_first_order", "sfx_gather_rows",
-           "sfx_dense_ffn_ws", "sfx_dense_ffn")
+           "sfx_dense_ffn_ws", "sfx_dense_ffn", "sfx_linear_q4", "sfx_kv_cache_bytes", "sfx_kv_append_q4",
+           "sfx_kv_read_q4", "sfx_attn_q4_ws", "sfx_attn_q4")
 HOT_MAX_MATS = 8
 SFX_DOWN_SCRATCH_BYTES = 17 << 20
 
@@ -117,6 +118,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sfx_ffn_pipeline_ws.argtypes = [I, I, I, I, I, I]
     lib.sfx_ffn_pipeline.restype = I
     lib.sfx_ffn_pipeline.argtypes = [P, I, I, I, I, I, I, I, P, P, Z]
+    lib.sfx_linear_q4.restype = I
+    lib.sfx_linear_q4.argtypes = [P, I, I, I, I, I, P, Z, P, P, P, I, P, Z]
+    lib.sfx_kv_cache_bytes.restype = Z
+    lib.sfx_kv_cache_bytes.argtypes = [I, I, I, I]
+    lib.sfx_kv_append_q4.restype = I
+    lib.sfx_kv_append_q4.argtypes = [P, I, I, I, I, I, I, P, Z, P, Z, P, Z, P, P, P, I, I, I, I, I, P, I, I, P, P]
+    lib.sfx_kv_read_q4.restype = I
+    lib.sfx_kv_read_q4.argtypes = [P, I, I, I, I, P, P, I, I, P, I, I, P, P, P]
+    lib.sfx_attn_q4_ws.restype = Z
+    lib.sfx_attn_q4_ws.argtypes = [I, I, I, I, I]
+    lib.sfx_attn_q4.restype = I
+    lib.sfx_attn_q4.argtypes = [P, I, I, I, I, I, P, Z, I, P, I, I, P, P, P, F, P, P, P, Z]
     _lib = lib
     return lib
 
@@ -476,6 +489,195 @@ def sfx_ffn_pipeline(wdt: int, act, B: int, d: int, h: int, f: int, descs: torch
     p = (_ptr(descs), _ptr(ws))
     st = load().sfx_ffn_pipeline(_stream(stream), wdt, a, B, d, h, f, L, p[0], p[1], ws.numel())
     _check(st, "sfx_ffn_pipeline")
+
+
+# ------------------------------------------------------------------------- int4 attention half
+
+def _same_device(where, *tensors):
+    """The device index the call's tensors share (None entries are skipped)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{where}: tensors must be on the GPU")
+        i = t.get_device()
+        if dev is None:
+            dev = i
+        elif i != dev:
+            raise ValueError(f"{where}: tensors are on different devices")
+    return dev
+
+
+def _run_on(dev, stream, fn, args, where):
+    """Call `fn(stream, *args)` with device `dev` current, on its current stream unless
+    `stream` is given."""
+    if dev == torch.cuda.current_device():
+        st = fn(torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, *args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, *args)
+    if st != 0:
+        raise SfxError(st, where)
+
+
+def _dense(t, where, name, dtype=None):
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, where, name):
+    """Row stride of a 2-D tensor whose rows are dense (rows may be apart)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{where}: {name} must be 2-D with dense rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _head_rows(t, where, name):
+    """Token stride of [tokens][heads][D] with dense heads (tokens may be apart)."""
+    if t.dim() != 3:
+        raise ValueError(f"{where}: {name} must be [tokens][heads][D]")
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{where}: the heads of {name} must be dense")
+    return t.stride(0) if T > 1 else max(t.stride(0), H * D)
+
+
+def sfx_linear_q4(x, W, W_scales, y, bias=None, accumulate=False, stream=None):
+    """y[B][n] (+)= x W^T + bias with int4 W: codes [n][d/2] uint8, W_scales
+    [n][d/group] fp16 (group 32, 64 or 128).  x [B][d] fp16 / bf16, y fp32; the rows of
+    x and y may be apart (slices of wider tensors)."""
+    w = "sfx_linear_q4"
+    ldx, ldy = _rows(x, w, "x"), _rows(y, w, "y")
+    B, d = x.shape
+    n = W.shape[0]
+    if W.dim() != 2 or W.shape[1] * 2 != d or y.shape[0] != B or y.shape[1] != n:
+        raise ValueError(f"{w}: shape mismatch")
+    if W_scales.dim() != 2 or W_scales.shape[0] != n or W_scales.shape[1] < 1 or d % W_scales.shape[1] != 0:
+        raise ValueError(f"{w}: W_scales must be [n][d / group]")
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{w}: x must be fp16 or bf16")
+    _need(y, torch.float32, "y")
+    if bias is not None and bias.numel() != n:
+        raise ValueError(f"{w}: bias must hold {n} values")
+    dev = _same_device(w, x, W, W_scales, y, bias)
+    _run_on(dev, stream, load().sfx_linear_q4,
+            (WDT[x.dtype], d // W_scales.shape[1], B, n, d, x.data_ptr(), ldx, _dense(W, w, "W", torch.uint8),
+             _dense(W_scales, w, "W_scales", torch.float16),
+             None if bias is None else _dense(bias, w, "bias", torch.float32), 1 if accumulate else 0,
+             y.data_ptr(), ldy), w)
+
+
+def kv_cache_q4(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> torch.Tensor:
+    """Uninitialised int4 key/value cache of one layer: uint8 [num_pages][Hkv][page/8][9 D]."""
+    if load().sfx_kv_cache_bytes(Hkv, D, page, num_pages) == 0:
+        raise SfxError(-2, "kv_cache_q4")
+    return torch.empty(num_pages, Hkv, page // 8, 9 * D, dtype=torch.uint8, device=device)
+
+
+def _cache_shape(cache, table, D, Hkv, w):
+    """(page, num_pages, max_pages, B) of a cache and its page table."""
+    if cache.dim() != 4 or cache.shape[1] != Hkv or cache.shape[3] != 9 * D:
+        raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/8][{9 * D}]")
+    if table.dim() != 2:
+        raise ValueError(f"{w}: table must be [B][max pages]")
+    return cache.shape[2] * 8, cache.shape[0], table.shape[1], table.shape[0]
+
+
+def _tokens(t, T, w, name):
+    if t.numel() != T:
+        raise ValueError(f"{w}: {name} must hold {T} entries")
+    return _dense(t, w, name, torch.int32)
+
+
+def sfx_kv_append_q4(q, k, v, pos, table, cache, q_out, seq=None, cos_sin=None, interleaved=False, stream=None):
+    """Rotate q [T][Hq][D] and k [T][Hkv][D] by the angles of `cos_sin` [max_pos][rot], store
+    k and v as int4 at (seq[t], pos[t]) of the paged cache and write the rotated queries
+    to q_out (fp16 / bf16).  q and q_out may be None (keys and values only)."""
+    w = "sfx_kv_append_q4"
+    ldk, ldv = _head_rows(k, w, "k"), _head_rows(v, w, "v")
+    T, Hkv, D = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError(f"{w}: k and v must have one shape and dtype")
+    if k.dtype not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {k.dtype}")
+    Hq, ldq, pq, pqo, qdt = 0, 0, None, None, 0
+    if q is not None:
+        ldq = _head_rows(q, w, "q")
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+            raise ValueError(f"{w}: q must be [{T}][Hq][{D}] in k's dtype")
+        if q_out is None or q_out.shape != q.shape:
+            raise ValueError(f"{w}: q_out must have q's shape")
+        if q_out.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"{w}: q_out must be fp16 or bf16")
+        pq, pqo, qdt = q.data_ptr(), _dense(q_out, w, "q_out"), WDT[q_out.dtype]
+    rot, max_pos, pcs = 0, 0, None
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError(f"{w}: cos_sin must be [positions][rot]")
+        max_pos, rot = cos_sin.shape
+        pcs = _dense(cos_sin, w, "cos_sin", torch.float32)
+    page, num_pages, max_pages, B = _cache_shape(cache, table, D, Hkv, w)
+    dev = _same_device(w, k, v, q, q_out, pos, seq, cos_sin, table, cache)
+    _run_on(dev, stream, load().sfx_kv_append_q4,
+            (WDT[k.dtype], qdt, T, Hq, Hkv, D, pq, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+             _tokens(pos, T, w, "pos"), None if seq is None else _tokens(seq, T, w, "seq"), pcs, rot, max_pos,
+             1 if interleaved else 0, B, max_pages, _dense(table, w, "table", torch.int32), page, num_pages,
+             _dense(cache, w, "cache", torch.uint8), pqo), w)
+
+
+def sfx_kv_read_q4(pos, table, cache, k_out, v_out, seq=None, stream=None):
+    """Values held at (seq[t], pos[t]): k_out, v_out [T][Hkv][D] (fp32, fp16 or bf16)."""
+    w = "sfx_kv_read_q4"
+    if k_out.dim() != 3 or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError(f"{w}: k_out and v_out must be [T][Hkv][D] of one dtype")
+    if k_out.dtype not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {k_out.dtype}")
+    T, Hkv, D = k_out.shape
+    page, num_pages, max_pages, B = _cache_shape(cache, table, D, Hkv, w)
+    dev = _same_device(w, pos, seq, table, cache, k_out, v_out)
+    _run_on(dev, stream, load().sfx_kv_read_q4,
+            (WDT[k_out.dtype], T, Hkv, D, _tokens(pos, T, w, "pos"),
+             None if seq is None else _tokens(seq, T, w, "seq"), B, max_pages,
+             _dense(table, w, "table", torch.int32), page, num_pages, _dense(cache, w, "cache", torch.uint8),
+             _dense(k_out, w, "k_out"), _dense(v_out, w, "v_out")), w)
+
+
+def sfx_attn_q4_ws(B: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    """Workspace bytes of sfx_attn_q4 for page tables of up to `max_len` positions."""
+    return load().sfx_attn_q4_ws(B, Hq, Hkv, D, max_len)
+
+
+def sfx_attn_q4(q, cache, table, lens, out, ws, starts=None, scale=None, lse=None, stream=None):
+    """Attention of one token per sequence over the int4 cache: q [B][Hq][D] (fp16 / bf16,
+    sequences may be apart), out [B][Hq][D] in q's dtype; positions [starts[b], lens[b]);
+    scale defaults to D ** -0.5; lse [B][Hq] fp32 optional."""
+    w = "sfx_attn_q4"
+    ldq = _head_rows(q, w, "q")
+    B, Hq, D = q.shape
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{w}: q must be fp16 or bf16")
+    if out.shape != q.shape:
+        raise ValueError(f"{w}: out must have q's shape")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError(f"{w}: lse must be [{B}][{Hq}]")
+    if cache.dim() != 4:
+        raise ValueError(f"{w}: cache must be [pages][Hkv][page/8][9 D]")
+    Hkv = cache.shape[1]
+    page, num_pages, max_pages, Bt = _cache_shape(cache, table, D, Hkv, w)
+    if Bt != B:
+        raise ValueError(f"{w}: table must have {B} rows")
+    dev = _same_device(w, q, cache, table, lens, out, ws, starts, lse)
+    _run_on(dev, stream, load().sfx_attn_q4,
+            (WDT[q.dtype], B, Hq, Hkv, D, q.data_ptr(), ldq, max_pages, _dense(table, w, "table", torch.int32), page,
+             num_pages, _dense(cache, w, "cache", torch.uint8), None if starts is None else _tokens(starts, B, w, "starts"),
+             _tokens(lens, B, w, "lens"), D ** -0.5 if scale is None else float(scale), _dense(out, w, "out", q.dtype),
+             None if lse is None else _dense(lse, w, "lse", torch.float32),
+             None if ws is None else _dense(ws, w, "ws"), 0 if ws is None else ws.numel() * ws.element_size()), w)
 
 
 STREAM_READ_OUT_WORDS = 16384

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "../../include/sfx.h"
 #include "sfx_launch.hpp"
@@ -23,6 +24,26 @@ int device_cu_count() {
   if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
   if (dev < 64) cache[dev].store(cus, std::memory_order_relaxed);
   return cus;
+}
+
+// Runs per sequence: enough workgroups of four waves for every compute unit to hold four,
+// and no run shorter than a tile per wave.
+AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len) {
+  AttnPlan p;
+  p.Hq = Hq;
+  p.G = Hq / Hkv;
+  p.HT = (p.G + 15) / 16;
+  p.HG = p.G < 16 ? p.G : 16;
+  const int units = B * Hkv * p.HT;
+  const int most = (max_len + 127) / 128;
+  p.S = (1024 + units - 1) / units;
+  if (p.S > most) p.S = most;
+  return p;
+}
+
+size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D) {
+  if (p.S <= 1) return kAttnTicketBytes;
+  return kAttnTicketBytes + (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 2) * 4;
 }
 
 }  // namespace sfx
@@ -55,6 +76,16 @@ bool row_ok(int wdt, long long n) {
   if (wdt == SFX_Q4G32) return n % 32 == 0;
   return (n * elem_bytes(wdt)) % 16 == 0;
 }
+
+// Shape of a paged int4 cache; fills `g` when it is one the kernels take.
+int kv_geom(int B, int Hkv, int D, int page, int num_pages, int max_pages, sfx::KvGeom* g) {
+  if (B < 1 || Hkv < 1 || Hkv > sfx::kAttnMaxHeads || D < 32 || D > 256 || D % 32 != 0) return SFX_E_SHAPE;
+  if (page < 8 || page > 1024 || (page & (page - 1)) != 0 || num_pages < 1 || max_pages < 1) return SFX_E_SHAPE;
+  if ((long long)max_pages * page > (1ll << 30)) return SFX_E_SHAPE;
+  *g = sfx::KvGeom{B, Hkv, D, __builtin_ctz((unsigned)page), num_pages, max_pages};
+  return SFX_OK;
+}
+constexpr int kKvMaxTokens = (1 << 24) - 1;   // one workgroup column of 256 threads per token
 
 }  // namespace
 
@@ -368,6 +399,93 @@ int sfx_ffn_pipeline(void* stream, int wdt, int act, int B, int d, int h, int f,
   const int w = check_ws(ws, ws_bytes, sfx::step_ws_bytes(B, h, f, P));
   if (w != SFX_OK) return w;
   return launch_status(sfx::launch_pipe((hipStream_t)stream, wdt, act, B, d, h, f, L, layers, ws, g));
+}
+
+// ------------------------------------------------------------------------------ int4 projection
+
+int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const void* x, size_t ldx, const void* W,
+                  const void* W_scales, const float* bias, int accumulate, float* y, size_t ldy) {
+  if (xdt != SFX_F16 && xdt != SFX_BF16) return SFX_E_DTYPE;
+  if (group != 32 && group != 64 && group != 128) return SFX_E_SHAPE;
+  if (B < 1 || B > SFX_MAX_B || n < 1 || n > (1 << 24) || d < 1 || d > (1 << 24) || d % group != 0) return SFX_E_SHAPE;
+  if (ldx < (size_t)d || ldy < (size_t)n) return SFX_E_SHAPE;
+  if (!x || !W || !W_scales || !y) return SFX_E_NULL;
+  if (!aligned16(x) || !aligned16(W) || ldx % 8 != 0) return SFX_E_ALIGN;
+  if (((uintptr_t)W_scales & 1u) || !aligned4(y) || (bias && !aligned4(bias))) return SFX_E_ALIGN;
+  const int gsh = group == 32 ? 0 : group == 64 ? 1 : 2;
+  const auto f = xdt == SFX_F16 ? sfx::launch_linear_q4_f16 : sfx::launch_linear_q4_bf16;
+  return launch_status(f((hipStream_t)stream, gsh, B, n, d, x, ldx * 2, W, W_scales, bias, accumulate, y, ldy));
+}
+
+// ------------------------------------------------------------------------------ int4 key/value cache
+
+size_t sfx_kv_cache_bytes(int Hkv, int D, int page, int num_pages) {
+  sfx::KvGeom g;
+  if (kv_geom(1, Hkv, D, page, num_pages, 1, &g) != SFX_OK) return 0;
+  return (size_t)num_pages * Hkv * (page / 8) * 9 * D;
+}
+
+int sfx_kv_append_q4(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int D, const void* q, size_t ldq,
+                     const void* k, size_t ldk, const void* v, size_t ldv, const int32_t* pos, const int32_t* seq,
+                     const float* cos_sin, int rot, int max_pos, int interleaved, int B, int max_pages,
+                     const int32_t* table, int page, int num_pages, void* cache, void* q_out) {
+  if (xdt != SFX_F32 && xdt != SFX_F16 && xdt != SFX_BF16) return SFX_E_DTYPE;
+  if (q && qdt != SFX_F16 && qdt != SFX_BF16) return SFX_E_DTYPE;
+  sfx::KvGeom g;
+  const int st = kv_geom(B, Hkv, D, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (T < 1 || T > kKvMaxTokens) return SFX_E_SHAPE;
+  if (q && (Hq < 1 || Hq > sfx::kAttnMaxHeads || ldq < (size_t)Hq * D)) return SFX_E_SHAPE;
+  if (ldk < (size_t)Hkv * D || ldv < (size_t)Hkv * D) return SFX_E_SHAPE;
+  if (cos_sin && (rot < 2 || rot > D || rot % 2 != 0 || max_pos < 1)) return SFX_E_SHAPE;
+  if (!k || !v || !pos || !table || !cache || (q && !q_out)) return SFX_E_NULL;
+  const uintptr_t em = (uintptr_t)elem_bytes(xdt) - 1;
+  if (((uintptr_t)k & em) || ((uintptr_t)v & em) || ((uintptr_t)q & em) || !aligned16(cache) || ((uintptr_t)q_out & 1u))
+    return SFX_E_ALIGN;
+  if (!aligned4(pos) || !aligned4(table) || (seq && !aligned4(seq)) || (cos_sin && !aligned4(cos_sin)))
+    return SFX_E_ALIGN;
+  return launch_status(sfx::launch_kv_append_q4((hipStream_t)stream, g, xdt, qdt, T, q ? Hq : 0, q, ldq, k, ldk, v, ldv,
+                                                pos, seq, cos_sin, rot, max_pos, interleaved != 0, table, cache, q_out));
+}
+
+int sfx_kv_read_q4(void* stream, int odt, int T, int Hkv, int D, const int32_t* pos, const int32_t* seq, int B,
+                   int max_pages, const int32_t* table, int page, int num_pages, const void* cache, void* k, void* v) {
+  if (odt != SFX_F32 && odt != SFX_F16 && odt != SFX_BF16) return SFX_E_DTYPE;
+  sfx::KvGeom g;
+  const int st = kv_geom(B, Hkv, D, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (T < 1 || T > kKvMaxTokens) return SFX_E_SHAPE;
+  if (!pos || !table || !cache || !k || !v) return SFX_E_NULL;
+  if (!aligned16(cache) || !aligned16(k) || !aligned16(v)) return SFX_E_ALIGN;
+  if (!aligned4(pos) || !aligned4(table) || (seq && !aligned4(seq))) return SFX_E_ALIGN;
+  return launch_status(sfx::launch_kv_read_q4((hipStream_t)stream, g, odt, T, pos, seq, table, cache, k, v));
+}
+
+size_t sfx_attn_q4_ws(int B, int Hq, int Hkv, int D, int max_len) {
+  if (B < 1 || B > SFX_MAX_B || Hkv < 1 || Hq < 1 || Hq > sfx::kAttnMaxHeads || Hq % Hkv != 0 || D < 32 || D > 256 ||
+      D % 32 != 0 || max_len < 1 || max_len > (1 << 30))
+    return 0;
+  return sfx::attn_ws_bytes(sfx::attn_plan(B, Hq, Hkv, max_len), B, Hkv, D);
+}
+
+int sfx_attn_q4(void* stream, int qdt, int B, int Hq, int Hkv, int D, const void* q, size_t ldq, int max_pages,
+                const int32_t* table, int page, int num_pages, const void* cache, const int32_t* starts,
+                const int32_t* lens, float scale, void* out, float* lse, void* ws, size_t ws_bytes) {
+  if (qdt != SFX_F16 && qdt != SFX_BF16) return SFX_E_DTYPE;
+  sfx::KvGeom g;
+  const int st = kv_geom(B, Hkv, D, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (B > SFX_MAX_B || Hq < 1 || Hq > sfx::kAttnMaxHeads || Hq % Hkv != 0 || ldq < (size_t)Hq * D) return SFX_E_SHAPE;
+  if (!(scale > -INFINITY && scale < INFINITY)) return SFX_E_SHAPE;
+  if (!q || !table || !cache || !lens || !out) return SFX_E_NULL;
+  if (!aligned16(q) || ldq % 8 != 0 || !aligned16(cache) || !aligned16(out)) return SFX_E_ALIGN;
+  if (!aligned4(table) || !aligned4(lens) || (starts && !aligned4(starts)) || (lse && !aligned4(lse))) return SFX_E_ALIGN;
+  const sfx::AttnPlan p = sfx::attn_plan(B, Hq, Hkv, max_pages * page);
+  const int w = check_ws(ws, ws_bytes, sfx::attn_ws_bytes(p, B, Hkv, D));
+  if (w != SFX_OK) return w;
+  const auto f = qdt == SFX_F16 ? sfx::launch_attn_q4_f16 : sfx::launch_attn_q4_bf16;
+  return launch_status(f((hipStream_t)stream, p, g, q, ldq * 2, cache, table, starts, lens, scale * 1.44269504088896341f,
+                         out, lse, ws));
 }
 
 // ------------------------------------------------------------------------------ measurement helper

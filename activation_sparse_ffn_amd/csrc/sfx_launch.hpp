@@ -75,4 +75,39 @@ hipError_t launch_hot_assign(hipStream_t s, int L, int G, int K, const uint32_t*
 hipError_t launch_hot_copy(hipStream_t s, int L, int K, const HotMats& mats, const void* const* src,
                            void* const* dst, const int32_t* copies, const int32_t* ncopies);
 
+// Int4 projection (gsh = log2(group / 32)).
+hipError_t launch_linear_q4_f16(hipStream_t s, int gsh, int B, int n, int d, const void* x, size_t ldx_bytes,
+                                const void* W, const void* Ws, const float* bias, int accumulate, float* y, size_t ldy);
+hipError_t launch_linear_q4_bf16(hipStream_t s, int gsh, int B, int n, int d, const void* x, size_t ldx_bytes,
+                                 const void* W, const void* Ws, const float* bias, int accumulate, float* y,
+                                 size_t ldy);
+
+// Paged int4 key/value cache.
+struct KvGeom {
+  int B, Hkv, D, page_shift, num_pages, max_pages;
+};
+hipError_t launch_kv_append_q4(hipStream_t s, const KvGeom& g, int xdt, int qdt, int T, int Hq, const void* q, size_t ldq,
+                               const void* k, size_t ldk, const void* v, size_t ldv, const int32_t* pos,
+                               const int32_t* seq, const float* cos_sin, int rot, int max_pos, int pairs,
+                               const int32_t* table, void* cache, void* q_out);
+hipError_t launch_kv_read_q4(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
+                             const int32_t* table, const void* cache, void* k, void* v);
+
+// Decode attention: heads per workgroup and the number of runs a sequence is split into.
+struct AttnPlan {
+  int Hq, G, HT, HG, S;      // query heads, per kv head, tiles of 16 of those, heads of a full tile, runs
+};
+// Tickets of every (sequence, kv head, head tile) up to SFX_MAX_B x 256 query heads, at the
+// start of the workspace whatever the shape, so shapes that share one never meet there.
+constexpr int kAttnMaxHeads = 256;
+constexpr size_t kAttnTicketBytes = (size_t)SFX_MAX_B * kAttnMaxHeads * 4;
+AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len);
+size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D);
+hipError_t launch_attn_q4_f16(hipStream_t s, const AttnPlan& p, const KvGeom& g, const void* q, size_t ldq_bytes,
+                              const void* cache, const int32_t* table, const int32_t* starts, const int32_t* lens,
+                              float k2, void* out, float* lse, void* ws);
+hipError_t launch_attn_q4_bf16(hipStream_t s, const AttnPlan& p, const KvGeom& g, const void* q, size_t ldq_bytes,
+                               const void* cache, const int32_t* table, const int32_t* starts, const int32_t* lens,
+                               float k2, void* out, float* lse, void* ws);
+
 }  // namespace sfx

@@ -14,6 +14,8 @@
  *   sfx_hot_update   hot region slots + copy of entering groups  once per step, all layers
  *   sfx_select_kth, sfx_count_active, sfx_hot_first_order, sfx_gather_rows
  *                    offline calibration: thresholds, frequencies, hot-first order
+ *   sfx_linear_q4, sfx_kv_append_q4, sfx_kv_read_q4, sfx_attn_q4
+ *                    the attention half of a layer: int4 projections, paged int4 cache
  *
  * Conventions shared by every entry point
  *   - Every pointer argument is a caller-owned DEVICE pointer unless the comment
@@ -474,6 +476,98 @@ int sfx_ffn_step(void* stream, int wdt, int act, int B, int d, int h, int f, int
 size_t sfx_ffn_pipeline_ws(int wdt, int act, int B, int d, int h, int f);
 int sfx_ffn_pipeline(void* stream, int wdt, int act, int B, int d, int h, int f, int L,
                      const sfx_layer* layers, void* ws, size_t ws_bytes);
+
+/* ---------------------------------------------------------------------------------
+ * The attention half of a decode layer in the storage of the int4 rows: projections
+ * with int4 weights, a paged int4 key/value cache, and attention of one token per
+ * sequence over it.
+ *
+ * sfx_linear_q4 -- y[b][i] (+)= sum_c W[i][c] x[b][c] + bias[i],  W = q * s.
+ *   xdt       SFX_F16 or SFX_BF16 (x).
+ *   group     columns per scale: 32 (the SFX_Q4G32 layout), 64 or 128; d % group == 0.
+ *   x         [B] rows of d elements, ldx elements apart (ldx a multiple of 8).
+ *   W         [n][d/2] codes as in SFX_Q4G32; W_scales [n][d/group] binary16 (2-byte
+ *             aligned).  bias [n] fp32 or NULL.
+ *   accumulate  0: y is overwritten; otherwise the product is added to it.
+ *   y         [B] rows of n fp32, ldy elements apart (4-byte aligned).
+ * B 1..64, n and d up to 2^24.  Products of a code and x are exact; a group's sum and
+ * the sum over groups are fp32, in an order fixed by the shape: y is bitwise
+ * reproducible.  Neither infinities nor NaN in x stay confined to finite results:
+ * they give a non-finite y for their token only.
+ * ------------------------------------------------------------------------------- */
+int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const void* x, size_t ldx,
+                  const void* W, const void* W_scales, const float* bias, int accumulate,
+                  float* y, size_t ldy);
+
+/* ---------------------------------------------------------------------------------
+ * Paged int4 key/value cache of one layer.  sfx_kv_cache_bytes(Hkv, D, page, num_pages)
+ * bytes of caller-owned device memory, 16-byte aligned, any contents at the start:
+ * [num_pages][Hkv][page/8] blocks of 9 D bytes, each 8 consecutive positions of one kv
+ * head: 4 D bytes of K codes (per position words [c < 4][g < D/32]; word (c, g) holds
+ * dims 32g + 8c + 2j and + 2j + 1 in nibbles j and j + 4), 4 D bytes of V codes
+ * ([n < 16][g][8]; the bytes of positions 0 2 1 3 4 6 5 7, dim 32g + n in the low and
+ * 32g + 16 + n in the high nibble), then binary16 scales [g][8 positions] of K and of V.
+ * A code is q + 8, a value q * scale, one scale per 32 dims.
+ *   Hkv 1..256;  D a multiple of 32 in 32..256;  page a power of two in 8..1024.
+ *   table     [B][max_pages] int32: page p / page of sequence b holds its position p.
+ *             A page id outside [0, num_pages) is no page: appends to it are skipped,
+ *             reads give zeros, attention leaves its positions out.
+ *             max_pages * page <= 2^30.
+ *   pos, seq  [T] int32: position and sequence of token t; seq NULL = token t belongs
+ *             to sequence t.  A token with pos < 0, a seq outside [0, B) or a position
+ *             without a page (or, where a table of angles is given, past its end) is
+ *             padding.
+ *
+ * sfx_kv_append_q4 -- rotates and stores T tokens (1..2^24 - 1):
+ *   k' = R(pos) k;  s = fp16(max |k'| / 7),  q = clamp(rne(k' / s), -8, 7) per 32 dims;
+ *   v alike, not rotated;  q_out = R(pos) q.
+ *   xdt       SFX_F32, SFX_F16 or SFX_BF16: q [T][Hq][D], k and v [T][Hkv][D], heads
+ *             dense, tokens ldq / ldk / ldv elements apart (slices of one projection).
+ *             q NULL: keys and values only (Hq, qdt, q_out unused).
+ *   cos_sin   [max_pos][rot] fp32, cosines of the rot/2 angles of a position, then their
+ *             sines; NULL: no rotation.  rot even, 2..D; dims from rot on are not turned.
+ *             Pair j is dims (j, j + rot/2), or (2j, 2j + 1) if interleaved.
+ *   q_out     [T][Hq][D] in qdt (SFX_F16 or SFX_BF16), dense; must not overlap q.
+ *             A padding token's row is left as it was.
+ * The rotation is taken in 64 bits and rounded once to fp32.  A scale is at most 65504
+ * for K and 8188 for V (larger values are clipped to 7 scales); a group that holds a NaN
+ * or an infinity takes a NaN scale.  Two tokens of one call must not name the same
+ * position of a page.  Different calls may append to one cache at the same time as long
+ * as no 8-position block is written by both.
+ *
+ * sfx_kv_read_q4 -- values of T listed positions: k, v [T][Hkv][D] in odt (SFX_F32 exact,
+ *   SFX_F16 / SFX_BF16 rounded once), written; zeros for a padding token.
+ *
+ * sfx_attn_q4 -- o[b][h] = sum_p w_p v_p,  w = softmax over p in [starts[b], lens[b]) of
+ *   scale q[b][h] . k_p, with kv head h / (Hq / Hkv).
+ *   qdt       SFX_F16 or SFX_BF16 (q and out).   B 1..64, Hq 1..256, Hq % Hkv == 0.
+ *   q         [B][Hq][D], sequences ldq elements apart (a multiple of 8).
+ *   lens      [B] int32 (clamped to [0, max_pages * page]); starts [B] int32 or NULL
+ *             (0): a sliding window or left padding.  Nothing to attend to gives a zero
+ *             row and lse = -inf.  What the cache holds at positions left out, NaN
+ *             included, does not matter.
+ *   out       [B][Hq][D] in qdt, dense, written.   lse [B][Hq] fp32 or NULL: the natural
+ *             logarithm of the sum of exp(scale q . k_p), to join with other positions.
+ *   ws        >= sfx_attn_q4_ws(B, Hq, Hkv, D, max_pages * page) bytes.
+ * Several query tokens of one sequence (drafted tokens) are rows with the same table
+ * entries and their own lens.  Sums are fp32; a weight and a dequantised value are each
+ * rounded once to fp16 (weights relative to the largest, down to 2^-33 of it).  Results
+ * are bitwise reproducible for the same shapes and lens.
+ * ------------------------------------------------------------------------------- */
+size_t sfx_kv_cache_bytes(int Hkv, int D, int page, int num_pages);
+int sfx_kv_append_q4(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int D,
+                     const void* q, size_t ldq, const void* k, size_t ldk, const void* v, size_t ldv,
+                     const int32_t* pos, const int32_t* seq, const float* cos_sin, int rot, int max_pos,
+                     int interleaved, int B, int max_pages, const int32_t* table, int page, int num_pages,
+                     void* cache, void* q_out);
+int sfx_kv_read_q4(void* stream, int odt, int T, int Hkv, int D, const int32_t* pos, const int32_t* seq,
+                   int B, int max_pages, const int32_t* table, int page, int num_pages,
+                   const void* cache, void* k, void* v);
+size_t sfx_attn_q4_ws(int B, int Hq, int Hkv, int D, int max_len);
+int sfx_attn_q4(void* stream, int qdt, int B, int Hq, int Hkv, int D, const void* q, size_t ldq,
+                int max_pages, const int32_t* table, int page, int num_pages, const void* cache,
+                const int32_t* starts, const int32_t* lens, float scale, void* out, float* lse,
+                void* ws, size_t ws_bytes);
 
 /* ---------------------------------------------------------------------------------
  * sfx_stream_read -- measurement helper, not a step of the method.  Reads the nbytes
