@@ -26,8 +26,8 @@ int device_cu_count() {
   return cus;
 }
 
-// Runs per sequence: enough workgroups of four waves for every compute unit to hold four,
-// and no run shorter than a tile per wave.
+// Runs per sequence: one workgroup of eight waves per compute unit, and no run shorter
+// than a tile per wave.
 AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len) {
   AttnPlan p;
   p.Hq = Hq;
@@ -35,15 +35,15 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len) {
   p.HT = (p.G + 15) / 16;
   p.HG = p.G < 16 ? p.G : 16;
   const int units = B * Hkv * p.HT;
-  const int most = (max_len + 127) / 128;
-  p.S = (1024 + units - 1) / units;
+  const int most = (max_len + 255) / 256;
+  p.S = (256 + units - 1) / units;
   if (p.S > most) p.S = most;
   return p;
 }
 
 size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D) {
   if (p.S <= 1) return kAttnTicketBytes;
-  return kAttnTicketBytes + (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 2) * 4;
+  return kAttnTicketBytes + (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 4) * 4;
 }
 
 }  // namespace sfx
