@@ -23,10 +23,10 @@ namespace {
 
 constexpr int kAttnTile = 32;          // positions a wave takes at a time
 constexpr float kRefMin = -3.0e38f;
-// Waves of a workgroup, and whether the next tile's registers are loaded while one is worked
-// on: from 160 dims on, two tiles do not fit the registers of two waves per SIMD.
+// Waves of a workgroup and tiles of LDS per wave: two workgroups fit a compute unit's 160 KB,
+// and a wave always has a tile or more on the way while it works on one.
 constexpr int attn_waves(int NG) { return NG <= 4 ? 8 : 4; }
-constexpr bool attn_ahead(int NG) { return NG <= 4; }
+constexpr int attn_slots(int NG) { return NG <= 2 ? 4 : NG == 5 ? 3 : 2; }
 
 struct AttnArgs {
   KvCache kv;
@@ -63,13 +63,6 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-__device__ __forceinline__ uint32_t pk_add24(uint32_t a) {
-  const half2_t k = {(_Float16)-24.0f, (_Float16)-24.0f};
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) + k);
-}
-__device__ __forceinline__ uint32_t pk_mul(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) * __builtin_bit_cast(half2_t, b));
-}
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const half2_t h = {(_Float16)a, (_Float16)b};
   return __builtin_bit_cast(uint32_t, h);
@@ -84,44 +77,52 @@ __device__ __forceinline__ float quarters_sum(float v, int lane) {
   return v + __uint_as_float(lane_xor_u32<16>(__float_as_uint(v), lane));
 }
 
-// What a lane holds of 32 positions: K rows of position n % 4 (+ 4) of octet n / 4, words of
-// quarter c; V unit n and the scales of octet c.
-template <int NG>
-struct AttnTile {
-  uint32_t k[2][NG], v[2 * NG];
-  Raw<16> ks[NG], vs[NG];
-  uint32_t on;              // bit i: position i of octet c counts
+// ---- the cache's way into LDS.  A tile of 32 positions is NP pieces of the cache, contiguous
+// bytes of one page each (1: pages of 32 or more, 2: 16, 4: 8), copied without passing
+// through registers.
+
+template <int NG, int NP>
+struct AttnPieces {
+  static constexpr int chunks = 72 * NG / NP;                  // of 16 bytes, per piece
+  static constexpr int loads = (chunks + kWave - 1) / kWave;   // instructions per piece
+  static constexpr int count = NP * loads;                     // per tile
 };
 
-// Pages of the two octets a lane reads in tile `it` (-1: none).
-struct AttnPages {
-  int k, v;
-};
-__device__ __forceinline__ AttnPages attn_pages(const AttnArgs& a, int b, int it, int n, int c) {
-  return AttnPages{kv_page(a.kv, b, it * kAttnTile + 8 * (n >> 2)), kv_page(a.kv, b, it * kAttnTile + 8 * c)};
+// Page ids of a wave's next 64 / NP tiles, one piece per lane; tile `it` of the sequence is
+// the wave's tile (it - first) / W from lane 0.
+template <int NP>
+__device__ __forceinline__ int attn_ids(const KvCache& kv, int b, int it, int W, int te, int lane) {
+  const int t = min(it + (lane / NP) * W, te - 1);
+  return kv_page(kv, b, t * kAttnTile + (lane % NP) * (kAttnTile / NP));
 }
 
-template <int NG>
-__device__ __forceinline__ void attn_load(const AttnArgs& a, int h, int it, AttnPages id, int start, int end, int n, int c,
-                                          AttnTile<NG>& x) {
-  constexpr int D = 32 * NG;
-  const int page_mask = (1 << a.kv.page_shift) - 1;
-  const int pk = it * kAttnTile + 8 * (n >> 2), pv = it * kAttnTile + 8 * c;
-  const uint8_t* bk = a.kv.base + kv_block(a.kv, max(id.k, 0), h, (pk & page_mask) >> 3);
-  const uint8_t* bv = a.kv.base + kv_block(a.kv, max(id.v, 0), h, (pv & page_mask) >> 3);
+template <int NG, int NP>
+__device__ __forceinline__ void attn_copy(const KvCache& kv, int h, int it, int ids, int at, uint8_t* dst, int lane) {
+  using P = AttnPieces<NG, NP>;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) load_words<NG>(bk + (4 * t + (n & 3)) * (D / 2) + c * 4 * NG, x.k[t]);
+  for (int p = 0; p < NP; ++p) {
+    const int pos = it * kAttnTile + p * (kAttnTile / NP);
+    const int id = max(__builtin_amdgcn_readlane(ids, at * NP + p), 0);
+    const uint32_t blk = ((uint32_t)(id * kv.Hkv + h) << (kv.page_shift - 3)) +
+                         (uint32_t)((pos & ((1 << kv.page_shift) - 1)) >> 3);
+    const uint8_t* src = kv.base + (size_t)blk * (288 * NG);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) x.ks[g] = load_raw<16>(bv + 8 * D + 16 * g);
-  load_words<2 * NG>(bv + 4 * D + n * 8 * NG, x.v);
-#pragma unroll
-  for (int g = 0; g < NG; ++g) x.vs[g] = load_raw<16>(bv + 8 * D + D / 2 + 16 * g);
-  uint32_t on = id.v < 0 ? 0u : 0xFFu;
-  const int lo = start - pv, hi = end - pv;
-  if (lo > 0) on &= lo >= 8 ? 0u : 0xFFu << lo;
-  if (hi < 8) on &= hi <= 0 ? 0u : (1u << hi) - 1u;
-  x.on = on;
+    for (int j = 0; j < P::loads; ++j) {
+      const int left = P::chunks - j * kWave;
+      if (left >= kWave || lane < left)
+        __builtin_amdgcn_global_load_lds((const void*)(src + (size_t)(uint32_t)((j * kWave + lane) * 16)),
+                                         (__attribute__((address_space(3))) void*)(dst + (p * P::chunks + j * kWave) * 16),
+                                         16, 0, 0);
+    }
+  }
 }
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N < 64, "vmcnt holds 6 bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // Running state of a wave: per lane the head n, of products m the dims 16 m + 4 c + i.
 template <int NG>
@@ -130,45 +131,69 @@ struct AttnState {
   f32x4 acc[2 * NG];
 };
 
+// One tile, from LDS.  A lane takes K rows of position n % 4 (+ 4) of octet n / 4, words of
+// quarter c; V unit n and the scales of octet c.  `on`: bit i says that position i of octet
+// c counts (all ones where `full`).
 template <class T, int NG>
-__device__ __forceinline__ void attn_tile(AttnTile<NG>& x, const Raw<16> (&qf)[NG], float k2, int lane,
+__device__ __forceinline__ void attn_tile(const uint8_t* tile, const Raw<16> (&qf)[NG], const Q4<T>& kc,
+                                          const Q4<TF16>& vc, float k2, bool full, uint32_t on, int lane,
                                           AttnState<NG>& st) {
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  constexpr int D = 32 * NG;
+  const int n = lane & 15, c = lane >> 4;
+  const uint8_t *bk = tile + (n >> 2) * 9 * D, *bv = tile + c * 9 * D;
+  uint32_t kw[2][NG], vw[2 * NG];
+  Raw<16> ks[NG], vs[NG];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) load_words<NG>(bk + (4 * t + (n & 3)) * (D / 2) + c * 4 * NG, kw[t]);
+#pragma unroll
+  for (int g = 0; g < NG; ++g) ks[g] = load_raw<16>(bv + 8 * D + 16 * g);
   float s[8];
+  Raw<16> m24;
+  if constexpr (Q4<T>::offset) m24 = Q4<T>::minus24();
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int g = 0; g < NG; ++g) {
+    f32x4 from = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (Q4<T>::offset) from = Mma<T>::run(m24, qf[g], from);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      // the -24 sum(q) of the codes' offset as a product of its own: the matrix cores have
-      // the time, and its result would hold 4 registers per group
-      f32x4 p = Mma<T>::run(q4_minus24<T>(), qf[g], zero);
-      p = Mma<T>::run(q4_word<T>(x.k[t][g]), qf[g], p);
+    for (int t = 0; t < 2; ++t) {
+      const f32x4 p = Mma<T>::run(kc.word(kw[t][g]), qf[g], from);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float sc = half_at(x.ks[g].w[2 * t + (i >> 1)], i & 1);
+        const float sc = half_at(ks[g].w[2 * t + (i >> 1)], i & 1);
         s[4 * t + i] = g == 0 ? sc * p[i] : fmaf(sc, p[i], s[4 * t + i]);
       }
     }
+  }
+  // the values' part is read only now: its registers are the scores' until here
+  __builtin_amdgcn_sched_barrier(0);
+  load_words<2 * NG>(bv + 4 * D + n * 8 * NG, vw);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] *= k2;
-  if (!__all(x.on == 0xFFu)) {
+  for (int g = 0; g < NG; ++g) vs[g] = load_raw<16>(bv + 8 * D + D / 2 + 16 * g);
+  const float off = 9.f - st.ref;
+  float e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = fmaf(s[i], k2, off);
+  if (!full) {
     // some position does not count: its weight is 0 and so is its value, whatever is held there
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (!((x.on >> i) & 1u)) s[i] = -INFINITY;
+      if (!((on >> i) & 1u)) e[i] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t keep =
-          ((x.on >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((x.on >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+      const uint32_t keep = ((on >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((on >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) x.vs[g].w[i] &= keep;
+      for (int g = 0; g < NG; ++g) vs[g].w[i] &= keep;
     }
   }
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, s[i]);
-  if (__any(top > st.ref + 6.f)) {
-    const float next = fmaxf(quarters_max(top, lane), st.ref);
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, e[i]);
+  if (__any(top > 15.f)) {
+    // raise the reference to the largest score so far
+    float most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, e[i] == -INFINITY ? e[i] : s[i] * k2);
+    const float next = fmaxf(quarters_max(most, lane), st.ref);
     const float f = exp2f(st.ref - next);
     st.ref = next;
     st.sum *= f;
@@ -176,31 +201,26 @@ __device__ __forceinline__ void attn_tile(AttnTile<NG>& x, const Raw<16> (&qf)[N
     for (int m = 0; m < 2 * NG; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.acc[m][i] *= f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = e[i] == -INFINITY ? e[i] : fmaf(s[i], k2, 9.f - next);
   }
-  const float off = 9.f - st.ref;
   Raw<16> p;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float e0 = __builtin_amdgcn_exp2f(s[2 * i] + off), e1 = __builtin_amdgcn_exp2f(s[2 * i + 1] + off);
+    const float e0 = __builtin_amdgcn_exp2f(e[2 * i]), e1 = __builtin_amdgcn_exp2f(e[2 * i + 1]);
     st.sum += e0 + e1;
     p.w[i] = pack_f16(e0, e1);
   }
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     Raw<16> lo, hi;
-    const uint32_t w0 = x.v[2 * g], w1 = x.v[2 * g + 1];
-    lo.w[0] = q4_pair<TF16, 0>(w0);
-    hi.w[0] = q4_pair<TF16, 1>(w0);
-    lo.w[1] = q4_pair<TF16, 2>(w0);
-    hi.w[1] = q4_pair<TF16, 3>(w0);
-    lo.w[2] = q4_pair<TF16, 0>(w1);
-    hi.w[2] = q4_pair<TF16, 1>(w1);
-    lo.w[3] = q4_pair<TF16, 2>(w1);
-    hi.w[3] = q4_pair<TF16, 3>(w1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo.w[i] = pk_mul(pk_add24(lo.w[i]), x.vs[g].w[i]);
-      hi.w[i] = pk_mul(pk_add24(hi.w[i]), x.vs[g].w[i]);
+    for (int j = 0; j < 2; ++j) {
+      const Raw<16> u = vc.word(vw[2 * g + j]);               // (dim n, dim n + 16) of positions 4 j + (0 1), (2 3)
+      lo.w[2 * j] = pk_mul(u.w[0], vs[g].w[2 * j]);
+      hi.w[2 * j] = pk_mul(u.w[1], vs[g].w[2 * j]);
+      lo.w[2 * j + 1] = pk_mul(u.w[2], vs[g].w[2 * j + 1]);
+      hi.w[2 * j + 1] = pk_mul(u.w[3], vs[g].w[2 * j + 1]);
     }
     st.acc[2 * g] = Mma<TF16>::run(lo, p, st.acc[2 * g]);
     st.acc[2 * g + 1] = Mma<TF16>::run(hi, p, st.acc[2 * g + 1]);
@@ -211,13 +231,69 @@ __device__ __forceinline__ float attn_lse(float ref, float sum) {
   return sum != 0.f ? (ref - 9.f + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
+// The tiles of one wave: tb + wave, then every W-th.
+template <class T, int NG, int NP>
+__device__ __forceinline__ void attn_wave(const AttnArgs& a, int b, int h, int it, int te, int start, int end, int lane,
+                                          uint8_t* ring, const Raw<16> (&qf)[NG], AttnState<NG>& st) {
+  constexpr int W = attn_waves(NG), SL = attn_slots(NG), bytes = kAttnTile / 8 * 288 * NG;
+  constexpr int kCount = AttnPieces<NG, NP>::count, kHold = kWave / NP;   // loads per tile, tiles per look-up
+  const int c = lane >> 4;
+  const int todo = (te - it + W - 1) / W;
+  const Q4<T> kc;
+  const Q4<TF16> vc;
+  int ids = attn_ids<NP>(a.kv, b, it, W, te, lane);
+  bool whole = __all(ids >= 0);                               // every piece of these tiles has a page
+#pragma unroll
+  for (int i = 0; i < SL - 1; ++i)
+    if (i < todo) attn_copy<NG, NP>(a.kv, h, it + i * W, ids, i, ring + i * bytes, lane);
+  // tile i + SL - 1 is asked for before tile i is worked on, into the slot tile i - 1 has left
+  int slot = 0, next = SL - 1, base = 0;                       // ids hold tiles base .. base + kHold - 1
+  int ids0 = ids, base0 = 0;                                   // the look-up that tile i came from
+  bool whole0 = whole;
+  for (int i = 0; i < todo; ++i) {
+    const int ahead = i + SL - 1;
+    if (ahead < todo) {
+      if (ahead - base == kHold) {
+        base = ahead;
+        ids = attn_ids<NP>(a.kv, b, it + ahead * W, W, te, lane);
+        whole = __all(ids >= 0);
+      }
+      wait_lds();
+      attn_copy<NG, NP>(a.kv, h, it + ahead * W, ids, ahead - base, ring + next * bytes, lane);
+      wait_vm<(SL - 1) * kCount>();
+    } else {
+      wait_vm<0>();
+    }
+    if (i - base0 == kHold) {
+      base0 = base;
+      ids0 = ids;
+      whole0 = whole;
+    }
+    const int pos = (it + i * W) * kAttnTile;
+    const bool full = whole0 && pos >= start && pos + kAttnTile <= end;
+    uint32_t on = 0xFFu;
+    if (!full) {
+      const int id = __shfl(ids0, (i - base0) * NP + c * NP / 4);
+      const int lo = start - pos - 8 * c, hi = end - pos - 8 * c;
+      if (lo > 0) on &= lo >= 8 ? 0u : 0xFFu << lo;
+      if (hi < 8) on &= hi <= 0 ? 0u : (1u << hi) - 1u;
+      if (id < 0) on = 0u;
+    }
+    attn_tile<T, NG>(ring + slot * bytes, qf, kc, vc, a.k2, full, on, lane, st);
+    slot = slot + 1 == SL ? 0 : slot + 1;
+    next = next + 1 == SL ? 0 : next + 1;
+  }
+}
+
 template <class T, int NG>
-__global__ __launch_bounds__(attn_waves(NG) * kWave) void k_attn_q4(AttnArgs a) {
-  constexpr int kAttnWaves = attn_waves(NG);
-  constexpr int D = 32 * NG, kThreads = kAttnWaves * kWave;
-  __shared__ float sh_ref[kAttnWaves][16], sh_sum[kAttnWaves][16];
-  __shared__ __attribute__((aligned(16))) float sh_acc[kAttnWaves * 16 * (D + 4)];
+__global__ __launch_bounds__(attn_waves(NG) * kWave, NG <= 4 ? 4 : 2) void k_attn_q4(AttnArgs a) {
+  constexpr int W = attn_waves(NG), D = 32 * NG, kThreads = W * kWave;
+  constexpr int kRing = W * attn_slots(NG) * (kAttnTile / 8) * 9 * D, kJoin = W * 16 * (D + 4) * 4;
+  static_assert((kRing > kJoin ? kRing : kJoin) >= 16 * kThreads + 16 * 4 * kAttnMaxRuns, "the join's LDS");
+  __shared__ float sh_ref[W][16], sh_sum[W][16];
+  __shared__ __attribute__((aligned(16))) uint8_t sh_mem[kRing > kJoin ? kRing : kJoin];
   __shared__ uint32_t sh_last;
+  float* sh_acc = (float*)sh_mem;
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, c = lane >> 4;
   const int split = blockIdx.x, ht = blockIdx.y % a.HT, h = blockIdx.y / a.HT, b = blockIdx.z;
@@ -229,7 +305,7 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave) void k_attn_q4(AttnArgs a) 
   // this workgroup's tiles of 32 positions: the sequence's tiles in S even runs
   const int t0 = start / kAttnTile, t1 = (end + kAttnTile - 1) / kAttnTile;
   const int ntile = end > start ? t1 - t0 : 0;
-  const int per = max(kAttnWaves, (ntile + a.S - 1) / a.S);
+  const int per = max(W, (ntile + a.S - 1) / a.S);
   const int active = max(1, (ntile + per - 1) / per);          // workgroups with work (one writes an empty row)
   if (split >= active) return;
   const int tb = t0 + split * per, te = min(t0 + ntile, tb + per);
@@ -244,39 +320,14 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave) void k_attn_q4(AttnArgs a) 
   st.sum = 0.f;
 #pragma unroll
   for (int m = 0; m < 2 * NG; ++m) st.acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // two tiles in registers: the next one's loads are under way while one is worked on, the
-  // pages of the one behind it are looked up before
-  int it = tb + wave;
-  if constexpr (!attn_ahead(NG)) {
-    AttnTile<NG> x;
-    for (; it < te; it += kAttnWaves) {
-      attn_load<NG>(a, h, it, attn_pages(a, b, it, n, c), start, end, n, c, x);
-      attn_tile<T, NG>(x, qf, a.k2, lane, st);
-    }
-  } else if (it < te) {
-    AttnTile<NG> x, y;
-    AttnPages id = attn_pages(a, b, it, n, c);
-    AttnPages id1 = attn_pages(a, b, min(it + kAttnWaves, te - 1), n, c);
-    attn_load<NG>(a, h, it, id, start, end, n, c, x);
-    while (true) {
-      int nx = it + kAttnWaves;
-      if (nx < te) attn_load<NG>(a, h, nx, id1, start, end, n, c, y);
-      id = attn_pages(a, b, min(nx + kAttnWaves, te - 1), n, c);
-      __builtin_amdgcn_sched_barrier(0);
-      attn_tile<T, NG>(x, qf, a.k2, lane, st);
-      if (nx >= te) break;
-      it = nx;
-      nx += kAttnWaves;
-      if (nx < te) attn_load<NG>(a, h, nx, id, start, end, n, c, x);
-      id1 = attn_pages(a, b, min(nx + kAttnWaves, te - 1), n, c);
-      __builtin_amdgcn_sched_barrier(0);
-      attn_tile<T, NG>(y, qf, a.k2, lane, st);
-      if (nx >= te) break;
-      it = nx;
-    }
+  uint8_t* ring = sh_mem + wave * (kRing / W);
+  if (tb + wave < te) {
+    if (a.kv.page_shift >= 5) attn_wave<T, NG, 1>(a, b, h, tb + wave, te, start, end, lane, ring, qf, st);
+    else if (a.kv.page_shift == 4) attn_wave<T, NG, 2>(a, b, h, tb + wave, te, start, end, lane, ring, qf, st);
+    else attn_wave<T, NG, 4>(a, b, h, tb + wave, te, start, end, lane, ring, qf, st);
   }
 
+  __syncthreads();                                             // the rings become the join's memory
   // join the waves
   st.sum = quarters_sum(st.sum, lane);
   if (c == 0) {
@@ -294,10 +345,10 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave) void k_attn_q4(AttnArgs a) 
     const int hd = e / (D / 2), d = 2 * (e % (D / 2));
     float r = sh_ref[0][hd];
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) r = fmaxf(r, sh_ref[w][hd]);
+    for (int w = 1; w < W; ++w) r = fmaxf(r, sh_ref[w][hd]);
     float v0 = 0.f, v1 = 0.f, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = exp2f(sh_ref[w][hd] - r);
       const float* p = sh_acc + (w * 16 + hd) * (D + 4) + d;
       v0 = fmaf(f, p[0], v0);
@@ -321,56 +372,70 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave) void k_attn_q4(AttnArgs a) 
   if (threadIdx.x == 0) sh_last = take_ticket(a.tickets + unit) == (uint32_t)(active - 1) ? 1u : 0u;
   __syncthreads();
   if (!sh_last) return;
-  acquire_agent();
   part = a.parts + unit * a.S * run;
-  // `items` threads hold 4 dims of a head each; where there are fewer items than threads
+  // weights of the runs: e^(ref - largest ref) per head, and the joined sums
+  float* sh_w = sh_acc + 4 * kThreads;                         // [heads][active]
+  for (int hd = wave; hd < heads; hd += W) {
+    const float* rs = part + a.HG * D + 2 * hd;
+    float r = kRefMin;
+    for (int k = lane; k < active; k += kWave) {
+      const float2 v = load_through2(rs + k * run);
+      sh_w[hd * active + k] = v.x;
+      r = fmaxf(r, v.x);
+    }
+    r = quarters_max(r, lane);
+    r = fmaxf(r, lane_xor_dpp<8>(r, lane));
+    r = fmaxf(r, lane_xor_dpp<4>(r, lane));
+    r = fmaxf(r, lane_xor_dpp<2>(r, lane));
+    r = fmaxf(r, lane_xor_dpp<1>(r, lane));
+    float l = 0.f;
+    for (int k = lane; k < active; k += kWave) {
+      const float f = exp2f(sh_w[hd * active + k] - r);
+      sh_w[hd * active + k] = f;
+      l = fmaf(f, load_through2(rs + k * run).y, l);
+    }
+    l = wave_sum(l);
+    if (lane == 0) {
+      sh_ref[0][hd] = r;
+      sh_sum[0][hd] = l;
+    }
+  }
+  __syncthreads();
+  // `items` threads hold 2 dims of a head each; where there are fewer items than threads
   // the runs are dealt out over groups of threads and their sums added in group order
-  const int items = heads * (D / 4);
-  const int ngroup = max(1, min(kThreads / items, kAttnWaves));
+  const int items = heads * (D / 2);
+  const int ngroup = max(1, kThreads / items);
   for (int e0 = 0; e0 < items; e0 += kThreads) {
     const int grp = ngroup > 1 ? threadIdx.x / items : 0;
     const int e = ngroup > 1 ? threadIdx.x % items : e0 + threadIdx.x;
     const bool mine = grp < ngroup && e < items;
-    const int hd = mine ? e / (D / 4) : 0, d = 4 * (e % (D / 4));
-    const float* rs = part + a.HG * D + 2 * hd;
-    float r = kRefMin;
-    for (int k = 0; k < active; ++k) r = fmaxf(r, rs[k * run]);
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
+    const int hd = mine ? e / (D / 2) : 0, d = 2 * (e % (D / 2));
+    float v0 = 0.f, v1 = 0.f;
     if (mine) {
+      const float* p = part + hd * D + d;
 #pragma unroll 8
       for (int k = grp; k < active; k += ngroup) {
-        const f32x4 pk = *reinterpret_cast<const f32x4*>(part + k * run + hd * D + d);
-        const float f = exp2f(rs[k * run] - r);
-        l = fmaf(f, rs[k * run + 1], l);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = fmaf(f, pk[i], v[i]);
+        const float2 v = load_through2(p + k * run);
+        const float f = sh_w[hd * active + k];
+        v0 = fmaf(f, v.x, v0);
+        v1 = fmaf(f, v.y, v1);
       }
     }
     if (ngroup > 1) {
+      if (mine) *reinterpret_cast<float2*>(sh_acc + (grp * items + e) * 2) = make_float2(v0, v1);
       __syncthreads();
-      if (mine) {
-        *reinterpret_cast<f32x4*>(sh_acc + (grp * items + e) * 4) = v;
-        if (d == 0) sh_acc[kThreads * 4 + grp * 16 + hd] = l;
-      }
-      __syncthreads();
-      if (grp == 0) {
+      if (grp == 0)
         for (int k = 1; k < ngroup; ++k) {
-          const f32x4 o = *reinterpret_cast<const f32x4*>(sh_acc + (k * items + e) * 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += o[i];
+          v0 += sh_acc[(k * items + e) * 2];
+          v1 += sh_acc[(k * items + e) * 2 + 1];
         }
-        l = 0.f;
-        for (int k = 0; k < ngroup; ++k) l += sh_acc[kThreads * 4 + k * 16 + hd];
-      }
     }
     if (mine && grp == 0) {
+      const float l = sh_sum[0][hd];
       const size_t o = (size_t)b * a.Hq + hq0 + hd;
       const float inv = l != 0.f ? 1.0f / l : 0.f;
-      uint32_t* dst = (uint32_t*)a.out + ((o * D + d) >> 1);
-      dst[0] = (uint32_t)to_16(T{}, v[0] * inv) | ((uint32_t)to_16(T{}, v[1] * inv) << 16);
-      dst[1] = (uint32_t)to_16(T{}, v[2] * inv) | ((uint32_t)to_16(T{}, v[3] * inv) << 16);
-      if (a.lse && d == 0) a.lse[o] = attn_lse(r, l);
+      ((uint32_t*)a.out)[(o * D + d) >> 1] = (uint32_t)to_16(T{}, v0 * inv) | ((uint32_t)to_16(T{}, v1 * inv) << 16);
+      if (a.lse && d == 0) a.lse[o] = attn_lse(sh_ref[0][hd], l);
     }
   }
   if (threadIdx.x == 0) store_through(a.tickets + unit, 0u);

@@ -65,6 +65,7 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) acc[r][t][i] = 0.f;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  const Q4<T> dec;
 
   for (int ck = wave; ck < nchunk; ck += kLinWaves) {
     uint32_t w[R][4];
@@ -91,10 +92,11 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
           xp.w[1] = __builtin_amdgcn_perm(xv.w[2], xv.w[0], 0x07060302u);
           xp.w[2] = __builtin_amdgcn_perm(xv.w[3], xv.w[1], 0x05040100u);
           xp.w[3] = __builtin_amdgcn_perm(xv.w[3], xv.w[1], 0x07060302u);
-          const f32x4 c24 = Mma<T>::run(xp, q4_minus24<T>(), zero);
+          f32x4 c24 = zero;
+          if constexpr (Q4<T>::offset) c24 = Mma<T>::run(xp, Q4<T>::minus24(), zero);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const f32x4 p = Mma<T>::run(xp, q4_word<T>(w[r][j]), c24);
+            const f32x4 p = Mma<T>::run(xp, dec.word(w[r][j]), c24);
 #pragma unroll
             for (int i = 0; i < NI; ++i) acc[r][t][i] = fmaf(sc[r][j], p[i], acc[r][t][i]);
           }

@@ -26,7 +26,7 @@ int device_cu_count() {
   return cus;
 }
 
-// Runs per sequence: one workgroup of eight waves per compute unit, and no run shorter
+// Runs per sequence: two workgroups of eight waves per compute unit, and no run shorter
 // than a tile per wave.
 AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len) {
   AttnPlan p;
@@ -36,8 +36,9 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len) {
   p.HG = p.G < 16 ? p.G : 16;
   const int units = B * Hkv * p.HT;
   const int most = (max_len + 255) / 256;
-  p.S = (256 + units - 1) / units;
+  p.S = (512 + units - 1) / units;
   if (p.S > most) p.S = most;
+  if (p.S > kAttnMaxRuns) p.S = kAttnMaxRuns;
   return p;
 }
 
@@ -82,6 +83,8 @@ int kv_geom(int B, int Hkv, int D, int page, int num_pages, int max_pages, sfx::
   if (B < 1 || Hkv < 1 || Hkv > sfx::kAttnMaxHeads || D < 32 || D > 256 || D % 32 != 0) return SFX_E_SHAPE;
   if (page < 8 || page > 1024 || (page & (page - 1)) != 0 || num_pages < 1 || max_pages < 1) return SFX_E_SHAPE;
   if ((long long)max_pages * page > (1ll << 30)) return SFX_E_SHAPE;
+  // blocks of 8 positions are counted in 31 bits (of 288 bytes and more: beyond any device)
+  if ((long long)num_pages * Hkv * (page / 8) > 0x7FFFFFFFll) return SFX_E_SHAPE;
   *g = sfx::KvGeom{B, Hkv, D, __builtin_ctz((unsigned)page), num_pages, max_pages};
   return SFX_OK;
 }

@@ -1,55 +1,83 @@
 // Int4 codes as matrix-core operands.
 //
-// A 4-bit code q in [-8, 7] is used as the 16-bit number 16 + u, u = q + 8 in 0..15:
-// in fp16 and in bf16 those 16 numbers are one exponent with u in the top mantissa
-// bits, so two codes become a register of two numbers with a shift and an and-or.  The
-// offset 24 = 16 + 8 is taken back inside the matrix cores: the accumulator starts at
-// -24 sum(x) (a product of x with a constant -24 operand), so
-//     sum (16 + u) x - 24 sum x = sum q x
-// with exact products and fp32 sums of one group of 32 at a time; the group's scale
-// multiplies that fp32 sum.  The offset makes the summed terms at most 31 |x| instead of
-// 8 |x|: about 2 bits of the 24 of an fp32 sum of 32 terms.
+// A 4-bit code is held as u = q + 8 in 0..15.  An and-or that puts u into the mantissa of a
+// 16-bit number of known exponent makes it base + u, two codes per register:
+//   fp16  nibbles at bits 0..3 take base 1024, those at bits 4..7 base 64 (no shift; the
+//         upper byte's nibbles after one shift by 8).  A packed addition of -(base + 8),
+//         exact, leaves q: 9 operations per 8 codes.
+//   bf16  has no packed addition.  All four nibble positions are shifted to base 16 and the
+//         24 = 16 + 8 is taken back by the matrix cores: the accumulator starts at
+//         -24 sum(x), a product of x with a constant operand.  sum (16 + u) x - 24 sum x =
+//         sum q x, with exact products and fp32 sums of one group of 32 at a time; the
+//         summed terms are at most 31 |x| instead of 8 |x|, about 2 of an fp32 sum's 24 bits.
+// The scale of a group multiplies its fp32 sum.
+//
+// The masks and bases are kept in registers behind empty asm statements: as literals, two of
+// them do not fit one instruction and the and-or becomes an and and an or.
 #pragma once
 #include "sfx_mfma.hpp"
 
 namespace sfx {
 
+__device__ __forceinline__ uint32_t scalar_const(uint32_t v) {
+  asm("" : "+s"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t vector_const(uint32_t v) {
+  asm("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t pk_add(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) + __builtin_bit_cast(half2_t, b));
+}
+__device__ __forceinline__ uint32_t pk_mul(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) * __builtin_bit_cast(half2_t, b));
+}
+
 template <class T>
 struct Q4;
 template <>
 struct Q4<TF16> {
-  static constexpr uint32_t mask = 0x03C003C0u, one16 = 0x4C004C00u, minus24 = 0xCE00CE00u;
-  static constexpr int up = 6;     // bit where the lowest of the four mantissa bits sits
+  static constexpr bool offset = false;
+  uint32_t m0, m1, o0, o1, d0, d1;
+  __device__ __forceinline__ Q4()
+      : m0(scalar_const(0x000F000Fu)), m1(scalar_const(0x00F000F0u)), o0(vector_const(0x64006400u)),
+        o1(vector_const(0x54005400u)), d0(scalar_const(0xE408E408u)), d1(scalar_const(0xD480D480u)) {}
+  // The codes of nibbles (0, 4) (1, 5) (2, 6) (3, 7) of v.
+  __device__ __forceinline__ Raw<16> word(uint32_t v) const {
+    const uint32_t h = v >> 8;
+    Raw<16> r;
+    r.w[0] = pk_add((v & m0) | o0, d0);
+    r.w[1] = pk_add((v & m1) | o1, d1);
+    r.w[2] = pk_add((h & m0) | o0, d0);
+    r.w[3] = pk_add((h & m1) | o1, d1);
+    return r;
+  }
 };
 template <>
 struct Q4<TBF16> {
-  static constexpr uint32_t mask = 0x00780078u, one16 = 0x41804180u, minus24 = 0xC1C0C1C0u;
-  static constexpr int up = 3;
+  static constexpr bool offset = true;       // word() gives 24 + q
+  uint32_t m, o;
+  __device__ __forceinline__ Q4() : m(scalar_const(0x00780078u)), o(vector_const(0x41804180u)) {}
+  __device__ __forceinline__ Raw<16> word(uint32_t v) const {
+    Raw<16> r;
+    r.w[0] = ((v << 3) & m) | o;
+    r.w[1] = ((v >> 1) & m) | o;
+    r.w[2] = ((v >> 5) & m) | o;
+    r.w[3] = ((v >> 9) & m) | o;
+    return r;
+  }
+  // Written anew at each call: a product of it with something fixed is not kept in
+  // registers across a loop.
+  __device__ __forceinline__ static Raw<16> minus24() {
+    uint32_t k = 0xC1C0C1C0u;
+    asm volatile("" : "+v"(k));
+    Raw<16> r;
+    r.w[0] = r.w[1] = r.w[2] = r.w[3] = k;
+    return r;
+  }
 };
 
-// Nibbles P and P + 4 of v (u codes) as a register of two 16-bit numbers 16 + u.
-template <class T, int P>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t v) {
-  constexpr int sh = Q4<T>::up - 4 * P;
-  if constexpr (sh >= 0) return ((v << sh) & Q4<T>::mask) | Q4<T>::one16;
-  else return ((v >> -sh) & Q4<T>::mask) | Q4<T>::one16;
-}
-// The eight codes of a word: registers (0, 4) (1, 5) (2, 6) (3, 7).
-template <class T>
-__device__ __forceinline__ Raw<16> q4_word(uint32_t v) {
-  Raw<16> r;
-  r.w[0] = q4_pair<T, 0>(v);
-  r.w[1] = q4_pair<T, 1>(v);
-  r.w[2] = q4_pair<T, 2>(v);
-  r.w[3] = q4_pair<T, 3>(v);
-  return r;
-}
-template <class T>
-__device__ __forceinline__ Raw<16> q4_minus24() {
-  Raw<16> r;
-  r.w[0] = r.w[1] = r.w[2] = r.w[3] = Q4<T>::minus24;
-  return r;
-}
 __device__ __forceinline__ float half_at(uint32_t pair, int hi) {
   const half2_t h = __builtin_bit_cast(half2_t, pair);
   return hi ? (float)h.y : (float)h.x;
