@@ -35,8 +35,7 @@ struct AttnArgs {
   const int32_t *starts, *lens;
   uint8_t* out;             // [B][Hq][D] 16 bit
   float* lse;               // [B][Hq] or null
-  uint32_t* tickets;        // [B][Hkv][head tiles]
-  float* parts;             // [B][Hkv][head tiles][S][HG][D + 4]
+  float* parts;             // [B][Hkv][head tiles][S] x ([HG][D] sums, [HG][2] reference and weight sum)
   float k2;                 // scale log2(e)
   int Hq, G, HT, HG, S;     // HG = heads of a full head tile, min(G, 16)
 };
@@ -231,6 +230,22 @@ __device__ __forceinline__ float attn_lse(float ref, float sum) {
   return sum != 0.f ? (ref - 9.f + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
+// A sequence's positions [start, end) as tiles t0 .. t0 + ntile - 1, cut into `active` runs of
+// `per` tiles: S even runs, but none shorter than a tile per wave.
+struct AttnSpan {
+  int start, end, t0, ntile, per, active;
+};
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int b, int W) {
+  AttnSpan s;
+  s.end = min(a.lens[b], a.kv.max_pages << a.kv.page_shift);
+  s.start = a.starts ? max(a.starts[b], 0) : 0;
+  s.t0 = s.start / kAttnTile;
+  s.ntile = s.end > s.start ? (s.end + kAttnTile - 1) / kAttnTile - s.t0 : 0;
+  s.per = max(W, (s.ntile + a.S - 1) / a.S);
+  s.active = max(1, (s.ntile + s.per - 1) / s.per);            // an empty sequence has one: its zero row
+  return s;
+}
+
 // The tiles of one wave: tb + wave, then every W-th.
 template <class T, int NG, int NP>
 __device__ __forceinline__ void attn_wave(const AttnArgs& a, int b, int h, int it, int te, int start, int end, int lane,
@@ -289,26 +304,17 @@ template <class T, int NG>
 __global__ __launch_bounds__(attn_waves(NG) * kWave, NG <= 4 ? 4 : 2) void k_attn_q4(AttnArgs a) {
   constexpr int W = attn_waves(NG), D = 32 * NG, kThreads = W * kWave;
   constexpr int kRing = W * attn_slots(NG) * (kAttnTile / 8) * 9 * D, kJoin = W * 16 * (D + 4) * 4;
-  static_assert((kRing > kJoin ? kRing : kJoin) >= 16 * kThreads + 16 * 4 * kAttnMaxRuns, "the join's LDS");
   __shared__ float sh_ref[W][16], sh_sum[W][16];
   __shared__ __attribute__((aligned(16))) uint8_t sh_mem[kRing > kJoin ? kRing : kJoin];
-  __shared__ uint32_t sh_last;
   float* sh_acc = (float*)sh_mem;
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, c = lane >> 4;
   const int split = blockIdx.x, ht = blockIdx.y % a.HT, h = blockIdx.y / a.HT, b = blockIdx.z;
   const int heads = min(16, a.G - 16 * ht);                    // query heads of this workgroup
-  const int max_len = a.kv.max_pages << a.kv.page_shift;
-  const int end = min(a.lens[b], max_len);
-  const int start = a.starts ? max(a.starts[b], 0) : 0;
-
-  // this workgroup's tiles of 32 positions: the sequence's tiles in S even runs
-  const int t0 = start / kAttnTile, t1 = (end + kAttnTile - 1) / kAttnTile;
-  const int ntile = end > start ? t1 - t0 : 0;
-  const int per = max(W, (ntile + a.S - 1) / a.S);
-  const int active = max(1, (ntile + per - 1) / per);          // workgroups with work (one writes an empty row)
+  const AttnSpan sp = attn_span(a, b, W);
+  const int active = sp.active;
   if (split >= active) return;
-  const int tb = t0 + split * per, te = min(t0 + ntile, tb + per);
+  const int tb = sp.t0 + split * sp.per, te = min(sp.t0 + sp.ntile, tb + sp.per);
 
   const int hq0 = h * a.G + 16 * ht;
   Raw<16> qf[NG];
@@ -322,9 +328,9 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave, NG <= 4 ? 4 : 2) void k_att
   for (int m = 0; m < 2 * NG; ++m) st.acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint8_t* ring = sh_mem + wave * (kRing / W);
   if (tb + wave < te) {
-    if (a.kv.page_shift >= 5) attn_wave<T, NG, 1>(a, b, h, tb + wave, te, start, end, lane, ring, qf, st);
-    else if (a.kv.page_shift == 4) attn_wave<T, NG, 2>(a, b, h, tb + wave, te, start, end, lane, ring, qf, st);
-    else attn_wave<T, NG, 4>(a, b, h, tb + wave, te, start, end, lane, ring, qf, st);
+    if (a.kv.page_shift >= 5) attn_wave<T, NG, 1>(a, b, h, tb + wave, te, sp.start, sp.end, lane, ring, qf, st);
+    else if (a.kv.page_shift == 4) attn_wave<T, NG, 2>(a, b, h, tb + wave, te, sp.start, sp.end, lane, ring, qf, st);
+    else attn_wave<T, NG, 4>(a, b, h, tb + wave, te, sp.start, sp.end, lane, ring, qf, st);
   }
 
   __syncthreads();                                             // the rings become the join's memory
@@ -338,9 +344,8 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave, NG <= 4 ? 4 : 2) void k_att
   for (int m = 0; m < 2 * NG; ++m)
     *reinterpret_cast<f32x4*>(sh_acc + (wave * 16 + n) * (D + 4) + 16 * m + 4 * c) = st.acc[m];
   __syncthreads();
-  const size_t unit = (size_t)b * gridDim.y + blockIdx.y;
-  const size_t run = (size_t)a.HG * (D + 4);                   // one run's part: [HG][D] and [HG] (ref, sum)
-  float* part = a.parts + (unit * a.S + split) * run;
+  const size_t run = (size_t)a.HG * (D + 4);
+  float* part = a.parts + (((size_t)b * gridDim.y + blockIdx.y) * a.S + split) * run;
   for (int e = threadIdx.x; e < heads * (D / 2); e += kThreads) {
     const int hd = e / (D / 2), d = 2 * (e % (D / 2));
     float r = sh_ref[0][hd];
@@ -361,100 +366,89 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave, NG <= 4 ? 4 : 2) void k_att
       ((uint32_t*)a.out)[(o * D + d) >> 1] = (uint32_t)to_16(T{}, v0 * inv) | ((uint32_t)to_16(T{}, v1 * inv) << 16);
       if (a.lse && d == 0) a.lse[o] = attn_lse(r, l);
     } else {
-      store_through2(part + hd * D + d, v0, v1);
-      if (d == 0) store_through2(part + a.HG * D + 2 * hd, r, l);
+      *reinterpret_cast<float2*>(part + hd * D + d) = make_float2(v0, v1);
+      if (d == 0) *reinterpret_cast<float2*>(part + a.HG * D + 2 * hd) = make_float2(r, l);
     }
   }
-  if (active == 1) return;
-  // the last workgroup of the unit joins the runs, in their order
-  wait_memory();
-  __syncthreads();
-  if (threadIdx.x == 0) sh_last = take_ticket(a.tickets + unit) == (uint32_t)(active - 1) ? 1u : 0u;
-  __syncthreads();
-  if (!sh_last) return;
-  part = a.parts + unit * a.S * run;
-  // weights of the runs: e^(ref - largest ref) per head, and the joined sums
-  float* sh_w = sh_acc + 4 * kThreads;                         // [heads][active]
-  for (int hd = wave; hd < heads; hd += W) {
-    const float* rs = part + a.HG * D + 2 * hd;
-    float r = kRefMin;
-    for (int k = lane; k < active; k += kWave) {
-      const float2 v = load_through2(rs + k * run);
-      sh_w[hd * active + k] = v.x;
-      r = fmaxf(r, v.x);
+}
+
+// Joins the runs of a sequence, one workgroup per query head.  Four dims to a thread; the
+// runs are dealt out over groups of D / 4 threads and the groups' sums added in order.
+template <class T, int NG>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  constexpr int W = attn_waves(NG), D = 32 * NG, kItems = D / 4, kGroups = 256 / kItems;
+  __shared__ __attribute__((aligned(16))) float sh_v[kGroups][D];
+  __shared__ float sh_l[kGroups], sh_r[kGroups];
+  const AttnSpan sp = attn_span(a, blockIdx.y, W);
+  if (sp.active == 1) return;                                   // the attention kernel wrote the row
+  const int hq = blockIdx.x, h = hq / a.G, ht = (hq % a.G) / 16, hd = (hq % a.G) % 16, b = blockIdx.y;
+  const size_t run = (size_t)a.HG * (D + 4);
+  const float* part = a.parts + ((size_t)b * (a.kv.Hkv * a.HT) + h * a.HT + ht) * a.S * run;
+  const float* rs = part + a.HG * D + 2 * hd;
+  const int grp = threadIdx.x / kItems, d = 4 * (threadIdx.x % kItems);
+  float r = kRefMin;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  if (grp < kGroups) {
+    // one pass: the group's reference goes up with its runs
+#pragma unroll 4
+    for (int k = grp; k < sp.active; k += kGroups) {
+      const f32x4 pk = *reinterpret_cast<const f32x4*>(part + k * run + hd * D + d);
+      const float2 rl = *reinterpret_cast<const float2*>(rs + k * run);
+      const float next = fmaxf(r, rl.x), f0 = exp2f(r - next), f1 = exp2f(rl.x - next);
+      r = next;
+      l = fmaf(f1, rl.y, l * f0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(f1, pk[i], v[i] * f0);
     }
-    r = quarters_max(r, lane);
-    r = fmaxf(r, lane_xor_dpp<8>(r, lane));
-    r = fmaxf(r, lane_xor_dpp<4>(r, lane));
-    r = fmaxf(r, lane_xor_dpp<2>(r, lane));
-    r = fmaxf(r, lane_xor_dpp<1>(r, lane));
-    float l = 0.f;
-    for (int k = lane; k < active; k += kWave) {
-      const float f = exp2f(sh_w[hd * active + k] - r);
-      sh_w[hd * active + k] = f;
-      l = fmaf(f, load_through2(rs + k * run).y, l);
-    }
-    l = wave_sum(l);
-    if (lane == 0) {
-      sh_ref[0][hd] = r;
-      sh_sum[0][hd] = l;
-    }
-  }
-  __syncthreads();
-  // `items` threads hold 2 dims of a head each; where there are fewer items than threads
-  // the runs are dealt out over groups of threads and their sums added in group order
-  const int items = heads * (D / 2);
-  const int ngroup = max(1, kThreads / items);
-  for (int e0 = 0; e0 < items; e0 += kThreads) {
-    const int grp = ngroup > 1 ? threadIdx.x / items : 0;
-    const int e = ngroup > 1 ? threadIdx.x % items : e0 + threadIdx.x;
-    const bool mine = grp < ngroup && e < items;
-    const int hd = mine ? e / (D / 2) : 0, d = 2 * (e % (D / 2));
-    float v0 = 0.f, v1 = 0.f;
-    if (mine) {
-      const float* p = part + hd * D + d;
-#pragma unroll 8
-      for (int k = grp; k < active; k += ngroup) {
-        const float2 v = load_through2(p + k * run);
-        const float f = sh_w[hd * active + k];
-        v0 = fmaf(f, v.x, v0);
-        v1 = fmaf(f, v.y, v1);
-      }
-    }
-    if (ngroup > 1) {
-      if (mine) *reinterpret_cast<float2*>(sh_acc + (grp * items + e) * 2) = make_float2(v0, v1);
-      __syncthreads();
-      if (grp == 0)
-        for (int k = 1; k < ngroup; ++k) {
-          v0 += sh_acc[(k * items + e) * 2];
-          v1 += sh_acc[(k * items + e) * 2 + 1];
-        }
-    }
-    if (mine && grp == 0) {
-      const float l = sh_sum[0][hd];
-      const size_t o = (size_t)b * a.Hq + hq0 + hd;
-      const float inv = l != 0.f ? 1.0f / l : 0.f;
-      ((uint32_t*)a.out)[(o * D + d) >> 1] = (uint32_t)to_16(T{}, v0 * inv) | ((uint32_t)to_16(T{}, v1 * inv) << 16);
-      if (a.lse && d == 0) a.lse[o] = attn_lse(sh_ref[0][hd], l);
+    *reinterpret_cast<f32x4*>(&sh_v[grp][d]) = v;
+    if (d == 0) {
+      sh_l[grp] = l;
+      sh_r[grp] = r;
     }
   }
-  if (threadIdx.x == 0) store_through(a.tickets + unit, 0u);
+  __syncthreads();
+  if (threadIdx.x < kItems) {
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) r = fmaxf(r, sh_r[k]);
+    l = 0.f;
+    v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const float f = exp2f(sh_r[k] - r);
+      const f32x4 o = *reinterpret_cast<const f32x4*>(&sh_v[k][d]);
+      l = fmaf(f, sh_l[k], l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(f, o[i], v[i]);
+    }
+    const size_t o = (size_t)b * a.Hq + hq;
+    const float inv = l != 0.f ? 1.0f / l : 0.f;
+    uint32_t* dst = (uint32_t*)a.out + ((o * D + d) >> 1);
+    dst[0] = (uint32_t)to_16(T{}, v[0] * inv) | ((uint32_t)to_16(T{}, v[1] * inv) << 16);
+    dst[1] = (uint32_t)to_16(T{}, v[2] * inv) | ((uint32_t)to_16(T{}, v[3] * inv) << 16);
+    if (a.lse && d == 0) a.lse[o] = attn_lse(r, l);
+  }
+}
+
+template <class T, int NG>
+hipError_t attn_run(hipStream_t s, const AttnArgs& a) {
+  k_attn_q4<T, NG><<<dim3(a.S, a.kv.Hkv * a.HT, a.kv.B), dim3(attn_waves(NG) * kWave), 0, s>>>(a);
+  if (a.S > 1) k_attn_join<T, NG><<<dim3(a.Hq, a.kv.B), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
 }
 
 template <class T>
 hipError_t attn_launch(hipStream_t s, const AttnArgs& a) {
-  const dim3 grid(a.S, a.kv.Hkv * a.HT, a.kv.B), blk(attn_waves(a.kv.D >> 5) * kWave);
   switch (a.kv.D >> 5) {
-    case 1: k_attn_q4<T, 1><<<grid, blk, 0, s>>>(a); break;
-    case 2: k_attn_q4<T, 2><<<grid, blk, 0, s>>>(a); break;
-    case 3: k_attn_q4<T, 3><<<grid, blk, 0, s>>>(a); break;
-    case 4: k_attn_q4<T, 4><<<grid, blk, 0, s>>>(a); break;
-    case 5: k_attn_q4<T, 5><<<grid, blk, 0, s>>>(a); break;
-    case 6: k_attn_q4<T, 6><<<grid, blk, 0, s>>>(a); break;
-    case 7: k_attn_q4<T, 7><<<grid, blk, 0, s>>>(a); break;
-    default: k_attn_q4<T, 8><<<grid, blk, 0, s>>>(a); break;
+    case 1: return attn_run<T, 1>(s, a);
+    case 2: return attn_run<T, 2>(s, a);
+    case 3: return attn_run<T, 3>(s, a);
+    case 4: return attn_run<T, 4>(s, a);
+    case 5: return attn_run<T, 5>(s, a);
+    case 6: return attn_run<T, 6>(s, a);
+    case 7: return attn_run<T, 7>(s, a);
+    default: return attn_run<T, 8>(s, a);
   }
-  return hipGetLastError();
 }
 
 }  // namespace

@@ -7,8 +7,8 @@ hipError_t launch_attn_q4_f16(hipStream_t s, const AttnPlan& p, const KvGeom& g,
                             const void* cache, const int32_t* table, const int32_t* starts, const int32_t* lens,
                             float k2, void* out, float* lse, void* ws) {
   const KvCache kv{(uint8_t*)cache, table, g.Hkv, g.D, g.page_shift, g.num_pages, g.max_pages, g.B};
-  const AttnArgs a{kv, (const uint8_t*)q, ldq_bytes, starts, lens, (uint8_t*)out, lse, (uint32_t*)ws,
-                   (float*)((uint8_t*)ws + kAttnTicketBytes), k2, p.Hq, p.G, p.HT, p.HG, p.S};
+  const AttnArgs a{kv, (const uint8_t*)q, ldq_bytes, starts, lens, (uint8_t*)out, lse, (float*)ws, k2,
+                   p.Hq, p.G, p.HT, p.HG, p.S};
   return attn_launch<TF16>(s, a);
 }
 

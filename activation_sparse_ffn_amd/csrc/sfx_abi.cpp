@@ -36,15 +36,17 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len) {
   p.HG = p.G < 16 ? p.G : 16;
   const int units = B * Hkv * p.HT;
   const int most = (max_len + 255) / 256;
-  p.S = (512 + units - 1) / units;
+#ifndef SWG
+#define SWG 512
+#endif
+  p.S = (SWG + units - 1) / units;
   if (p.S > most) p.S = most;
-  if (p.S > kAttnMaxRuns) p.S = kAttnMaxRuns;
   return p;
 }
 
 size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D) {
-  if (p.S <= 1) return kAttnTicketBytes;
-  return kAttnTicketBytes + (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 4) * 4;
+  if (p.S <= 1) return 0;
+  return (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 4) * 4;
 }
 
 }  // namespace sfx

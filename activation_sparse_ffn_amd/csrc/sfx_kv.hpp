@@ -36,12 +36,4 @@ __device__ __forceinline__ size_t kv_block(const KvCache& kv, int id, int h, int
   return ((((size_t)id * kv.Hkv + h) << (kv.page_shift - 3)) + o) * (size_t)kv_block_bytes(kv.D);
 }
 
-// Handed-over data (store_through2) read past the caches: a consumer that reads little does
-// without an agent acquire, which drops the caches of everyone on its XCD.
-__device__ __forceinline__ float2 load_through2(const float* p) {  // p 8-byte aligned
-  const unsigned long long v = __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
-                                                 __HIP_MEMORY_SCOPE_AGENT);
-  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-
 }  // namespace sfx

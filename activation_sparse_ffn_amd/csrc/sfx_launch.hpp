@@ -97,11 +97,7 @@ hipError_t launch_kv_read_q4(hipStream_t s, const KvGeom& g, int odt, int T, con
 struct AttnPlan {
   int Hq, G, HT, HG, S;      // query heads, per kv head, tiles of 16 of those, heads of a full tile, runs
 };
-// Tickets of every (sequence, kv head, head tile) up to SFX_MAX_B x 256 query heads, at the
-// start of the workspace whatever the shape, so shapes that share one never meet there.
 constexpr int kAttnMaxHeads = 256;
-constexpr size_t kAttnTicketBytes = (size_t)SFX_MAX_B * kAttnMaxHeads * 4;
-constexpr int kAttnMaxRuns = 256;      // their weights fit the joining workgroup's LDS
 AttnPlan attn_plan(int B, int Hq, int Hkv, int max_len);
 size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D);
 hipError_t launch_attn_q4_f16(hipStream_t s, const AttnPlan& p, const KvGeom& g, const void* q, size_t ldq_bytes,
