@@ -27,8 +27,6 @@ struct LinearArgs {
   int B, n, d, accumulate;
 };
 
-constexpr int kLinWaves = 8;
-
 // Token that row m of token tile nt stands for.  NI accumulator rows per lane are used:
 // below 16 tokens the tokens are spread over the quarters (row 4 c + i is token NI c + i),
 // so only NI of a lane's four sums are scaled.
@@ -81,104 +79,50 @@ __device__ __forceinline__ float lin_scale(const LinChunk<GSH>& x, int j) {
   else return half_at(x.s[0], 0);
 }
 
-// XLDS: x lies in LDS, ordered, token rows d * 2 + 16 bytes apart (the 16 put eight tokens on
-// different banks).  AHEAD chunks of a wave's weights are on the way at a time.
-template <class T, int NT, int NI, int R, int GSH, bool XLDS, int AHEAD>
-__global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
-  constexpr int TT = 4 * NI * NT, kThreads = kLinWaves * kWave;
-  extern __shared__ __attribute__((aligned(16))) uint8_t sh[];
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m = lane & 15, c = lane >> 4;
-  const int row0 = blockIdx.x * 16 * R;
-  const int ng = a.d >> 5, nsc = ng >> GSH;
-  const int nchunk = (ng + 3) >> 2;
-  // the wave's chunks: a run of its own, so its rows are read in whole lines
-  const int per = (nchunk + kLinWaves - 1) / kLinWaves;
-  const int ck0 = wave * per, ck1 = min(nchunk, ck0 + per);
-  const uint8_t* wrow[R];
-  const uint16_t* srow[R];
+// Sums of a chunk: `groups` of its 32 columns exist (4 but in the last chunk); k: the codes
+// as loaded; xrow: this lane's slice of the chunk's ordered x per token tile, in LDS.
+template <class T, int NT, int NI, int R, int GSH>
+__device__ __forceinline__ void lin_chunk(LinChunk<GSH> (&w)[R], const uint8_t* const (&xrow)[NT], int groups,
+                                          const Q4<T>& dec, float (&acc)[R][NT][NI]) {
+  uint32_t k[R][4];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int row = min(row0 + 16 * r + m, a.n - 1);
-    wrow[r] = a.W + (size_t)row * (a.d >> 1);
-    srow[r] = a.s + (size_t)row * nsc;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[r][j] = w[r].q.w[j] ^ 0x88888888u;
+    quarter_transpose(k[r]);
   }
-  LinChunk<GSH> w[AHEAD][R];
+  // groups that share a scale (1 << GSH of them) are summed in the matrix cores before it
+  constexpr int kPer = 1 << GSH;
 #pragma unroll
-  for (int u = 0; u < AHEAD; ++u)
-    if (ck0 + u < ck1) {
+  for (int j = 0; j < 4; j += kPer) {
+    if (j < groups) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) lin_load<GSH>(wrow[r], srow[r], ck0 + u, c, ng, w[u][r]);
-    }
-  const int xstride = a.d * 2 + 16;
-  const uint8_t* xrow[NT];
-  if constexpr (XLDS) {
-    const int pieces = a.d >> 3;
-    for (int b = 0; b < a.B; ++b)
-      for (int i = threadIdx.x; i < pieces; i += kThreads)
-        *reinterpret_cast<Raw<16>*>(sh + b * xstride + i * 16) = lin_order(load_raw<16>(a.x + (size_t)b * a.ldx + i * 16));
-    __syncthreads();
-  }
+      for (int t = 0; t < NT; ++t) {
+        Raw<16> xp[kPer];
+        f32x4 from = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int tok = min(lin_token<NI>(t, m), a.B - 1);
-    xrow[t] = (XLDS ? sh + tok * xstride : a.x + (size_t)tok * a.ldx) + c * 16;
-  }
-
-  float acc[R][NT][NI];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) acc[r][t][i] = 0.f;
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  const Q4<T> dec;
-
-  for (int ckb = ck0; ckb < ck1; ckb += AHEAD) {
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int ck = ckb + u;
-      if (ck < ck1) {
-        uint32_t k[R][4];
-        float sc[R][4];
+        for (int u = 0; u < kPer; ++u) {
+          xp[u] = load_raw<16>(xrow[t] + (j + u) * 64);
+          if constexpr (Q4<T>::offset) from = Mma<T>::run(xp[u], Q4<T>::minus24(), from);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+          f32x4 p = from;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            k[r][j] = w[u][r].q.w[j] ^ 0x88888888u;
-            sc[r][j] = lin_scale<GSH>(w[u][r], j);
-          }
-          quarter_transpose(k[r]);
-        }
-        if (ck + AHEAD < ck1) {
+          for (int u = 0; u < kPer; ++u) p = Mma<T>::run(xp[u], dec.word(k[r][j + u]), p);
 #pragma unroll
-          for (int r = 0; r < R; ++r) lin_load<GSH>(wrow[r], srow[r], ck + AHEAD, c, ng, w[u][r]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (4 * ck + j < ng) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              Raw<16> xp = load_raw<16>(xrow[t] + (size_t)(4 * ck + j) * 64);
-              if constexpr (!XLDS) xp = lin_order(xp);
-              f32x4 from = zero;
-              if constexpr (Q4<T>::offset) from = Mma<T>::run(xp, Q4<T>::minus24(), zero);
-#pragma unroll
-              for (int r = 0; r < R; ++r) {
-                const f32x4 p = Mma<T>::run(xp, dec.word(k[r][j]), from);
-#pragma unroll
-                for (int i = 0; i < NI; ++i) acc[r][t][i] = fmaf(sc[r][j], p[i], acc[r][t][i]);
-              }
-            }
-          }
+          for (int i = 0; i < NI; ++i) acc[r][t][i] = fmaf(lin_scale<GSH>(w[r], j), p[i], acc[r][t][i]);
         }
       }
     }
   }
-  // the waves' sums in wave order: red[wave][row][token]
-  float* red = (float*)sh;
-  if constexpr (XLDS) __syncthreads();
+}
+
+// The waves' sums in wave order, bias, y.
+template <int NT, int NI, int R, int W>
+__device__ __forceinline__ void lin_finish(const LinearArgs& a, float* red, int row0, int wave, int m, int c,
+                                           const float (&acc)[R][NT][NI]) {
+  constexpr int TT = 4 * NI * NT;
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -186,12 +130,12 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) red[(wave * 16 * R + 16 * r + m) * (TT + 1) + (4 * t + c) * NI + i] = acc[r][t][i];
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * R * TT; e += kThreads) {
+  for (int e = threadIdx.x; e < 16 * R * TT; e += W * kWave) {
     const int row = e % (16 * R), tok = e / (16 * R);
     if (row0 + row < a.n && tok < a.B) {
       float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < kLinWaves; ++k) v += red[(k * 16 * R + row) * (TT + 1) + tok];
+      for (int k = 0; k < W; ++k) v += red[(k * 16 * R + row) * (TT + 1) + tok];
       if (a.bias) v += a.bias[row0 + row];
       float* y = a.y + (size_t)tok * a.ldy + row0 + row;
       *y = a.accumulate ? *y + v : v;
@@ -199,28 +143,179 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
   }
 }
 
-constexpr int kLinXLds = 64 << 10;       // x is kept in LDS up to here: two workgroups per compute unit
+constexpr int kLinWaves = 8;
+constexpr int kLinAhead = 4;             // chunks of a wave's weights on the way at a time
 
-template <class T, int NT, int NI, int R, bool XLDS, int AHEAD>
+// Few tokens: all of x lies in LDS, ordered, token rows 2 d + 16 bytes apart (the 16 put
+// eight tokens on different banks).  16 weight rows per workgroup.
+template <class T, int NI, int GSH>
+__global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
+  constexpr int kThreads = kLinWaves * kWave;
+  extern __shared__ __attribute__((aligned(16))) uint8_t sh[];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, c = lane >> 4;
+  const int row0 = blockIdx.x * 16;
+  const int ng = a.d >> 5, nchunk = (ng + 3) >> 2;
+  // the wave's chunks: a run of its own, so its rows are read in whole lines
+  const int per = (nchunk + kLinWaves - 1) / kLinWaves;
+  const int ck0 = wave * per, ck1 = min(nchunk, ck0 + per);
+  const int row = min(row0 + m, a.n - 1);
+  const uint8_t* wrow = a.W + (size_t)row * (a.d >> 1);
+  const uint16_t* srow = a.s + (size_t)row * (ng >> GSH);
+  LinChunk<GSH> w[kLinAhead][1];
+#pragma unroll
+  for (int u = 0; u < kLinAhead; ++u)
+    if (ck0 + u < ck1) lin_load<GSH>(wrow, srow, ck0 + u, c, ng, w[u][0]);
+  const int xstride = a.d * 2 + 16, pieces = a.d >> 3;
+  constexpr int NB = 4 * NI;                                   // tokens whose loads go out together
+  for (int i = threadIdx.x; i < pieces; i += kThreads) {
+    Raw<16> v[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) v[b] = load_raw<16>(a.x + (size_t)min(b, a.B - 1) * a.ldx + i * 16);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (b < a.B) *reinterpret_cast<Raw<16>*>(sh + b * xstride + i * 16) = lin_order(v[b]);
+  }
+  __syncthreads();
+  const uint8_t* xlane = sh + min(lin_token<NI>(0, m), a.B - 1) * xstride + c * 16;
+
+  float acc[1][1][NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) acc[0][0][i] = 0.f;
+  const Q4<T> dec;
+  for (int ckb = ck0; ckb < ck1; ckb += kLinAhead) {
+#pragma unroll
+    for (int u = 0; u < kLinAhead; ++u) {
+      const int ck = ckb + u;
+      if (ck < ck1) {
+        LinChunk<GSH> now[1] = {w[u][0]};
+        if (ck + kLinAhead < ck1) lin_load<GSH>(wrow, srow, ck + kLinAhead, c, ng, w[u][0]);
+        const uint8_t* xr[1] = {xlane + ck * 256};
+        if (4 * ck + 4 <= ng) lin_chunk<T, 1, NI, 1, GSH>(now, xr, 4, dec, acc);
+        else lin_chunk<T, 1, NI, 1, GSH>(now, xr, ng - 4 * ck, dec, acc);
+      }
+    }
+  }
+  __syncthreads();
+  lin_finish<1, NI, 1, kLinWaves>(a, (float*)sh, row0, wave, m, c, acc);
+}
+
+// More tokens, or long rows: x passes through LDS in blocks of 1024 columns, a chunk of 128
+// for each wave; the next block's x and weights are on the way in registers meanwhile.
+// 16 R weight rows per workgroup.
+template <class T, int NT, int R, int GSH>
+__global__ __launch_bounds__(kLinWaves * kWave, NT * R <= 2 ? 4 : 2) void k_linear_q4_wide(LinearArgs a) {
+  constexpr int kThreads = kLinWaves * kWave, kCols = 128 * kLinWaves, kRow = kCols * 2 + 16;
+  constexpr int kX = 16 * NT * kRow, kRed = kLinWaves * 16 * R * (16 * NT + 1) * 4;
+  constexpr int kPass = 16 * NT * (kCols / 8) / kThreads;       // 16-byte pieces of x per thread and block
+  constexpr int kAhead = NT * R <= 6 ? 4 : 2;                   // blocks of weights on the way (registers)
+  __shared__ __attribute__((aligned(16))) uint8_t sh[kX > kRed ? kX : kRed];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, c = lane >> 4;
+  const int row0 = blockIdx.x * 16 * R;
+  const int ng = a.d >> 5, nblock = (ng + 4 * kLinWaves - 1) / (4 * kLinWaves);
+  const uint8_t* wrow[R];
+  const uint16_t* srow[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = min(row0 + 16 * r + m, a.n - 1);
+    wrow[r] = a.W + (size_t)row * (a.d >> 1);
+    srow[r] = a.s + (size_t)row * (ng >> GSH);
+  }
+  // thread's pieces of x: piece tid % 128 of tokens tid / 128 + 4 i
+  const int piece = threadIdx.x & (kCols / 8 - 1), tok0 = threadIdx.x / (kCols / 8);
+  constexpr int kStep = kThreads / (kCols / 8);
+  Raw<16> xv[kPass];
+  auto load_x = [&](int blk) {
+    const int col = min(blk * kCols + piece * 8, a.d - 8);
+#pragma unroll
+    for (int i = 0; i < kPass; ++i)
+      xv[i] = load_raw<16>(a.x + (size_t)min(tok0 + kStep * i, a.B - 1) * a.ldx + (size_t)col * 2);
+  };
+  LinChunk<GSH> w[kAhead][R];
+  auto load_w = [&](int blk, LinChunk<GSH> (&to)[R]) {
+    const int ck = blk * kLinWaves + wave;
+    if (4 * ck < ng) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) lin_load<GSH>(wrow[r], srow[r], ck, c, ng, to[r]);
+    }
+  };
+  load_x(0);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load_w(u, w[u]);
+  const uint8_t* xrow[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) xrow[t] = sh + min(16 * t + m, a.B - 1) * kRow + wave * 256 + c * 16;
+  float acc[R][NT][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.f;
+  const Q4<T> dec;
+  for (int blk0 = 0; blk0 < nblock; blk0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int blk = blk0 + u;
+      if (blk < nblock) {
+#pragma unroll
+        for (int i = 0; i < kPass; ++i)
+          *reinterpret_cast<Raw<16>*>(sh + (tok0 + kStep * i) * kRow + piece * 16) = lin_order(xv[i]);
+        // x before the weights: loads are waited for in their order, and x is needed first
+        if (blk + 1 < nblock) load_x(blk + 1);
+        LinChunk<GSH> now[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) now[r] = w[u][r];
+        load_w(blk + kAhead, w[u]);
+        __syncthreads();
+        const int groups = ng - 4 * (blk * kLinWaves + wave);
+        if (groups >= 4) lin_chunk<T, NT, 4, R, GSH>(now, xrow, 4, dec, acc);
+        else lin_chunk<T, NT, 4, R, GSH>(now, xrow, groups, dec, acc);
+        __syncthreads();
+      }
+    }
+  }
+  lin_finish<NT, 4, R, kLinWaves>(a, (float*)sh, row0, wave, m, c, acc);
+}
+
+constexpr int kLinXLds = 64 << 10;       // x is kept whole in LDS up to here: two workgroups per compute unit
+
+template <class T, int NI>
 hipError_t lin_run(hipStream_t s, const LinearArgs& a, int gsh) {
+  const dim3 grid((a.n + 15) / 16), blk(kLinWaves * kWave);
+  const size_t red = (size_t)kLinWaves * 16 * (4 * NI + 1) * 4, x = (size_t)a.B * (a.d * 2 + 16);
+  const size_t lds = red > x ? red : x;
+  if (gsh == 0) k_linear_q4<T, NI, 0><<<grid, blk, lds, s>>>(a);
+  else if (gsh == 1) k_linear_q4<T, NI, 1><<<grid, blk, lds, s>>>(a);
+  else k_linear_q4<T, NI, 2><<<grid, blk, lds, s>>>(a);
+  return hipGetLastError();
+}
+template <class T, int NT, int R>
+hipError_t lin_run_wide(hipStream_t s, const LinearArgs& a, int gsh) {
   const dim3 grid((a.n + 16 * R - 1) / (16 * R)), blk(kLinWaves * kWave);
-  const size_t red = (size_t)kLinWaves * 16 * R * (4 * NI * NT + 1) * 4, xl = XLDS ? (size_t)a.B * (a.d * 2 + 16) : 0;
-  const size_t lds = red > xl ? red : xl;
-  if (gsh == 0) k_linear_q4<T, NT, NI, R, 0, XLDS, AHEAD><<<grid, blk, lds, s>>>(a);
-  else if (gsh == 1) k_linear_q4<T, NT, NI, R, 1, XLDS, AHEAD><<<grid, blk, lds, s>>>(a);
-  else k_linear_q4<T, NT, NI, R, 2, XLDS, AHEAD><<<grid, blk, lds, s>>>(a);
+  if (gsh == 0) k_linear_q4_wide<T, NT, R, 0><<<grid, blk, 0, s>>>(a);
+  else if (gsh == 1) k_linear_q4_wide<T, NT, R, 1><<<grid, blk, 0, s>>>(a);
+  else k_linear_q4_wide<T, NT, R, 2><<<grid, blk, 0, s>>>(a);
   return hipGetLastError();
 }
 
+#ifndef LR
+#define LR 8192
+#endif
 template <class T>
 hipError_t lin_launch(hipStream_t s, const LinearArgs& a, int gsh) {
-  const bool x_lds = (size_t)a.B * (a.d * 2 + 16) <= (size_t)kLinXLds;
-  if (a.B <= 4) return x_lds ? lin_run<T, 1, 1, 1, true, 4>(s, a, gsh) : lin_run<T, 1, 1, 1, false, 4>(s, a, gsh);
-  if (a.B <= 8) return x_lds ? lin_run<T, 1, 2, 1, true, 4>(s, a, gsh) : lin_run<T, 1, 2, 1, false, 4>(s, a, gsh);
-  if (a.B <= 16) return x_lds ? lin_run<T, 1, 4, 1, true, 4>(s, a, gsh) : lin_run<T, 1, 4, 1, false, 4>(s, a, gsh);
-  if (a.B <= 32) return lin_run<T, 2, 4, 2, false, 1>(s, a, gsh);
-  if (a.B <= 48) return lin_run<T, 3, 4, 2, false, 1>(s, a, gsh);
-  return lin_run<T, 4, 4, 2, false, 1>(s, a, gsh);
+  if (a.B <= 16 && (size_t)a.B * (a.d * 2 + 16) <= (size_t)kLinXLds) {
+    if (a.B <= 4) return lin_run<T, 1>(s, a, gsh);
+    if (a.B <= 8) return lin_run<T, 2>(s, a, gsh);
+    return lin_run<T, 4>(s, a, gsh);
+  }
+  // two row tiles per wave halve the reads of x; one leaves enough workgroups for few rows
+  const bool two = a.n >= LR;
+  if (a.B <= 16) return two ? lin_run_wide<T, 1, 2>(s, a, gsh) : lin_run_wide<T, 1, 1>(s, a, gsh);
+  if (a.B <= 32) return two ? lin_run_wide<T, 2, 2>(s, a, gsh) : lin_run_wide<T, 2, 1>(s, a, gsh);
+  if (a.B <= 48) return two ? lin_run_wide<T, 3, 2>(s, a, gsh) : lin_run_wide<T, 3, 1>(s, a, gsh);
+  return two ? lin_run_wide<T, 4, 2>(s, a, gsh) : lin_run_wide<T, 4, 1>(s, a, gsh);
 }
 
 }  // namespace
