@@ -8,6 +8,8 @@
 // (the products are exact there) and rounded once to fp32: a quotient next to a rounding
 // border then falls the same way wherever it is computed.  max / 7 and k' / s are
 // correctly rounded fp32 quotients.
+#include <type_traits>
+
 #include "sfx_kv.hpp"
 #include "sfx_launch.hpp"
 #include "sfx_q4.hpp"
@@ -38,98 +40,204 @@ struct AppendArgs {
   int T, Hq, rot, max_pos, pairs;
 };
 
-// Dim d of a head after the rotation (`head`: the head's first element).
+// Eight consecutive elements as they lie; VEC: at 16-byte aligned places.
 template <int DT>
-__device__ __forceinline__ float rotated(const AppendArgs& a, const void* p, size_t head, int d, const float* cs) {
-  const float x = load_elem<DT>(p, head + d);
-  if (cs == nullptr || d >= a.rot) return x;
-  const int half = a.rot >> 1;
-  int i, other;
-  bool first;
-  if (a.pairs) {
-    i = d >> 1;
-    other = d ^ 1;
-    first = (d & 1) == 0;
+struct Eight {
+  Raw<16> r[DT == DT_F32 ? 2 : 1];
+};
+template <int DT, bool VEC>
+__device__ __forceinline__ Eight<DT> load8(const void* p, size_t i) {
+  Eight<DT> e;
+  if constexpr (VEC) {
+    const uint8_t* q = (const uint8_t*)p + i * (DT == DT_F32 ? 4 : 2);
+    e.r[0] = load_raw<16>(q);
+    if constexpr (DT == DT_F32) e.r[1] = load_raw<16>(q + 16);
   } else {
-    first = d < half;
-    i = first ? d : d - half;
-    other = first ? d + half : d - half;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (DT == DT_F32) {
+        e.r[j >> 2].w[j & 3] = ((const uint32_t*)p)[i + j];
+      } else {
+        const uint32_t v = ((const uint16_t*)p)[i + j];
+        e.r[0].w[j >> 1] = (j & 1) ? e.r[0].w[j >> 1] | (v << 16) : v;
+      }
+    }
   }
-  const double o = (double)load_elem<DT>(p, head + other), co = (double)cs[i], si = (double)cs[half + i];
-  const double turn = first ? -(o * si) : o * si;
-  // the fp32 value is what is rounded on to 16 bits or quantised: the copy keeps the
-  // compiler from converting the 64-bit sum to 16 bits directly
-  float y = (float)((double)x * co + turn);
+  return e;
+}
+template <int DT>
+__device__ __forceinline__ void widen(const Eight<DT>& e, float (&x)[8]) {
+  if constexpr (DT == DT_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(e.r[j >> 2].w[j & 3]);
+  } else if constexpr (DT == DT_F16) {
+    unpack<TF16, 4>(e.r[0].w, x);
+  } else {
+    unpack<TBF16, 4>(e.r[0].w, x);
+  }
+}
+
+// x co + turn in 64 bits, where the product and the sum's operands are exact, rounded once.
+// The fp32 value is what is rounded on to 16 bits or quantised: the copy keeps the compiler
+// from converting the 64-bit sum to 16 bits directly.
+__device__ __forceinline__ float turned(float x, float o, float co, float si, bool first) {
+  const double turn = (double)o * (double)si;
+  float y = (float)((double)x * (double)co + (first ? -turn : turn));
   asm volatile("" : "+v"(y));
   return y;
 }
 
-// Scale (fp16 bits) and the codes u = q + 8 of a lane's two values; the 16 lanes of a
-// quarter hold one group of 32.  A group with a NaN or an infinity takes a NaN scale;
-// `top` is the largest scale.
-__device__ __forceinline__ void quant_pair(float a, float b, float top, int lane, uint16_t* s_out, uint32_t* ua,
-                                           uint32_t* ub) {
-  uint32_t m = max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu);
-  m = max(m, lane_xor_u32<8>(m, lane));
-  m = max(m, lane_xor_u32<4>(m, lane));
+// What turns a thread's dims d0 .. d0 + 7 at one position: cosine and sine per dim, whether it
+// is the first of its pair, and where the other one is.
+struct Turn {
+  float co[8], si[8];
+};
+__device__ __forceinline__ int turn_pair(const AppendArgs& a, int d) { return a.pairs ? d >> 1 : d < (a.rot >> 1) ? d : d - (a.rot >> 1); }
+__device__ __forceinline__ bool turn_first(const AppendArgs& a, int d) { return a.pairs ? (d & 1) == 0 : d < (a.rot >> 1); }
+__device__ __forceinline__ int turn_other(const AppendArgs& a, int d) {
+  return a.pairs ? d ^ 1 : d < (a.rot >> 1) ? d + (a.rot >> 1) : d - (a.rot >> 1);
+}
+// VEC: the first `rot` dims and their halves are whole slices of 8.
+template <bool VEC>
+__device__ __forceinline__ void load_turn(const AppendArgs& a, const float* cs, int d0, Turn& t) {
+  const int half = a.rot >> 1;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = min(turn_pair(a, d0 + j), half - 1);         // dims past rot are not turned
+    t.co[j] = cs[i];
+    t.si[j] = cs[half + i];
+  }
+}
+// Where the slice's partners lie, for a whole slice of them in another place.
+__device__ __forceinline__ bool turn_apart(const AppendArgs& a, int d0) { return a.cs && !a.pairs && d0 < a.rot; }
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void turn8(const AppendArgs& a, const void* p, size_t head, int d0, const Eight<DT>& own,
+                                      const Eight<DT>& apart, const Turn& t, float (&y)[8]) {
+  float x[8];
+  widen<DT>(own, x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = x[j];
+  if (!a.cs || d0 >= a.rot) return;
+  if constexpr (VEC) {
+    if (a.pairs) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = turned(x[j], x[j ^ 1], t.co[j], t.si[j], (j & 1) == 0);
+    } else {
+      float o[8];
+      widen<DT>(apart, o);
+      const bool first = d0 < (a.rot >> 1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = turned(x[j], o[j], t.co[j], t.si[j], first);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (d0 + j < a.rot)
+        y[j] = turned(x[j], load_elem<DT>(p, head + turn_other(a, d0 + j)), t.co[j], t.si[j], turn_first(a, d0 + j));
+  }
+}
+
+// Scale (fp16 bits) and the codes u = q + 8, one per nibble of the result in element order;
+// the 4 lanes of a quad hold one group of 32.  A group with a NaN or an infinity takes a NaN
+// scale; `top` is the largest scale.
+__device__ __forceinline__ uint32_t quant8(const float (&x)[8], float top, int lane, uint16_t* s_out) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
   m = max(m, lane_xor_u32<2>(m, lane));
   m = max(m, lane_xor_u32<1>(m, lane));
   if (m >= 0x7F800000u) {
     *s_out = 0x7E00;
-    *ua = *ub = 8u;
-    return;
+    return 0x88888888u;
   }
   const _Float16 s = (_Float16)fminf(__uint_as_float(m) / 7.0f, top);
   const float sf = (float)s;
-  const float qa = sf > 0.f ? fminf(fmaxf(rintf(a / sf), -8.f), 7.f) : 0.f;
-  const float qb = sf > 0.f ? fminf(fmaxf(rintf(b / sf), -8.f), 7.f) : 0.f;
   *s_out = __builtin_bit_cast(uint16_t, s);
-  *ua = (uint32_t)((int)qa + 8);
-  *ub = (uint32_t)((int)qb + 8);
+  if (!(sf > 0.f)) return 0x88888888u;
+  uint32_t u = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) u |= (uint32_t)((int)fminf(fmaxf(rintf(x[j] / sf), -8.f), 7.f) + 8) << (4 * j);
+  return u;
 }
 
 // Largest scales.  The attention takes V values as fp16 (code times scale), which stay
 // finite up to 8 x 8188 = 65504; K scales multiply fp32 sums.
 constexpr float kTopK = 65504.f, kTopV = 8188.f;
 
-// One wave per token and head: first the query heads, then the kv heads.
-template <int DT, int QDT>
-__global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int t = blockIdx.x;
-  const int unit = blockIdx.y * kWavesPerBlock + (threadIdx.x >> 6);
-  const int Hkv = a.kv.Hkv, D = a.kv.D, NG = D >> 5;
-  if (unit >= a.Hq + Hkv) return;
+// A thread takes 8 dims of HP heads of one token, queries or keys and values by the
+// workgroup's column: all its loads go out before the position is looked up.
+template <int DT, int QDT, bool VEC, int HP>
+__global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a, int qcols) {
+  const int D = a.kv.D, NG = D >> 5, slices = D >> 3, heads = kBlock / slices;
+  const int mine = threadIdx.x / slices, slice = threadIdx.x - mine * slices;
+  // workgroups 8 apart are on one XCD: the eight tokens of a block of positions are, so its
+  // bytes meet in one cache
+  const int blk = blockIdx.x, t = ((blk >> 6) * 8 + (blk & 7)) * 8 + ((blk >> 3) & 7);
+  if (t >= a.T || mine >= heads) return;
+  const int lane = threadIdx.x & (kWave - 1), d0 = 8 * slice, c = slice & 3, g = slice >> 2;
+  const bool query = (int)blockIdx.y < qcols;
+  const int unit0 = (query ? blockIdx.y : blockIdx.y - qcols) * heads * HP + mine, units = query ? a.Hq : a.kv.Hkv;
+  if (unit0 >= units) return;
+  const void* src = query ? a.q : a.k;
+  const size_t row = (size_t)t * (query ? a.ldq : a.ldk);
+  const bool apart = VEC && turn_apart(a, d0);
+  Eight<DT> own[HP], oth[HP], val[HP];
+#pragma unroll
+  for (int k = 0; k < HP; ++k) {
+    const size_t head = (size_t)min(unit0 + k * heads, units - 1) * D;
+    own[k] = load8<DT, VEC>(src, row + head + d0);
+    if (apart) oth[k] = load8<DT, VEC>(src, row + head + turn_other(a, d0));
+    if (!query) val[k] = load8<DT, VEC>(a.v, (size_t)t * a.ldv + head + d0);
+  }
   const int pos = a.pos[t], b = a.seq ? a.seq[t] : t;
   if (pos < 0 || (unsigned)b >= (unsigned)a.kv.B || (a.cs && pos >= a.max_pos)) return;
   const int id = kv_page(a.kv, b, pos);
+  Turn turn;
+  if (a.cs && d0 < a.rot) load_turn<VEC>(a, a.cs + (size_t)pos * a.rot, d0, turn);
   if (id < 0) return;
-  const float* cs = a.cs ? a.cs + (size_t)pos * a.rot : nullptr;
-  const int n = lane & 15;
-  if (unit < a.Hq) {
-    const size_t head = (size_t)t * a.ldq + (size_t)unit * D;
-    const size_t out = ((size_t)t * a.Hq + unit) * D;
-    for (int d = lane; d < D; d += kWave) store_elem<QDT>(a.q_out, out + d, rotated<DT>(a, a.q, head, d, cs));
-    return;
-  }
-  const int h = unit - a.Hq, in_page = pos & ((1 << a.kv.page_shift) - 1), i = in_page & 7;
-  uint8_t* blk = a.kv.base + kv_block(a.kv, id, h, in_page >> 3);
-  const size_t khead = (size_t)t * a.ldk + (size_t)h * D, vhead = (size_t)t * a.ldv + (size_t)h * D;
-  for (int g = lane >> 4; g < NG; g += 4) {
+  const int in_page = pos & ((1 << a.kv.page_shift) - 1), i = in_page & 7;
+#pragma unroll
+  for (int k = 0; k < HP; ++k) {
+    const int unit = unit0 + k * heads;
+    if (unit >= units) break;
+    float y[8];
+    turn8<DT, VEC>(a, src, row + (size_t)unit * D, d0, own[k], oth[k], turn, y);
+    if (query) {
+      const size_t out = ((size_t)t * a.Hq + unit) * D + d0;
+      if constexpr (VEC) {
+        using T = std::conditional_t<QDT == DT_F16, TF16, TBF16>;
+        Raw<16> w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w.w[j] = (uint32_t)to_16(T{}, y[2 * j]) | ((uint32_t)to_16(T{}, y[2 * j + 1]) << 16);
+        *(Raw<16>*)((uint16_t*)a.q_out + out) = w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) store_elem<QDT>(a.q_out, out + j, y[j]);
+      }
+      continue;
+    }
+    uint8_t* at = a.kv.base + kv_block(a.kv, id, unit, in_page >> 3);
     uint16_t s;
-    uint32_t ua, ub;
-    const int dk = 32 * g + 2 * n;
-    const float k0 = rotated<DT>(a, a.k, khead, dk, cs), k1 = rotated<DT>(a, a.k, khead, dk + 1, cs);
-    quant_pair(k0, k1, kTopK, lane, &s, &ua, &ub);
-    uint32_t w = (ua << (4 * (n & 3))) | (ub << (16 + 4 * (n & 3)));
-    w |= lane_xor_u32<1>(w, lane);
-    w |= lane_xor_u32<2>(w, lane);
-    if ((n & 3) == 0) *(uint32_t*)(blk + i * (D >> 1) + ((n >> 2) * NG + g) * 4) = w;
-    if (n == 0) *(uint16_t*)(blk + 8 * D + g * 16 + i * 2) = s;
-    const float v0 = load_elem<DT>(a.v, vhead + 32 * g + n), v1 = load_elem<DT>(a.v, vhead + 32 * g + 16 + n);
-    quant_pair(v0, v1, kTopV, lane, &s, &ua, &ub);
-    blk[4 * D + n * 8 * NG + g * 8 + kv_byte(i)] = (uint8_t)(ua | (ub << 4));
-    if (n == 0) *(uint16_t*)(blk + 8 * D + (D >> 1) + g * 16 + i * 2) = s;
+    uint32_t u = quant8(y, kTopK, lane, &s);
+    // dims 2 j and 2 j + 1 to nibbles j and j + 4
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w |= ((u >> (8 * j)) & 15u) << (4 * j) | ((u >> (8 * j + 4)) & 15u) << (16 + 4 * j);
+    *(uint32_t*)(at + i * (D >> 1) + (c * NG + g) * 4) = w;
+    if (c == 0) *(uint16_t*)(at + 8 * D + g * 16 + i * 2) = s;
+    float v[8];
+    widen<DT>(val[k], v);
+    u = quant8(v, kTopV, lane, &s);
+    // dims n and 16 + n share a byte: the quad's lanes c and c + 2 hold them, each writes half
+    const uint32_t other = lane_xor_u32<2>(u, lane);
+    const uint32_t lo = (c & 2) ? other >> 16 : u & 0xFFFFu, hi = (c & 2) ? u >> 16 : other & 0xFFFFu;
+    const int n0 = 8 * (c & 1) + ((c & 2) ? 4 : 0);
+    uint8_t* bv = at + 4 * D + g * 8 + kv_byte(i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      bv[(n0 + j) * 8 * NG] = (uint8_t)(((lo >> (4 * j)) & 15u) | (((hi >> (4 * j)) & 15u) << 4));
+    if (c == 0) *(uint16_t*)(at + 8 * D + (D >> 1) + g * 16 + i * 2) = s;
   }
 }
 
@@ -177,10 +285,24 @@ KvCache make_cache(const KvGeom& g, const void* cache, const int32_t* table) {
   return KvCache{(uint8_t*)cache, table, g.Hkv, g.D, g.page_shift, g.num_pages, g.max_pages, g.B};
 }
 
+template <int DT, int QDT, bool VEC>
+void run_append(hipStream_t s, const AppendArgs& a) {
+  const int heads = kBlock / (a.kv.D >> 3);
+  const auto columns = [&](int hp, int n) { return (n + heads * hp - 1) / (heads * hp); };
+  const int tokens = (a.T + 63) / 64 * 64;
+  // four heads to a thread where that leaves four workgroups per compute unit
+  if ((long long)a.T * (columns(4, a.Hq) + columns(4, a.kv.Hkv)) >= 1024) {
+    const int qc = columns(4, a.Hq);
+    k_kv_append<DT, QDT, VEC, 4><<<dim3(tokens, qc + columns(4, a.kv.Hkv)), dim3(kBlock), 0, s>>>(a, qc);
+  } else {
+    const int qc = columns(1, a.Hq);
+    k_kv_append<DT, QDT, VEC, 1><<<dim3(tokens, qc + columns(1, a.kv.Hkv)), dim3(kBlock), 0, s>>>(a, qc);
+  }
+}
 template <int DT>
-void run_append(hipStream_t s, dim3 grid, const AppendArgs& a, int qdt) {
-  if (qdt == DT_F16) k_kv_append<DT, DT_F16><<<grid, dim3(kBlock), 0, s>>>(a);
-  else k_kv_append<DT, DT_BF16><<<grid, dim3(kBlock), 0, s>>>(a);
+void run_append(hipStream_t s, const AppendArgs& a, int qdt, bool vec) {
+  if (qdt == DT_F16) vec ? run_append<DT, DT_F16, true>(s, a) : run_append<DT, DT_F16, false>(s, a);
+  else vec ? run_append<DT, DT_BF16, true>(s, a) : run_append<DT, DT_BF16, false>(s, a);
 }
 
 }  // namespace
@@ -191,10 +313,12 @@ hipError_t launch_kv_append_q4(hipStream_t s, const KvGeom& g, int xdt, int qdt,
                                const int32_t* table, void* cache, void* q_out) {
   const AppendArgs a{make_cache(g, cache, table), q, k, v, ldq, ldk, ldv, pos, seq, cos_sin, q_out, T, Hq, rot,
                      max_pos, pairs};
-  const dim3 grid(T, (Hq + g.Hkv + kWavesPerBlock - 1) / kWavesPerBlock);
-  if (xdt == DT_F32) run_append<DT_F32>(s, grid, a, qdt);
-  else if (xdt == DT_F16) run_append<DT_F16>(s, grid, a, qdt);
-  else run_append<DT_BF16>(s, grid, a, qdt);
+  const uintptr_t row = xdt == DT_F32 ? 4 : 8;                  // elements of 16 bytes
+  const bool vec = (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 15u) == 0 &&
+                   ((ldq | ldk | ldv) & (row - 1)) == 0 && (!cos_sin || (pairs ? rot % 8 == 0 : rot % 16 == 0));
+  if (xdt == DT_F32) run_append<DT_F32>(s, a, qdt, vec);
+  else if (xdt == DT_F16) run_append<DT_F16>(s, a, qdt, vec);
+  else run_append<DT_BF16>(s, a, qdt, vec);
   return hipGetLastError();
 }
 
