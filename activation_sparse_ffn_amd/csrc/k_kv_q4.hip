@@ -87,6 +87,24 @@ __device__ __forceinline__ float turned(float x, float o, float co, float si, bo
   return y;
 }
 
+template <int DT>
+__device__ __forceinline__ void store8(void* p, size_t i, const float (&x)[8]) {
+  Raw<16> r;
+  if constexpr (DT == DT_F32) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[j] = __float_as_uint(x[4 * k + j]);
+      *(Raw<16>*)((float*)p + i + 4 * k) = r;
+    }
+  } else {
+    using T = std::conditional_t<DT == DT_F16, TF16, TBF16>;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)to_16(T{}, x[2 * j]) | ((uint32_t)to_16(T{}, x[2 * j + 1]) << 16);
+    *(Raw<16>*)((uint16_t*)p + i) = r;
+  }
+}
+
 // What turns a thread's dims d0 .. d0 + 7 at one position: cosine and sine per dim, whether it
 // is the first of its pair, and where the other one is.
 struct Turn {
@@ -206,11 +224,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a, int qcols) {
     if (query) {
       const size_t out = ((size_t)t * a.Hq + unit) * D + d0;
       if constexpr (VEC) {
-        using T = std::conditional_t<QDT == DT_F16, TF16, TBF16>;
-        Raw<16> w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w.w[j] = (uint32_t)to_16(T{}, y[2 * j]) | ((uint32_t)to_16(T{}, y[2 * j + 1]) << 16);
-        *(Raw<16>*)((uint16_t*)a.q_out + out) = w;
+        store8<QDT>(a.q_out, out, y);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) store_elem<QDT>(a.q_out, out + j, y[j]);
@@ -248,36 +262,53 @@ struct ReadArgs {
   int T;
 };
 
-// One wave per token and kv head.
-template <int DT>
+// A thread takes 8 dims of HP heads of one token; tokens on XCDs as in the append.
+template <int DT, int HP>
 __global__ __launch_bounds__(kBlock) void k_kv_read(ReadArgs a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int t = blockIdx.x;
-  const int h = blockIdx.y * kWavesPerBlock + (threadIdx.x >> 6);
-  const int D = a.kv.D, NG = D >> 5;
-  if (h >= a.kv.Hkv) return;
+  const int D = a.kv.D, NG = D >> 5, slices = D >> 3, heads = kBlock / slices;
+  const int mine = threadIdx.x / slices, slice = threadIdx.x - mine * slices;
+  const int blk = blockIdx.x, t = ((blk >> 6) * 8 + (blk & 7)) * 8 + ((blk >> 3) & 7);
+  if (t >= a.T || mine >= heads) return;
+  const int h0 = blockIdx.y * heads * HP + mine;
+  if (h0 >= a.kv.Hkv) return;
+  const int lane = threadIdx.x & (kWave - 1), d0 = 8 * slice, c = slice & 3, g = slice >> 2;
   const int pos = a.pos[t], b = a.seq ? a.seq[t] : t;
   const int id = pos >= 0 && (unsigned)b < (unsigned)a.kv.B ? kv_page(a.kv, b, pos) : -1;
-  const int n = lane & 15;
-  const size_t out = ((size_t)t * a.kv.Hkv + h) * D;
   const int in_page = max(pos, 0) & ((1 << a.kv.page_shift) - 1), i = in_page & 7;
-  const uint8_t* blk = a.kv.base + kv_block(a.kv, max(id, 0), h, in_page >> 3);
-  for (int g = lane >> 4; g < NG; g += 4) {
-    float k0 = 0.f, k1 = 0.f, v0 = 0.f, v1 = 0.f;
-    if (id >= 0) {
-      const uint32_t w = *(const uint32_t*)(blk + i * (D >> 1) + ((n >> 2) * NG + g) * 4) >> (4 * (n & 3));
-      const float ks = half_at(*(const uint16_t*)(blk + 8 * D + g * 16 + i * 2), 0);
-      const float vs = half_at(*(const uint16_t*)(blk + 8 * D + (D >> 1) + g * 16 + i * 2), 0);
-      const uint32_t u = blk[4 * D + n * 8 * NG + g * 8 + kv_byte(i)];
-      k0 = (float)((int)(w & 15u) - 8) * ks;
-      k1 = (float)((int)((w >> 16) & 15u) - 8) * ks;
-      v0 = (float)((int)(u & 15u) - 8) * vs;
-      v1 = (float)((int)(u >> 4) - 8) * vs;
+  uint32_t w[HP], u[HP][4];
+  uint16_t ks[HP], vs[HP];
+#pragma unroll
+  for (int k = 0; k < HP; ++k) {
+    const uint8_t* at = a.kv.base + kv_block(a.kv, max(id, 0), min(h0 + k * heads, a.kv.Hkv - 1), in_page >> 3);
+    w[k] = *(const uint32_t*)(at + i * (D >> 1) + (c * NG + g) * 4);
+    ks[k] = *(const uint16_t*)(at + 8 * D + g * 16 + i * 2);
+    vs[k] = *(const uint16_t*)(at + 8 * D + (D >> 1) + g * 16 + i * 2);
+    // the bytes of dims n and 16 + n, n = 8 (c & 1) + 0..7, serve lanes c and c + 2: each
+    // loads four of them
+    const uint8_t* bv = at + 4 * D + (8 * (c & 1) + 2 * (c & 2)) * 8 * NG + g * 8 + kv_byte(i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[k][j] = bv[j * 8 * NG];
+  }
+#pragma unroll
+  for (int k = 0; k < HP; ++k) {
+    const int h = h0 + k * heads;
+    if (h >= a.kv.Hkv) break;
+    // a padding token's values are zero whatever was read
+    const float ksf = half_at(ks[k], 0), vsf = half_at(vs[k], 0);
+    const uint32_t own = u[k][0] | u[k][1] << 8 | u[k][2] << 16 | u[k][3] << 24, oth = lane_xor_u32<2>(own, lane);
+    const int nib = c & 2 ? 4 : 0;
+    const uint32_t v0 = (c & 2 ? oth : own) >> nib, v1 = (c & 2 ? own : oth) >> nib;
+    float kf[8], vf[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int ku = (int)((w[k] >> (4 * ((j >> 1) + 4 * (j & 1)))) & 15u);
+      const int vu = (int)(((j < 4 ? v0 : v1) >> (8 * (j & 3))) & 15u);
+      kf[j] = id >= 0 ? (float)(ku - 8) * ksf : 0.f;
+      vf[j] = id >= 0 ? (float)(vu - 8) * vsf : 0.f;
     }
-    store_elem<DT>(a.k, out + 32 * g + 2 * n, k0);
-    store_elem<DT>(a.k, out + 32 * g + 2 * n + 1, k1);
-    store_elem<DT>(a.v, out + 32 * g + n, v0);
-    store_elem<DT>(a.v, out + 32 * g + 16 + n, v1);
+    const size_t out = ((size_t)t * a.kv.Hkv + h) * D + d0;
+    store8<DT>(a.k, out, kf);
+    store8<DT>(a.v, out, vf);
   }
 }
 
@@ -305,6 +336,16 @@ void run_append(hipStream_t s, const AppendArgs& a, int qdt, bool vec) {
   else vec ? run_append<DT, DT_BF16, true>(s, a) : run_append<DT, DT_BF16, false>(s, a);
 }
 
+template <int DT>
+void run_read(hipStream_t s, const ReadArgs& a) {
+  const int heads = kBlock / (a.kv.D >> 3), tokens = (a.T + 63) / 64 * 64;
+  const auto columns = [&](int hp) { return (a.kv.Hkv + heads * hp - 1) / (heads * hp); };
+  if (a.kv.Hkv >= 2 * heads && (long long)a.T * columns(2) >= 1024)
+    k_kv_read<DT, 2><<<dim3(tokens, columns(2)), dim3(kBlock), 0, s>>>(a);
+  else
+    k_kv_read<DT, 1><<<dim3(tokens, columns(1)), dim3(kBlock), 0, s>>>(a);
+}
+
 }  // namespace
 
 hipError_t launch_kv_append_q4(hipStream_t s, const KvGeom& g, int xdt, int qdt, int T, int Hq, const void* q, size_t ldq,
@@ -325,10 +366,9 @@ hipError_t launch_kv_append_q4(hipStream_t s, const KvGeom& g, int xdt, int qdt,
 hipError_t launch_kv_read_q4(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
                              const int32_t* table, const void* cache, void* k, void* v) {
   const ReadArgs a{make_cache(g, cache, table), pos, seq, k, v, T};
-  const dim3 grid(T, (g.Hkv + kWavesPerBlock - 1) / kWavesPerBlock);
-  if (odt == DT_F32) k_kv_read<DT_F32><<<grid, dim3(kBlock), 0, s>>>(a);
-  else if (odt == DT_F16) k_kv_read<DT_F16><<<grid, dim3(kBlock), 0, s>>>(a);
-  else k_kv_read<DT_BF16><<<grid, dim3(kBlock), 0, s>>>(a);
+  if (odt == DT_F32) run_read<DT_F32>(s, a);
+  else if (odt == DT_F16) run_read<DT_F16>(s, a);
+  else run_read<DT_BF16>(s, a);
   return hipGetLastError();
 }
 
