@@ -493,26 +493,21 @@ def sfx_ffn_pipeline(wdt: int, act, B: int, d: int, h: int, f: int, descs: torch
 
 # ------------------------------------------------------------------------- int4 attention half
 
-def _same_device(where, *tensors):
-    """The device index the call's tensors share (None entries are skipped)."""
-    dev = None
+_F16, _BF16, _U8, _I32, _FP32 = torch.float16, torch.bfloat16, torch.uint8, torch.int32, torch.float32
+
+
+def _device_error(where, *tensors):
+    """Raise for tensors that are not all on one GPU."""
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
+        if t is not None and not t.is_cuda:
             raise ValueError(f"{where}: tensors must be on the GPU")
-        i = t.get_device()
-        if dev is None:
-            dev = i
-        elif i != dev:
-            raise ValueError(f"{where}: tensors are on different devices")
-    return dev
+    raise ValueError(f"{where}: tensors are on different devices")
 
 
 def _run_on(dev, stream, fn, args, where):
     """Call `fn(stream, *args)` with device `dev` current, on its current stream unless
     `stream` is given."""
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = fn(torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, *args)
     else:
         with torch.cuda.device(dev):
@@ -521,8 +516,8 @@ def _run_on(dev, stream, fn, args, where):
         raise SfxError(st, where)
 
 
-def _dense(t, where, name, dtype=None):
-    if dtype is not None and t.dtype != dtype:
+def _dense(t, where, name, dtype):
+    if t.dtype != dtype:
         raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous")
@@ -531,19 +526,22 @@ def _dense(t, where, name, dtype=None):
 
 def _rows(t, where, name):
     """Row stride of a 2-D tensor whose rows are dense (rows may be apart)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{where}: {name} must be 2-D with dense rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    n, d = t.shape
+    if t.is_contiguous():
+        return d
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{where}: the rows of {name} must be dense")
+    return t.stride(0) if n > 1 else d
 
 
 def _head_rows(t, where, name):
     """Token stride of [tokens][heads][D] with dense heads (tokens may be apart)."""
-    if t.dim() != 3:
-        raise ValueError(f"{where}: {name} must be [tokens][heads][D]")
     T, H, D = t.shape
+    if t.is_contiguous():
+        return H * D
     if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
         raise ValueError(f"{where}: the heads of {name} must be dense")
-    return t.stride(0) if T > 1 else max(t.stride(0), H * D)
+    return t.stride(0) if T > 1 else H * D
 
 
 def sfx_linear_q4(x, W, W_scales, y, bias=None, accumulate=False, stream=None):
@@ -551,24 +549,34 @@ def sfx_linear_q4(x, W, W_scales, y, bias=None, accumulate=False, stream=None):
     [n][d/group] fp16 (group 32, 64 or 128).  x [B][d] fp16 / bf16, y fp32; the rows of
     x and y may be apart (slices of wider tensors)."""
     w = "sfx_linear_q4"
-    ldx, ldy = _rows(x, w, "x"), _rows(y, w, "y")
+    if x.dim() != 2 or W.dim() != 2 or W_scales.dim() != 2 or y.dim() != 2:
+        raise ValueError(f"{w}: x, W, W_scales and y must be 2-D")
     B, d = x.shape
-    n = W.shape[0]
-    if W.dim() != 2 or W.shape[1] * 2 != d or y.shape[0] != B or y.shape[1] != n:
+    n, dw = W.shape
+    ns, groups = W_scales.shape
+    if dw * 2 != d or y.shape != (B, n):
         raise ValueError(f"{w}: shape mismatch")
-    if W_scales.dim() != 2 or W_scales.shape[0] != n or W_scales.shape[1] < 1 or d % W_scales.shape[1] != 0:
+    if ns != n or groups < 1 or d % groups != 0:
         raise ValueError(f"{w}: W_scales must be [n][d / group]")
-    if x.dtype not in (torch.float16, torch.bfloat16):
+    xdt = x.dtype
+    if xdt != _F16 and xdt != _BF16:
         raise TypeError(f"{w}: x must be fp16 or bf16")
-    _need(y, torch.float32, "y")
-    if bias is not None and bias.numel() != n:
-        raise ValueError(f"{w}: bias must hold {n} values")
-    dev = _same_device(w, x, W, W_scales, y, bias)
+    if y.dtype != _FP32:
+        raise TypeError(f"{w}: y is {y.dtype}, expected {_FP32}")
+    dev = x.get_device()
+    if dev < 0 or W.get_device() != dev or W_scales.get_device() != dev or y.get_device() != dev:
+        _device_error(w, x, W, W_scales, y)
+    pb = None
+    if bias is not None:
+        if bias.numel() != n:
+            raise ValueError(f"{w}: bias must hold {n} values")
+        if bias.get_device() != dev:
+            _device_error(w, x, bias)
+        pb = _dense(bias, w, "bias", _FP32)
     _run_on(dev, stream, load().sfx_linear_q4,
-            (WDT[x.dtype], d // W_scales.shape[1], B, n, d, x.data_ptr(), ldx, _dense(W, w, "W", torch.uint8),
-             _dense(W_scales, w, "W_scales", torch.float16),
-             None if bias is None else _dense(bias, w, "bias", torch.float32), 1 if accumulate else 0,
-             y.data_ptr(), ldy), w)
+            (SFX_F16 if xdt == _F16 else SFX_BF16, d // groups, B, n, d, x.data_ptr(), _rows(x, w, "x"),
+             _dense(W, w, "W", _U8), _dense(W_scales, w, "W_scales", _F16), pb, 1 if accumulate else 0, y.data_ptr(),
+             _rows(y, w, "y")), w)
 
 
 def kv_cache_q4(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> torch.Tensor:
@@ -580,17 +588,23 @@ def kv_cache_q4(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> t
 
 def _cache_shape(cache, table, D, Hkv, w):
     """(page, num_pages, max_pages, B) of a cache and its page table."""
-    if cache.dim() != 4 or cache.shape[1] != Hkv or cache.shape[3] != 9 * D:
+    if cache.dim() != 4:
+        raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/8][{9 * D}]")
+    num_pages, hc, octets, nine_d = cache.shape
+    if hc != Hkv or nine_d != 9 * D:
         raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/8][{9 * D}]")
     if table.dim() != 2:
         raise ValueError(f"{w}: table must be [B][max pages]")
-    return cache.shape[2] * 8, cache.shape[0], table.shape[1], table.shape[0]
+    B, max_pages = table.shape
+    return octets * 8, num_pages, max_pages, B
 
 
-def _tokens(t, T, w, name):
+def _tokens(t, T, dev, w, name):
     if t.numel() != T:
         raise ValueError(f"{w}: {name} must hold {T} entries")
-    return _dense(t, w, name, torch.int32)
+    if t.get_device() != dev:
+        _device_error(w, t)
+    return _dense(t, w, name, _I32)
 
 
 def sfx_kv_append_q4(q, k, v, pos, table, cache, q_out, seq=None, cos_sin=None, interleaved=False, stream=None):
@@ -598,53 +612,64 @@ def sfx_kv_append_q4(q, k, v, pos, table, cache, q_out, seq=None, cos_sin=None, 
     k and v as int4 at (seq[t], pos[t]) of the paged cache and write the rotated queries
     to q_out (fp16 / bf16).  q and q_out may be None (keys and values only)."""
     w = "sfx_kv_append_q4"
-    ldk, ldv = _head_rows(k, w, "k"), _head_rows(v, w, "v")
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"{w}: k and v must be [T][Hkv][D]")
     T, Hkv, D = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype:
+    xdt = k.dtype
+    if v.shape != k.shape or v.dtype != xdt:
         raise ValueError(f"{w}: k and v must have one shape and dtype")
-    if k.dtype not in WDT:
-        raise TypeError(f"{w}: unsupported dtype {k.dtype}")
+    if xdt not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {xdt}")
+    dev = k.get_device()
+    if dev < 0 or v.get_device() != dev or table.get_device() != dev or cache.get_device() != dev:
+        _device_error(w, k, v, table, cache)
     Hq, ldq, pq, pqo, qdt = 0, 0, None, None, 0
     if q is not None:
-        ldq = _head_rows(q, w, "q")
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != xdt:
             raise ValueError(f"{w}: q must be [{T}][Hq][{D}] in k's dtype")
+        Hq = q.shape[1]
         if q_out is None or q_out.shape != q.shape:
             raise ValueError(f"{w}: q_out must have q's shape")
-        if q_out.dtype not in (torch.float16, torch.bfloat16):
+        qdt = WDT.get(q_out.dtype, SFX_F32)
+        if qdt == SFX_F32:
             raise TypeError(f"{w}: q_out must be fp16 or bf16")
-        pq, pqo, qdt = q.data_ptr(), _dense(q_out, w, "q_out"), WDT[q_out.dtype]
+        if q.get_device() != dev or q_out.get_device() != dev:
+            _device_error(w, k, q, q_out)
+        pq, ldq, pqo = q.data_ptr(), _head_rows(q, w, "q"), _dense(q_out, w, "q_out", q_out.dtype)
     rot, max_pos, pcs = 0, 0, None
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError(f"{w}: cos_sin must be [positions][rot]")
+        if cos_sin.get_device() != dev:
+            _device_error(w, k, cos_sin)
         max_pos, rot = cos_sin.shape
-        pcs = _dense(cos_sin, w, "cos_sin", torch.float32)
+        pcs = _dense(cos_sin, w, "cos_sin", _FP32)
     page, num_pages, max_pages, B = _cache_shape(cache, table, D, Hkv, w)
-    dev = _same_device(w, k, v, q, q_out, pos, seq, cos_sin, table, cache)
     _run_on(dev, stream, load().sfx_kv_append_q4,
-            (WDT[k.dtype], qdt, T, Hq, Hkv, D, pq, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
-             _tokens(pos, T, w, "pos"), None if seq is None else _tokens(seq, T, w, "seq"), pcs, rot, max_pos,
-             1 if interleaved else 0, B, max_pages, _dense(table, w, "table", torch.int32), page, num_pages,
-             _dense(cache, w, "cache", torch.uint8), pqo), w)
+            (WDT[xdt], qdt, T, Hq, Hkv, D, pq, ldq, k.data_ptr(), _head_rows(k, w, "k"), v.data_ptr(),
+             _head_rows(v, w, "v"), _tokens(pos, T, dev, w, "pos"),
+             None if seq is None else _tokens(seq, T, dev, w, "seq"), pcs, rot, max_pos, 1 if interleaved else 0, B,
+             max_pages, _dense(table, w, "table", _I32), page, num_pages, _dense(cache, w, "cache", _U8), pqo), w)
 
 
 def sfx_kv_read_q4(pos, table, cache, k_out, v_out, seq=None, stream=None):
     """Values held at (seq[t], pos[t]): k_out, v_out [T][Hkv][D] (fp32, fp16 or bf16)."""
     w = "sfx_kv_read_q4"
-    if k_out.dim() != 3 or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+    odt = k_out.dtype
+    if k_out.dim() != 3 or v_out.shape != k_out.shape or v_out.dtype != odt:
         raise ValueError(f"{w}: k_out and v_out must be [T][Hkv][D] of one dtype")
-    if k_out.dtype not in WDT:
-        raise TypeError(f"{w}: unsupported dtype {k_out.dtype}")
+    if odt not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {odt}")
     T, Hkv, D = k_out.shape
+    dev = k_out.get_device()
+    if dev < 0 or v_out.get_device() != dev or table.get_device() != dev or cache.get_device() != dev:
+        _device_error(w, k_out, v_out, table, cache)
     page, num_pages, max_pages, B = _cache_shape(cache, table, D, Hkv, w)
-    dev = _same_device(w, pos, seq, table, cache, k_out, v_out)
     _run_on(dev, stream, load().sfx_kv_read_q4,
-            (WDT[k_out.dtype], T, Hkv, D, _tokens(pos, T, w, "pos"),
-             None if seq is None else _tokens(seq, T, w, "seq"), B, max_pages,
-             _dense(table, w, "table", torch.int32), page, num_pages, _dense(cache, w, "cache", torch.uint8),
-             _dense(k_out, w, "k_out"), _dense(v_out, w, "v_out")), w)
+            (WDT[odt], T, Hkv, D, _tokens(pos, T, dev, w, "pos"),
+             None if seq is None else _tokens(seq, T, dev, w, "seq"), B, max_pages, _dense(table, w, "table", _I32), page,
+             num_pages, _dense(cache, w, "cache", _U8), _dense(k_out, w, "k_out", odt), _dense(v_out, w, "v_out", odt)),
+            w)
 
 
 def sfx_attn_q4_ws(B: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
@@ -657,27 +682,38 @@ def sfx_attn_q4(q, cache, table, lens, out, ws, starts=None, scale=None, lse=Non
     sequences may be apart), out [B][Hq][D] in q's dtype; positions [starts[b], lens[b]);
     scale defaults to D ** -0.5; lse [B][Hq] fp32 optional."""
     w = "sfx_attn_q4"
-    ldq = _head_rows(q, w, "q")
+    if q.dim() != 3 or cache.dim() != 4:
+        raise ValueError(f"{w}: q must be [B][Hq][D], cache [pages][Hkv][page/8][9 D]")
     B, Hq, D = q.shape
-    if q.dtype not in (torch.float16, torch.bfloat16):
+    qdt = q.dtype
+    if qdt != _F16 and qdt != _BF16:
         raise TypeError(f"{w}: q must be fp16 or bf16")
     if out.shape != q.shape:
         raise ValueError(f"{w}: out must have q's shape")
-    if lse is not None and lse.shape != q.shape[:2]:
-        raise ValueError(f"{w}: lse must be [{B}][{Hq}]")
-    if cache.dim() != 4:
-        raise ValueError(f"{w}: cache must be [pages][Hkv][page/8][9 D]")
     Hkv = cache.shape[1]
     page, num_pages, max_pages, Bt = _cache_shape(cache, table, D, Hkv, w)
     if Bt != B:
         raise ValueError(f"{w}: table must have {B} rows")
-    dev = _same_device(w, q, cache, table, lens, out, ws, starts, lse)
+    dev = q.get_device()
+    if dev < 0 or cache.get_device() != dev or table.get_device() != dev or out.get_device() != dev:
+        _device_error(w, q, cache, table, out)
+    pl = pw = None
+    nws = 0
+    if lse is not None:
+        if lse.shape != (B, Hq):
+            raise ValueError(f"{w}: lse must be [{B}][{Hq}]")
+        if lse.get_device() != dev:
+            _device_error(w, q, lse)
+        pl = _dense(lse, w, "lse", _FP32)
+    if ws is not None:
+        if ws.get_device() != dev:
+            _device_error(w, q, ws)
+        pw, nws = _dense(ws, w, "ws", ws.dtype), ws.numel() * ws.element_size()
     _run_on(dev, stream, load().sfx_attn_q4,
-            (WDT[q.dtype], B, Hq, Hkv, D, q.data_ptr(), ldq, max_pages, _dense(table, w, "table", torch.int32), page,
-             num_pages, _dense(cache, w, "cache", torch.uint8), None if starts is None else _tokens(starts, B, w, "starts"),
-             _tokens(lens, B, w, "lens"), D ** -0.5 if scale is None else float(scale), _dense(out, w, "out", q.dtype),
-             None if lse is None else _dense(lse, w, "lse", torch.float32),
-             None if ws is None else _dense(ws, w, "ws"), 0 if ws is None else ws.numel() * ws.element_size()), w)
+            (SFX_F16 if qdt == _F16 else SFX_BF16, B, Hq, Hkv, D, q.data_ptr(), _head_rows(q, w, "q"), max_pages,
+             _dense(table, w, "table", _I32), page, num_pages, _dense(cache, w, "cache", _U8),
+             None if starts is None else _tokens(starts, B, dev, w, "starts"), _tokens(lens, B, dev, w, "lens"),
+             D ** -0.5 if scale is None else float(scale), _dense(out, w, "out", qdt), pl, pw, nws), w)
 
 
 STREAM_READ_OUT_WORDS = 16384
