@@ -116,13 +116,6 @@ __device__ __forceinline__ void attn_copy(const KvCache& kv, int h, int it, int 
   }
 }
 
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(N < 64, "vmcnt holds 6 bits");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
 // Running state of a wave: per lane the head n, of products m the dims 16 m + 4 c + i.
 template <int NG>
 struct AttnState {

@@ -144,37 +144,94 @@ __device__ __forceinline__ void lin_finish(const LinearArgs& a, float* red, int 
 }
 
 constexpr int kLinWaves = 8;
-constexpr int kLinAhead = 4;             // chunks of a wave's weights on the way at a time
 
-// Few tokens: all of x lies in LDS, ordered, token rows 2 d + 16 bytes apart (the 16 put
-// eight tokens on different banks).  16 weight rows per workgroup.
+// ---- few tokens.  A unit is 256 columns of 16 weight rows: 128 bytes of codes per row, so rows
+// are read in whole lines (with 64 bytes per row and load, the loads alone of 28672 x 7168
+// codes took 25 us instead of 21).  It is copied into LDS by the wave that uses it: row r's
+// eight 16-byte pieces (a group each) lie rotated by r / 2, so the 64 lanes of a read hit 64
+// banks.
+constexpr int kLinUnit = 16 * 128;       // bytes
+// Units of a wave in LDS or on the way.  Two, not more: 32 KB leave room for three or four
+// workgroups per compute unit, which hide more than longer queues in two (four units: 8192 x
+// 8192 at one token 16.7 us against 12.2, 16384 x 4096 at four 20.5 against 13.9).
+constexpr int kLinSlots = 2;
+
+// A row's scales of one unit, as they lie: 8 >> GSH of them.
+template <int GSH>
+struct LinScales {
+  uint32_t w[GSH == 0 ? 4 : GSH == 1 ? 2 : 1];
+};
+template <int GSH>
+__device__ __forceinline__ LinScales<GSH> lin_scales(const uint16_t* srow, int unit, int ng) {
+  constexpr int N = 8 >> GSH;
+  LinScales<GSH> s;
+  const int s0 = unit * N, last = ((ng - 1) >> GSH);
+  if (s0 + N - 1 <= last) {
+    struct __attribute__((packed, aligned(2))) Words {
+      uint32_t w[N / 2];
+    };
+    const Words v = *reinterpret_cast<const Words*>(srow + s0);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) s.w[i] = v.w[i];
+  } else {                               // the row ends in this unit
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      s.w[i] = srow[min(s0 + 2 * i, last)] | (uint32_t)srow[min(s0 + 2 * i + 1, last)] << 16;
+  }
+  return s;
+}
+
+// All of x lies in LDS, ordered, token rows 2 d + 16 bytes apart (the 16 put eight tokens on
+// different banks).  16 weight rows per workgroup; unit u is wave u % 8's.
 template <class T, int NI, int GSH>
 __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
-  constexpr int kThreads = kLinWaves * kWave;
+  constexpr int kThreads = kLinWaves * kWave, kPer = 1 << GSH;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kLinWaves][kLinSlots][kLinUnit];
   extern __shared__ __attribute__((aligned(16))) uint8_t sh[];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, c = lane >> 4;
   const int row0 = blockIdx.x * 16;
-  const int ng = a.d >> 5, nchunk = (ng + 3) >> 2;
-  // the wave's chunks: a run of its own, so its rows are read in whole lines
-  const int per = (nchunk + kLinWaves - 1) / kLinWaves;
-  const int ck0 = wave * per, ck1 = min(nchunk, ck0 + per);
-  const int row = min(row0 + m, a.n - 1);
-  const uint8_t* wrow = a.W + (size_t)row * (a.d >> 1);
-  const uint16_t* srow = a.s + (size_t)row * (ng >> GSH);
-  LinChunk<GSH> w[kLinAhead][1];
-#pragma unroll
-  for (int u = 0; u < kLinAhead; ++u)
-    if (ck0 + u < ck1) lin_load<GSH>(wrow, srow, ck0 + u, c, ng, w[u][0]);
+  const int ng = a.d >> 5, nunit = (ng + 7) >> 3;
+  // x first: the wait for it then leaves the weights on their way
   const int xstride = a.d * 2 + 16, pieces = a.d >> 3;
   constexpr int NB = 4 * NI;                                   // tokens whose loads go out together
-  for (int i = threadIdx.x; i < pieces; i += kThreads) {
-    Raw<16> v[NB];
+  Raw<16> xv[NB];
+  const int p0 = min((int)threadIdx.x, pieces - 1);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) v[b] = load_raw<16>(a.x + (size_t)min(b, a.B - 1) * a.ldx + i * 16);
+  for (int b = 0; b < NB; ++b) xv[b] = load_raw<16>(a.x + (size_t)min(b, a.B - 1) * a.ldx + (size_t)p0 * 16);
+  // copy: lane l brings the piece of row 8 i + l / 8 that its slot of LDS holds
+  const uint8_t* from[2];
+  int piece[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    from[i] = a.W + (size_t)min(row0 + r, a.n - 1) * (a.d >> 1);
+    piece[i] = ((lane & 7) - (r >> 1)) & 7;
+  }
+  const uint16_t* srow = a.s + (size_t)min(row0 + m, a.n - 1) * (ng >> GSH);
+  const int todo = nunit > wave ? (nunit - wave + kLinWaves - 1) / kLinWaves : 0;
+  LinScales<GSH> sc[kLinSlots];
+  auto fetch = [&](int i, int slot, LinScales<GSH>& s) {
+    const int unit = wave + i * kLinWaves;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      __builtin_amdgcn_global_load_lds((const void*)(from[k] + (size_t)min(8 * unit + piece[k], ng - 1) * 16),
+                                       (__attribute__((address_space(3))) void*)(ring[wave][slot] + k * 1024), 16, 0, 0);
+    s = lin_scales<GSH>(srow, unit, ng);
+  };
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < kLinSlots; ++i)
+    if (i < todo) fetch(i, i, sc[i]);
+  __builtin_amdgcn_sched_barrier(0);
+  for (int i = threadIdx.x; i < pieces; i += kThreads) {
+    if (i >= kThreads) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) xv[b] = load_raw<16>(a.x + (size_t)min(b, a.B - 1) * a.ldx + (size_t)i * 16);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (b < a.B) *reinterpret_cast<Raw<16>*>(sh + b * xstride + i * 16) = lin_order(v[b]);
+      if (b < a.B) *reinterpret_cast<Raw<16>*>(sh + b * xstride + i * 16) = lin_order(xv[b]);
   }
   __syncthreads();
   const uint8_t* xlane = sh + min(lin_token<NI>(0, m), a.B - 1) * xstride + c * 16;
@@ -183,21 +240,44 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
 #pragma unroll
   for (int i = 0; i < NI; ++i) acc[0][0][i] = 0.f;
   const Q4<T> dec;
-  for (int ckb = ck0; ckb < ck1; ckb += kLinAhead) {
+  for (int i0 = 0; i0 < todo; i0 += kLinSlots) {
 #pragma unroll
-    for (int u = 0; u < kLinAhead; ++u) {
-      const int ck = ckb + u;
-      if (ck < ck1) {
-        LinChunk<GSH> now[1] = {w[u][0]};
-        if (ck + kLinAhead < ck1) lin_load<GSH>(wrow, srow, ck + kLinAhead, c, ng, w[u][0]);
-        const uint8_t* xr[1] = {xlane + ck * 256};
-        if (4 * ck + 4 <= ng) lin_chunk<T, 1, NI, 1, GSH>(now, xr, 4, dec, acc);
-        else lin_chunk<T, 1, NI, 1, GSH>(now, xr, ng - 4 * ck, dec, acc);
+    for (int s = 0; s < kLinSlots; ++s) {
+      const int i = i0 + s;
+      if (i < todo) {
+        // a unit is two copies and at least one load; the younger ones may still be on the way
+        const int younger = min(todo - 1 - i, kLinSlots - 1);
+        static_assert(kLinSlots == 2, "the waits count one younger unit");
+        if (younger > 0) wait_vm<3>();
+        else wait_vm<0>();
+        const int unit = wave + i * kLinWaves, groups = ng - 8 * unit;
+        const uint8_t* w = ring[wave][s] + m * 128 + c * 4;
+        const uint8_t* xr = xlane + unit * 512;
+#pragma unroll
+        for (int j = 0; j < 8; j += kPer) {
+          if (j < groups) {
+            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+              const Raw<16> xp = load_raw<16>(xr + (j + u) * 64);
+              const uint32_t k = *reinterpret_cast<const uint32_t*>(w + ((j + u + (m >> 1)) & 7) * 16) ^ 0x88888888u;
+              if constexpr (Q4<T>::offset) p = Mma<T>::run(xp, Q4<T>::minus24(), p);
+              p = Mma<T>::run(xp, dec.word(k), p);
+            }
+            const float f = half_at(sc[s].w[(j >> GSH) >> 1], (j >> GSH) & 1);
+#pragma unroll
+            for (int t = 0; t < NI; ++t) acc[0][0][t] = fmaf(f, p[t], acc[0][0][t]);
+          }
+        }
+        if (i + kLinSlots < todo) {
+          wait_lds();
+          fetch(i + kLinSlots, s, sc[s]);
+        }
       }
     }
   }
   __syncthreads();
-  lin_finish<1, NI, 1, kLinWaves>(a, (float*)sh, row0, wave, m, c, acc);
+  lin_finish<1, NI, 1, kLinWaves>(a, (float*)&ring[0][0][0], row0, wave, m, c, acc);
 }
 
 // More tokens, or long rows: x passes through LDS in blocks of 1024 columns, a chunk of 128
@@ -284,8 +364,7 @@ constexpr int kLinXLds = 64 << 10;       // x is kept whole in LDS up to here: t
 template <class T, int NI>
 hipError_t lin_run(hipStream_t s, const LinearArgs& a, int gsh) {
   const dim3 grid((a.n + 15) / 16), blk(kLinWaves * kWave);
-  const size_t red = (size_t)kLinWaves * 16 * (4 * NI + 1) * 4, x = (size_t)a.B * (a.d * 2 + 16);
-  const size_t lds = red > x ? red : x;
+  const size_t lds = (size_t)a.B * (a.d * 2 + 16);
   if (gsh == 0) k_linear_q4<T, NI, 0><<<grid, blk, lds, s>>>(a);
   else if (gsh == 1) k_linear_q4<T, NI, 1><<<grid, blk, lds, s>>>(a);
   else k_linear_q4<T, NI, 2><<<grid, blk, lds, s>>>(a);

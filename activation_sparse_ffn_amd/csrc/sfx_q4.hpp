@@ -96,6 +96,15 @@ __device__ __forceinline__ void quarter_transpose(uint32_t (&w)[4]) {
   w[3] = d[1];
 }
 
+// Waits of a wave for its own copies into LDS (all but the N youngest memory operations) and
+// for its own LDS reads; the compiler moves no memory access across them.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N < 64, "vmcnt holds 6 bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 __device__ __forceinline__ uint16_t to_16(TF16, float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 __device__ __forceinline__ uint16_t to_16(TBF16, float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
