@@ -7,9 +7,10 @@
 //   scores   two 16x16x32 products per group of 32 dims, 16 positions (rows) x 16 query
 //            heads (columns) each, on the codes (sfx_q4.hpp); the key's fp32 scale multiplies
 //            each group's fp32 sum;
-//   weights  P = 2^(s - ref + 9) in fp32, rounded to fp16 as the second product's operand (the
-//            sum of weights keeps the fp32 values); the lane that holds a score holds it in
-//            the place where the product wants the weight, so nothing crosses lanes;
+//   weights  P = 2^(s - ref + 9) in fp32, as one fp16 operand of the second product (bf16
+//            results) or two (fp16 results); the sum of weights keeps the fp32 values.  The
+//            lane that holds a score holds it in the place where the product wants the
+//            weight, so nothing crosses lanes;
 //   output   codes times scale, rounded once to fp16, as rows of 16 dims x 32 positions.
 // The reference is raised only when a score passes it by 6 (in powers of two), so P stays
 // below 2^15; the 2^9 keeps weights down to 2^-33 of the largest above fp16's last bit.
@@ -196,12 +197,17 @@ __device__ __forceinline__ void attn_tile(const uint8_t* tile, const Raw<16> (&q
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = e[i] == -INFINITY ? e[i] : fmaf(s[i], k2, 9.f - next);
   }
-  Raw<16> p;
+  // fp16 queries get results of 11 bits: their weights' rounding errors are kept as a second
+  // fp16 term (products the matrix cores have time for), else they would add half of the
+  // result's own rounding to it; bf16 results have 8 bits
+  constexpr bool kTwo = !Q4<T>::offset;
+  Raw<16> p, p2;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float e0 = __builtin_amdgcn_exp2f(e[2 * i]), e1 = __builtin_amdgcn_exp2f(e[2 * i + 1]);
     st.sum += e0 + e1;
     p.w[i] = pack_f16(e0, e1);
+    if constexpr (kTwo) p2.w[i] = pack_f16(e0 - half_at(p.w[i], 0), e1 - half_at(p.w[i], 1));
   }
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
@@ -216,6 +222,10 @@ __device__ __forceinline__ void attn_tile(const uint8_t* tile, const Raw<16> (&q
     }
     st.acc[2 * g] = Mma<TF16>::run(lo, p, st.acc[2 * g]);
     st.acc[2 * g + 1] = Mma<TF16>::run(hi, p, st.acc[2 * g + 1]);
+    if constexpr (kTwo) {
+      st.acc[2 * g] = Mma<TF16>::run(lo, p2, st.acc[2 * g]);
+      st.acc[2 * g + 1] = Mma<TF16>::run(hi, p2, st.acc[2 * g + 1]);
+    }
   }
 }
 
