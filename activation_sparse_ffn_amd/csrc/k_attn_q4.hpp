@@ -260,21 +260,18 @@ __device__ __forceinline__ void attn_wave(const AttnArgs& a, int b, int h, int i
   const Q4<T> kc;
   const Q4<TF16> vc;
   int ids = attn_ids<NP>(a.kv, b, it, W, te, lane);
-  bool whole = __all(ids >= 0);                               // every piece of these tiles has a page
 #pragma unroll
   for (int i = 0; i < SL - 1; ++i)
     if (i < todo) attn_copy<NG, NP>(a.kv, h, it + i * W, ids, i, ring + i * bytes, lane);
   // tile i + SL - 1 is asked for before tile i is worked on, into the slot tile i - 1 has left
   int slot = 0, next = SL - 1, base = 0;                       // ids hold tiles base .. base + kHold - 1
   int ids0 = ids, base0 = 0;                                   // the look-up that tile i came from
-  bool whole0 = whole;
   for (int i = 0; i < todo; ++i) {
     const int ahead = i + SL - 1;
     if (ahead < todo) {
       if (ahead - base == kHold) {
         base = ahead;
         ids = attn_ids<NP>(a.kv, b, it + ahead * W, W, te, lane);
-        whole = __all(ids >= 0);
       }
       wait_lds();
       attn_copy<NG, NP>(a.kv, h, it + ahead * W, ids, ahead - base, ring + next * bytes, lane);
@@ -285,10 +282,11 @@ __device__ __forceinline__ void attn_wave(const AttnArgs& a, int b, int h, int i
     if (i - base0 == kHold) {
       base0 = base;
       ids0 = ids;
-      whole0 = whole;
     }
     const int pos = (it + i * W) * kAttnTile;
-    const bool full = whole0 && pos >= start && pos + kAttnTile <= end;
+    bool full = pos >= start && pos + kAttnTile <= end;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) full = full && __builtin_amdgcn_readlane(ids0, (i - base0) * NP + p) >= 0;
     uint32_t on = 0xFFu;
     if (!full) {
       const int id = __shfl(ids0, (i - base0) * NP + c * NP / 4);

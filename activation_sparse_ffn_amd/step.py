@@ -1,9 +1,13 @@
 """Buffers and call order of one layer-step (predict -> compact -> up -> down) and of
 the per-step TAM update, on top of the libsfx binding.  Orchestration only: every
 number is produced by the library's kernels."""
+import contextlib
+
 import torch
 
 from . import _abi as A
+
+_NO_STREAM = contextlib.nullcontext()
 
 TORCH_WDT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 WDT_CODE = {"f32": A.SFX_F32, "f16": A.SFX_F16, "bf16": A.SFX_BF16, "q4": A.SFX_Q4G32}
@@ -50,9 +54,11 @@ class StepBuffers:
 
 
 def run_layer(buf: StepBuffers, layer, x: torch.Tensor, threshold: float, act: str,
-              tok_bits: bool = True, stream=None):
+              tok_bits: bool = True, stream=None, attn: "AttnStep" = None):
     """predict -> compact -> up -> down for one layer.  `layer` holds the device
-    tensors W1, W2, Wa, ba, Wd (Wl, Wa_s, Wl_s, Wd_s when present)."""
+    tensors W1, W2, Wa, ba, Wd (Wl, Wa_s, Wl_s, Wd_s when present).  With `attn` the
+    layer is a parallel block: its attention half (weights Wqkv, Wqkv_s, Wo, Wo_s, biases
+    bqkv, bo when present) reads the same x and is added to buf.y."""
     g = layer.get if isinstance(layer, dict) else (lambda k: getattr(layer, k, None))
     if g("W1_s") is not None:
         A.sfx_predict_q4(x, g("W1"), g("W1_s"), g("W2"), g("W2_s"), buf.scores, buf.ws_pred, stream=stream)
@@ -64,6 +70,62 @@ def run_layer(buf: StepBuffers, layer, x: torch.Tensor, threshold: float, act: s
                     Wl=g("Wl"), Wl_scales=g("Wl_s"), stream=stream)
     A.sfx_sparse_down(g("Wd"), buf.idx, buf.count, buf.hact, buf.y, buf.ws_down, Wd_scales=g("Wd_s"),
                       stream=stream)
+    if attn is not None:
+        attn.run(layer, x, buf.y, accumulate=True, stream=stream)
+
+
+class AttnStep:
+    """The attention half of one layer's decode step in int4: projection to queries, keys
+    and values, append to the layer's paged cache, attention over it, output projection.
+
+    `table` [B][max pages] int32 (layers of a model may share it) and `pos` [B] int32, the
+    position of each sequence's token (-1: no token; its output is the bias of the output
+    projection), are the caller's and may change between steps, also of a captured graph;
+    the attention covers positions max(0, pos + 1 - window) .. pos (window 0: all).  Every
+    pos >= 0 must have a page in `table` and a row in `cos_sin`: a token that is not stored
+    gets no queries of its own either."""
+
+    def __init__(self, Hq: int, Hkv: int, D: int, B: int, dtype: str, table: torch.Tensor, pos: torch.Tensor,
+                 num_pages: int, page: int = 16, cos_sin: torch.Tensor = None, interleaved: bool = False,
+                 scale: float = None, window: int = 0, device="cuda"):
+        self.Hq, self.Hkv, self.D, self.B, self.window = Hq, Hkv, D, B, window
+        self.table, self.pos, self.cos_sin, self.interleaved, self.scale = table, pos, cos_sin, interleaved, scale
+        dev = torch.device(device)
+        dt = TORCH_WDT[dtype]
+        self.cache = A.kv_cache_q4(num_pages, Hkv, page, D, dev)
+        self.qkv = torch.empty(B, (Hq + 2 * Hkv) * D, dtype=torch.float32, device=dev)
+        self.q = torch.zeros(B, Hq, D, dtype=dt, device=dev)
+        self.o = torch.zeros(B, Hq, D, dtype=dt, device=dev)
+        self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.starts = torch.zeros(B, dtype=torch.int32, device=dev) if window else None
+        self.ws = A.workspace(A.sfx_attn_q4_ws(B, Hq, Hkv, D, table.shape[1] * page), dev)
+
+    def _cut(self, t: torch.Tensor):
+        """q, k and v of the projection's rows [T][(Hq + 2 Hkv) D]."""
+        a, b = self.Hq * self.D, self.Hkv * self.D
+        return (t[:, :a].unflatten(1, (self.Hq, self.D)), t[:, a:a + b].unflatten(1, (self.Hkv, self.D)),
+                t[:, a + b:].unflatten(1, (self.Hkv, self.D)))
+
+    def prefill(self, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, seq: torch.Tensor, stream=None):
+        """Store a prompt's keys and values [T][Hkv][D] (not yet rotated) at (seq, pos)."""
+        A.sfx_kv_append_q4(None, k, v, pos, self.table, self.cache, None, seq=seq, cos_sin=self.cos_sin,
+                           interleaved=self.interleaved, stream=stream)
+
+    def run(self, layer, x: torch.Tensor, y: torch.Tensor, accumulate: bool = False, stream=None):
+        """y [B][d] (+)= the attention half of `layer` on x [B][d] at the positions `pos`."""
+        g = layer.get if isinstance(layer, dict) else (lambda k: getattr(layer, k, None))
+        with torch.cuda.stream(stream) if stream is not None else _NO_STREAM:
+            torch.add(self.pos, 1, out=self.lens)
+            if self.starts is not None:
+                torch.sub(self.lens, self.window, out=self.starts)
+        A.sfx_linear_q4(x, g("Wqkv"), g("Wqkv_s"), self.qkv, bias=g("bqkv"), stream=stream)
+        q, k, v = self._cut(self.qkv)
+        A.sfx_kv_append_q4(q, k, v, self.pos, self.table, self.cache, self.q, cos_sin=self.cos_sin,
+                           interleaved=self.interleaved, stream=stream)
+        A.sfx_attn_q4(self.q, self.cache, self.table, self.lens, self.o, self.ws, starts=self.starts, scale=self.scale,
+                      stream=stream)
+        A.sfx_linear_q4(self.o.view(self.B, -1), g("Wo"), g("Wo_s"), y, bias=g("bo"), accumulate=accumulate,
+                        stream=stream)
 
 
 class TamState:

@@ -39,7 +39,8 @@ def make_linear(B, n, d, group, dt, seed):
     return x, W, s, bias
 
 
-LINEAR = [(1, 1, 32, 32), (1, 17, 64, 64), (2, 15, 96, 32), (1, 33, 128, 128), (3, 100, 160, 32), (4, 1003, 1056, 32),
+LINEAR = [(3, 40, 8192, 64), (2, 20, 40960, 128), (16, 33, 2016, 32), (13, 8200, 1056, 32), (40, 8193, 288, 32),
+          (64, 8192, 160, 32), (1, 1, 32, 32), (1, 17, 64, 64), (2, 15, 96, 32), (1, 33, 128, 128), (3, 100, 160, 32), (4, 1003, 1056, 32),
           (5, 48, 192, 64), (8, 130, 4096, 128), (9, 64, 1024, 32), (16, 257, 640, 128), (17, 31, 2048, 64),
           (32, 96, 352, 32), (33, 80, 512, 128), (64, 129, 1152, 64), (1, 4096, 4096, 32), (7, 512, 8192, 32)]
 
@@ -348,3 +349,265 @@ def test_attention_missing_pages_and_long_tables():
     A.sfx_attn_q4(q.to(DEV), cache, cut, torch.tensor([130, 10 ** 9, -3], dtype=torch.int32, device=DEV), out, ws, lse=lse)
     check_attn(q, [tuple(x[:72] for x in p) for p in kv], [72, 72, 0], None, D ** -0.5, "bf16", out, lse,
                [s[:72] for s in skip])
+
+
+# ------------------------------------------------------------------------------ together
+
+def make_layer(d, Hq, Hkv, D, seed):
+    """Attention weights of one layer in int4 (host)."""
+    g = torch.Generator().manual_seed(seed)
+    n = (Hq + 2 * Hkv) * D
+    w = {"Wqkv": torch.randint(0, 256, (n, d // 2), generator=g, dtype=torch.uint8),
+         "Wqkv_s": (torch.rand(n, d // 32, generator=g) * 0.5 / d ** 0.5 + 1e-3).half(),
+         "Wo": torch.randint(0, 256, (d, Hq * D // 2), generator=g, dtype=torch.uint8),
+         "Wo_s": (torch.rand(d, Hq * D // (64 if Hq * D % 64 == 0 else 32), generator=g) * 0.5 / (Hq * D) ** 0.5 + 1e-3).half(),
+         "bqkv": torch.randn(n, generator=g) * 0.1, "bo": torch.randn(d, generator=g)}
+    return w
+
+
+class Reference:
+    """The attention half in fp64 on the host: values of the cache by (sequence, position)."""
+
+    def __init__(self, w, Hq, Hkv, D, cs, pairs, dt, scale):
+        self.w = {k: v.numpy() for k, v in w.items()}
+        self.Hq, self.Hkv, self.D, self.cs, self.pairs, self.dt, self.scale = Hq, Hkv, D, cs, pairs, dt, scale
+        self.k, self.v = {}, {}
+
+    def store(self, b, p, k, v):
+        """k, v [Hkv][D] fp32, not rotated."""
+        at = np.array([p])
+        self.k[b, p] = Q.values(*Q.quantise(Q.rotate(k[None], at, self.cs, self.pairs)[0], 65504.0))
+        self.v[b, p] = Q.values(*Q.quantise(v.astype(np.float32), 8188.0))
+
+    def step(self, qkv32, pos, window):
+        """From the GPU's fp32 projection qkv32: o [B][Hq D] in fp64 and its rounding bound."""
+        Hq, Hkv, D = self.Hq, self.Hkv, self.D
+        outs, tols = [], []
+        for b, p in enumerate(pos):
+            q = qkv32[b, :Hq * D].reshape(Hq, D)
+            if p < 0:
+                outs.append(np.zeros(Hq * D))
+                tols.append(np.zeros(Hq * D))
+                continue
+            self.store(b, p, qkv32[b, Hq * D:(Hq + Hkv) * D].reshape(Hkv, D), qkv32[b, (Hq + Hkv) * D:].reshape(Hkv, D))
+            q = np64(torch.from_numpy(Q.rotate(q[None], np.array([p]), self.cs, self.pairs)[0]).to(DT[self.dt]))
+            at = range(max(0, p + 1 - window) if window else 0, p + 1)
+            k, v = (np.stack([c[b, i] for i in at]) for c in (self.k, self.v))
+            o, _, ab = Q.attention(q, k, v, self.scale)
+            d = Q.score_bound(q, np.abs(k).reshape(len(k), Hkv, -1, 32).max((0, 1, 3)) / 7, self.scale) + 2.0 ** -22 * 40
+            tol = (2 * 2.0 ** -11 + 2 * d + 2.0 ** -18) * ab * 1.01 + HALF_STEP[self.dt] * np.abs(o) + 2.0 ** -25
+            outs.append(o.reshape(-1))
+            tols.append(tol.reshape(-1))
+        return np.stack(outs), np.stack(tols)
+
+    def project_out(self, o, x_tol):
+        q = Q.unpack_rows(self.w["Wo"]).astype(np.float64)
+        wo = q * np.repeat(self.w["Wo_s"].astype(np.float64), q.shape[1] // self.w["Wo_s"].shape[1], 1)
+        y = o @ wo.T + self.w["bo"].astype(np.float64)
+        tol = x_tol @ np.abs(wo).T + Q.linear_q4_bound(o, self.w["Wo"], self.w["Wo_s"]) * 1.01 + 2.0 ** -22 * np.abs(y)
+        return y, tol
+
+
+BLOCKS = [(256, 4, 2, 64, 16, "f16", False, 0), (320, 5, 5, 32, 8, "bf16", True, 9)]
+
+
+@pytest.mark.parametrize("case", BLOCKS, ids=lambda c: "-".join(map(str, c)))
+def test_attention_half_over_steps(case):
+    """A prompt of ragged lengths, then decode steps: projection, append, attention and output
+    projection through AttnStep, each step against the oracle on the same cache."""
+    from activation_sparse_ffn_amd import AttnStep
+    d, Hq, Hkv, D, page, dt, pairs, window = case
+    say(f"attention half {case}")
+    B, lens = 3, [19, 0, 7]
+    table, pages = make_table([n + 12 for n in lens], page, 5)
+    cs = rope_table(64, D)
+    w = make_layer(d, Hq, Hkv, D, 3)
+    dev_w = {k: v.to(DEV) for k, v in w.items()}
+    pos = torch.tensor([n - 1 for n in lens], dtype=torch.int32, device=DEV)
+    step = AttnStep(Hq, Hkv, D, B, dt, table.to(DEV), pos, pages, page=page, cos_sin=torch.from_numpy(cs).to(DEV),
+                    interleaved=pairs, window=window)
+    ref = Reference(w, Hq, Hkv, D, cs, pairs, dt, D ** -0.5)
+    g = torch.Generator().manual_seed(1)
+    T = sum(lens)
+    k, v = (torch.randn(T, Hkv, D, generator=g) for _ in range(2))
+    p_seq = np.concatenate([np.full(n, b) for b, n in enumerate(lens)]).astype(np.int32)
+    p_pos = np.concatenate([np.arange(n) for n in lens]).astype(np.int32)
+    step.prefill(k.to(DEV), v.to(DEV), torch.from_numpy(p_pos).to(DEV), torch.from_numpy(p_seq).to(DEV))
+    for t in range(T):
+        ref.store(int(p_seq[t]), int(p_pos[t]), k[t].numpy(), v[t].numpy())
+    for s in range(5):
+        pos += 1
+        if s == 3:
+            pos[2] = -1                                  # a request that has ended
+        x = torch.randn(B, d, generator=g).to(DT[dt])
+        y = torch.full((B, d), float("nan"), device=DEV)
+        step.run(dev_w, x.to(DEV), y)
+        qkv = step.qkv.cpu().numpy()
+        want = Q.linear_q4(np64(x), w["Wqkv"].numpy(), w["Wqkv_s"].numpy(), w["bqkv"].numpy())
+        tol = Q.linear_q4_bound(np64(x), w["Wqkv"].numpy(), w["Wqkv_s"].numpy()) + 2.0 ** -22 * np.abs(want)
+        assert (np.abs(qkv - want) <= tol).all()
+        o, o_tol = ref.step(qkv, pos.tolist(), window)
+        assert (np.abs(np64(step.o).reshape(B, -1) - o) <= o_tol).all(), s
+        yo, y_tol = ref.project_out(o, o_tol)
+        assert (np.abs(np64(y) - yo) <= y_tol).all(), s
+
+
+def test_parallel_block_layer():
+    """run_layer with an attention half: the FFN's y and the attention's, added."""
+    import synthetic as S
+    from activation_sparse_ffn_amd import AttnStep, StepBuffers, run_layer
+    cfg = S.scaled(S.CONFIGS["C4"], name="par", d=512, f=1056, h=128)
+    B, Hq, Hkv, D, page = 2, 4, 2, 64, 8
+    say("parallel block")
+    L = S.make_layer(cfg, 0, device=DEV)
+    w = {k: v.to(DEV) for k, v in make_layer(cfg.d, Hq, Hkv, D, 8).items()}
+    layer = {**L.tensors(), **w}
+    x = S.make_tokens(cfg, 0, 1, B, device=DEV)[0]
+    table, pages = make_table([10, 10], page, 2)
+    outs = []
+    for both in (False, True):
+        buf = StepBuffers(cfg.d, cfg.f, cfg.h, B, cfg.wdtype, cfg.pred_storage)
+        attn = AttnStep(Hq, Hkv, D, B, "f16", table.to(DEV), torch.zeros(B, dtype=torch.int32, device=DEV), pages, page=page)
+        run_layer(buf, layer, x, L.threshold, cfg.act, attn=attn if both else None)
+        outs.append(np64(buf.y))
+    y = torch.empty(B, cfg.d, device=DEV)
+    attn.run(layer, x, y)
+    ffn, both = outs
+    assert (np.abs(both - (ffn + np64(y))) <= 2.0 ** -22 * (np.abs(both) + np.abs(np64(y)) + np.abs(ffn))).all()
+    assert np.abs(np64(y)).max() > 0
+
+
+def test_graph_replays_and_shared_workspace():
+    """A captured decode step replayed over moving positions, with eager work between, and two
+    captured graphs of different shapes that share one workspace."""
+    from activation_sparse_ffn_amd import AttnStep
+    d, Hq, Hkv, D, page, B = 256, 8, 2, 64, 16, 2
+    table, pages = make_table([900, 900], page, 1)
+    w = {k: v.to(DEV) for k, v in make_layer(d, Hq, Hkv, D, 4).items()}
+    g = torch.Generator().manual_seed(9)
+    steps = []
+    for _ in range(2):
+        pos = torch.tensor([699, 400], dtype=torch.int32, device=DEV)
+        steps.append(AttnStep(Hq, Hkv, D, B, "f16", table.to(DEV), pos, pages, page=page))
+    k, v = (torch.randn(1101, Hkv, D, generator=g).to(DEV) for _ in range(2))
+    p_seq = torch.tensor([0] * 700 + [1] * 401, dtype=torch.int32, device=DEV)
+    p_pos = torch.cat([torch.arange(700), torch.arange(401)]).to(torch.int32).to(DEV)
+    for s in steps:
+        s.prefill(k, v, p_pos, p_seq)
+    graphed, eager = steps
+    x = torch.zeros(B, d, dtype=torch.float16, device=DEV)
+    y = torch.zeros(B, d, device=DEV)
+    # another shape on the same workspace
+    q2, cache2, table2, _ = make_attn(3, 4, 4, 32, 8, [600, 1, 300], "f16", 3)
+    lens2 = torch.tensor([600, 1, 300], dtype=torch.int32, device=DEV)
+    q2 = q2.to(DEV)
+    out2, ref2 = torch.zeros_like(q2), torch.zeros_like(q2)
+    need = max(graphed.ws.numel(), A.sfx_attn_q4_ws(3, 4, 4, 32, table2.shape[1] * 8))
+    graphed.ws = A.workspace(need)
+    A.sfx_attn_q4(q2, cache2, table2, lens2, ref2, A.workspace(need))
+    for s in steps:                                      # warm; both caches take this token
+        s.run(w, x, y)
+    torch.cuda.synchronize()
+    ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(ga):
+        graphed.run(w, x, y)
+    with torch.cuda.graph(gb):
+        A.sfx_attn_q4(q2, cache2, table2, lens2, out2, graphed.ws)
+    for rep in range(4):
+        say(f"graph replay {rep}")
+        xn = torch.randn(B, d, generator=g).half()
+        for s in steps:
+            s.pos += 1
+        x.copy_(xn.to(DEV))
+        ga.replay()
+        out2.zero_()
+        gb.replay()
+        ye = torch.empty(B, d, device=DEV)
+        eager.run(w, xn.to(DEV), ye)
+        torch.cuda.synchronize()
+        assert torch.equal(y, ye) and torch.equal(out2, ref2), rep
+        _ = torch.randn(1000, device=DEV).sum().item()
+
+
+def test_two_streams():
+    """Two attention calls and two projections at once, on streams and workspaces of their own."""
+    cases = [make_attn(2, 8, 2, 128, 16, [3000, 2500], "bf16", s) for s in (1, 2)]
+    lens = torch.tensor([3000, 2500], dtype=torch.int32, device=DEV)
+    lin = [[t.to(DEV) for t in make_linear(3, 700, 1024, 64, "f16", s)] for s in (5, 6)]
+    want = []
+    for (q, cache, table, _), (x, W, s, b) in zip(cases, lin):
+        out, y = torch.empty(2, 8, 128, dtype=torch.bfloat16, device=DEV), torch.empty(3, 700, device=DEV)
+        A.sfx_attn_q4(q.to(DEV), cache, table, lens, out, A.workspace(A.sfx_attn_q4_ws(2, 8, 2, 128, table.shape[1] * 16)))
+        A.sfx_linear_q4(x, W, s, y, bias=b)
+        want.append((out, y))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [(torch.empty_like(o), torch.empty_like(y)) for o, y in want]
+    qs = [c[0].to(DEV) for c in cases]
+    wss = [A.workspace(A.sfx_attn_q4_ws(2, 8, 2, 128, c[2].shape[1] * 16)) for c in cases]
+    torch.cuda.synchronize()
+    for rep in range(5):
+        for i, st in enumerate(streams):
+            A.sfx_attn_q4(qs[i], cases[i][1], cases[i][2], lens, got[i][0], wss[i], stream=st)
+            with torch.cuda.stream(st):
+                A.sfx_linear_q4(lin[i][0], lin[i][1], lin[i][2], got[i][1], bias=lin[i][3])
+    torch.cuda.synchronize()
+    for (o, y), (wo, wy) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(y, wy)
+
+
+def test_cache_beyond_4_gib():
+    """Pages whose bytes lie past 32-bit offsets."""
+    Hq, Hkv, D, page = 8, 8, 256, 128
+    per_page = Hkv * (page // 8) * 9 * D
+    pages = (9 << 29) // per_page + 2                     # 4.5 GiB
+    say(f"cache of {pages * per_page / 2**30:.2f} GiB")
+    cache = torch.empty(pages, Hkv, page // 8, 9 * D, dtype=torch.uint8, device=DEV)
+    ids = [pages - 1, 0, pages - 2]
+    table = torch.tensor([ids], dtype=torch.int32, device=DEV)
+    for i in ids:
+        cache[i].fill_(0xFF)
+    n = 300
+    rng = np.random.default_rng(0)
+    k, v = (torch.from_numpy(rng.standard_normal((n, Hkv, D)).astype(np.float32)) for _ in range(2))
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    seq = torch.zeros(n, dtype=torch.int32, device=DEV)
+    A.sfx_kv_append_q4(None, k.to(DEV), v.to(DEV), pos, table, cache, None, seq=seq)
+    kn, vn = Q.values(*Q.quantise(k.numpy(), 65504.0)), Q.values(*Q.quantise(v.numpy(), 8188.0))
+    ko, vo = torch.empty(n, Hkv, D, device=DEV), torch.empty(n, Hkv, D, device=DEV)
+    A.sfx_kv_read_q4(pos, table, cache, ko, vo, seq=seq)
+    assert np.array_equal(np64(ko), kn) and np.array_equal(np64(vo), vn)
+    q = torch.from_numpy(rng.standard_normal((1, Hq, D)).astype(np.float32)).half()
+    out, lse = torch.empty(1, Hq, D, dtype=torch.float16, device=DEV), torch.empty(1, Hq, device=DEV)
+    ws = A.workspace(A.sfx_attn_q4_ws(1, Hq, Hkv, D, 3 * page))
+    A.sfx_attn_q4(q.to(DEV), cache, table, torch.tensor([n], dtype=torch.int32, device=DEV), out, ws, lse=lse)
+    check_attn(q, [(kn, vn)], [n], None, D ** -0.5, "f16", out, lse)
+
+
+def test_attention_largest_batch():
+    """64 sequences and 256 query heads, lengths from none to many, queries apart in memory."""
+    B, Hq, Hkv, D, page = 64, 256, 8, 32, 8
+    lens = [(b * 37) % 500 for b in range(B)]
+    q, cache, table, kv = make_attn(B, Hq, Hkv, D, page, lens, "f16", 77)
+    wide = torch.zeros(B, Hq + 1, D, dtype=torch.float16, device=DEV)
+    wide[:, :Hq] = q.to(DEV)
+    ws = A.workspace(A.sfx_attn_q4_ws(B, Hq, Hkv, D, table.shape[1] * page))
+    out, lse = torch.empty(B, Hq, D, dtype=torch.float16, device=DEV), torch.empty(B, Hq, device=DEV)
+    say("attention 64 x 256")
+    A.sfx_attn_q4(wide[:, :Hq], cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), out, ws, lse=lse)
+    check_attn(q, kv, lens, None, D ** -0.5, "f16", out, lse)
+
+
+def test_shared_pages_and_drafted_tokens():
+    """Two sequences whose tables share a prefix, and several query tokens of one sequence as
+    rows with the same pages and their own lens."""
+    Hq, Hkv, D, page = 4, 1, 64, 8
+    q, cache, table, kv = make_attn(1, Hq, Hkv, D, page, [50], "bf16", 31)
+    rows = table.expand(4, -1).contiguous()
+    lens = [50, 49, 48, 1]
+    rng = np.random.default_rng(1)
+    q = torch.from_numpy(rng.standard_normal((4, Hq, D)).astype(np.float32)).to(torch.bfloat16)
+    ws = A.workspace(A.sfx_attn_q4_ws(4, Hq, Hkv, D, rows.shape[1] * page))
+    out, lse = torch.empty(4, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(4, Hq, device=DEV)
+    A.sfx_attn_q4(q.to(DEV), cache, rows, torch.tensor(lens, dtype=torch.int32, device=DEV), out, ws, lse=lse)
+    check_attn(q, kv * 4, lens, None, D ** -0.5, "bf16", out, lse)
