@@ -516,32 +516,29 @@ def _run_on(dev, stream, fn, args, where):
         raise SfxError(st, where)
 
 
-def _dense(t, where, name, dtype):
-    if t.dtype != dtype:
-        raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be contiguous")
-    return t.data_ptr()
-
-
 def _rows(t, where, name):
     """Row stride of a 2-D tensor whose rows are dense (rows may be apart)."""
     n, d = t.shape
-    if t.is_contiguous():
-        return d
-    if d > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if d > 1 and s1 != 1:
         raise ValueError(f"{where}: the rows of {name} must be dense")
-    return t.stride(0) if n > 1 else d
+    return s0 if n > 1 else d
 
 
 def _head_rows(t, where, name):
     """Token stride of [tokens][heads][D] with dense heads (tokens may be apart)."""
     T, H, D = t.shape
-    if t.is_contiguous():
-        return H * D
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    s0, s1, s2 = t.stride()
+    if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
         raise ValueError(f"{where}: the heads of {name} must be dense")
-    return t.stride(0) if T > 1 else H * D
+    return s0 if T > 1 else H * D
+
+
+def _not_dense(where, t, name, dtype):
+    """Raise for a tensor that is not of `dtype` or not contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+    raise ValueError(f"{where}: {name} must be contiguous")
 
 
 def sfx_linear_q4(x, W, W_scales, y, bias=None, accumulate=False, stream=None):
@@ -559,10 +556,14 @@ def sfx_linear_q4(x, W, W_scales, y, bias=None, accumulate=False, stream=None):
     if ns != n or groups < 1 or d % groups != 0:
         raise ValueError(f"{w}: W_scales must be [n][d / group]")
     xdt = x.dtype
-    if xdt != _F16 and xdt != _BF16:
+    if xdt is not _F16 and xdt is not _BF16:
         raise TypeError(f"{w}: x must be fp16 or bf16")
-    if y.dtype != _FP32:
+    if y.dtype is not _FP32:
         raise TypeError(f"{w}: y is {y.dtype}, expected {_FP32}")
+    if W.dtype is not _U8 or not W.is_contiguous():
+        _not_dense(w, W, "W", _U8)
+    if W_scales.dtype is not _F16 or not W_scales.is_contiguous():
+        _not_dense(w, W_scales, "W_scales", _F16)
     dev = x.get_device()
     if dev < 0 or W.get_device() != dev or W_scales.get_device() != dev or y.get_device() != dev:
         _device_error(w, x, W, W_scales, y)
@@ -570,13 +571,15 @@ def sfx_linear_q4(x, W, W_scales, y, bias=None, accumulate=False, stream=None):
     if bias is not None:
         if bias.numel() != n:
             raise ValueError(f"{w}: bias must hold {n} values")
+        if bias.dtype is not _FP32 or not bias.is_contiguous():
+            _not_dense(w, bias, "bias", _FP32)
         if bias.get_device() != dev:
             _device_error(w, x, bias)
-        pb = _dense(bias, w, "bias", _FP32)
-    _run_on(dev, stream, load().sfx_linear_q4,
-            (SFX_F16 if xdt == _F16 else SFX_BF16, d // groups, B, n, d, x.data_ptr(), _rows(x, w, "x"),
-             _dense(W, w, "W", _U8), _dense(W_scales, w, "W_scales", _F16), pb, 1 if accumulate else 0, y.data_ptr(),
-             _rows(y, w, "y")), w)
+        pb = bias.data_ptr()
+    _run_on(dev, stream, (_lib or load()).sfx_linear_q4,
+            (SFX_F16 if xdt is _F16 else SFX_BF16, d // groups, B, n, d, x.data_ptr(),
+             d if x.is_contiguous() else _rows(x, w, "x"), W.data_ptr(), W_scales.data_ptr(), pb, 1 if accumulate else 0,
+             y.data_ptr(), n if y.is_contiguous() else _rows(y, w, "y")), w)
 
 
 def kv_cache_q4(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> torch.Tensor:
@@ -588,13 +591,15 @@ def kv_cache_q4(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> t
 
 def _cache_shape(cache, table, D, Hkv, w):
     """(page, num_pages, max_pages, B) of a cache and its page table."""
-    if cache.dim() != 4:
-        raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/8][{9 * D}]")
+    if cache.dim() != 4 or table.dim() != 2:
+        raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/8][{9 * D}], table [B][max pages]")
     num_pages, hc, octets, nine_d = cache.shape
     if hc != Hkv or nine_d != 9 * D:
         raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/8][{9 * D}]")
-    if table.dim() != 2:
-        raise ValueError(f"{w}: table must be [B][max pages]")
+    if cache.dtype is not _U8 or not cache.is_contiguous():
+        _not_dense(w, cache, "cache", _U8)
+    if table.dtype is not _I32 or not table.is_contiguous():
+        _not_dense(w, table, "table", _I32)
     B, max_pages = table.shape
     return octets * 8, num_pages, max_pages, B
 
@@ -602,9 +607,11 @@ def _cache_shape(cache, table, D, Hkv, w):
 def _tokens(t, T, dev, w, name):
     if t.numel() != T:
         raise ValueError(f"{w}: {name} must hold {T} entries")
+    if t.dtype is not _I32 or not t.is_contiguous():
+        _not_dense(w, t, name, _I32)
     if t.get_device() != dev:
         _device_error(w, t)
-    return _dense(t, w, name, _I32)
+    return t.data_ptr()
 
 
 def sfx_kv_append_q4(q, k, v, pos, table, cache, q_out, seq=None, cos_sin=None, interleaved=False, stream=None):
@@ -614,9 +621,10 @@ def sfx_kv_append_q4(q, k, v, pos, table, cache, q_out, seq=None, cos_sin=None, 
     w = "sfx_kv_append_q4"
     if k.dim() != 3 or v.dim() != 3:
         raise ValueError(f"{w}: k and v must be [T][Hkv][D]")
-    T, Hkv, D = k.shape
+    shape = k.shape
+    T, Hkv, D = shape
     xdt = k.dtype
-    if v.shape != k.shape or v.dtype != xdt:
+    if v.shape != shape or v.dtype is not xdt:
         raise ValueError(f"{w}: k and v must have one shape and dtype")
     if xdt not in WDT:
         raise TypeError(f"{w}: unsupported dtype {xdt}")
@@ -625,50 +633,58 @@ def sfx_kv_append_q4(q, k, v, pos, table, cache, q_out, seq=None, cos_sin=None, 
         _device_error(w, k, v, table, cache)
     Hq, ldq, pq, pqo, qdt = 0, 0, None, None, 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != xdt:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != D or q.dtype is not xdt:
             raise ValueError(f"{w}: q must be [{T}][Hq][{D}] in k's dtype")
-        Hq = q.shape[1]
-        if q_out is None or q_out.shape != q.shape:
+        Hq = shape[1]
+        if q_out is None or q_out.shape != shape:
             raise ValueError(f"{w}: q_out must have q's shape")
-        qdt = WDT.get(q_out.dtype, SFX_F32)
-        if qdt == SFX_F32:
+        odt = q_out.dtype
+        if odt is not _F16 and odt is not _BF16:
             raise TypeError(f"{w}: q_out must be fp16 or bf16")
+        if not q_out.is_contiguous():
+            _not_dense(w, q_out, "q_out", odt)
+        qdt = SFX_F16 if odt is _F16 else SFX_BF16
         if q.get_device() != dev or q_out.get_device() != dev:
             _device_error(w, k, q, q_out)
-        pq, ldq, pqo = q.data_ptr(), _head_rows(q, w, "q"), _dense(q_out, w, "q_out", q_out.dtype)
+        pq, ldq, pqo = q.data_ptr(), _head_rows(q, w, "q"), q_out.data_ptr()
     rot, max_pos, pcs = 0, 0, None
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError(f"{w}: cos_sin must be [positions][rot]")
+        if cos_sin.dtype is not _FP32 or not cos_sin.is_contiguous():
+            _not_dense(w, cos_sin, "cos_sin", _FP32)
         if cos_sin.get_device() != dev:
             _device_error(w, k, cos_sin)
         max_pos, rot = cos_sin.shape
-        pcs = _dense(cos_sin, w, "cos_sin", _FP32)
+        pcs = cos_sin.data_ptr()
     page, num_pages, max_pages, B = _cache_shape(cache, table, D, Hkv, w)
-    _run_on(dev, stream, load().sfx_kv_append_q4,
+    _run_on(dev, stream, (_lib or load()).sfx_kv_append_q4,
             (WDT[xdt], qdt, T, Hq, Hkv, D, pq, ldq, k.data_ptr(), _head_rows(k, w, "k"), v.data_ptr(),
              _head_rows(v, w, "v"), _tokens(pos, T, dev, w, "pos"),
              None if seq is None else _tokens(seq, T, dev, w, "seq"), pcs, rot, max_pos, 1 if interleaved else 0, B,
-             max_pages, _dense(table, w, "table", _I32), page, num_pages, _dense(cache, w, "cache", _U8), pqo), w)
+             max_pages, table.data_ptr(), page, num_pages, cache.data_ptr(), pqo), w)
 
 
 def sfx_kv_read_q4(pos, table, cache, k_out, v_out, seq=None, stream=None):
     """Values held at (seq[t], pos[t]): k_out, v_out [T][Hkv][D] (fp32, fp16 or bf16)."""
     w = "sfx_kv_read_q4"
-    odt = k_out.dtype
-    if k_out.dim() != 3 or v_out.shape != k_out.shape or v_out.dtype != odt:
+    odt, shape = k_out.dtype, k_out.shape
+    if len(shape) != 3 or v_out.shape != shape or v_out.dtype is not odt:
         raise ValueError(f"{w}: k_out and v_out must be [T][Hkv][D] of one dtype")
     if odt not in WDT:
         raise TypeError(f"{w}: unsupported dtype {odt}")
-    T, Hkv, D = k_out.shape
+    if not k_out.is_contiguous() or not v_out.is_contiguous():
+        raise ValueError(f"{w}: k_out and v_out must be contiguous")
+    T, Hkv, D = shape
     dev = k_out.get_device()
     if dev < 0 or v_out.get_device() != dev or table.get_device() != dev or cache.get_device() != dev:
         _device_error(w, k_out, v_out, table, cache)
     page, num_pages, max_pages, B = _cache_shape(cache, table, D, Hkv, w)
-    _run_on(dev, stream, load().sfx_kv_read_q4,
+    _run_on(dev, stream, (_lib or load()).sfx_kv_read_q4,
             (WDT[odt], T, Hkv, D, _tokens(pos, T, dev, w, "pos"),
-             None if seq is None else _tokens(seq, T, dev, w, "seq"), B, max_pages, _dense(table, w, "table", _I32), page,
-             num_pages, _dense(cache, w, "cache", _U8), _dense(k_out, w, "k_out", odt), _dense(v_out, w, "v_out", odt)),
+             None if seq is None else _tokens(seq, T, dev, w, "seq"), B, max_pages, table.data_ptr(), page,
+             num_pages, cache.data_ptr(), k_out.data_ptr(), v_out.data_ptr()),
             w)
 
 
@@ -684,12 +700,15 @@ def sfx_attn_q4(q, cache, table, lens, out, ws, starts=None, scale=None, lse=Non
     w = "sfx_attn_q4"
     if q.dim() != 3 or cache.dim() != 4:
         raise ValueError(f"{w}: q must be [B][Hq][D], cache [pages][Hkv][page/8][9 D]")
-    B, Hq, D = q.shape
+    shape = q.shape
+    B, Hq, D = shape
     qdt = q.dtype
-    if qdt != _F16 and qdt != _BF16:
+    if qdt is not _F16 and qdt is not _BF16:
         raise TypeError(f"{w}: q must be fp16 or bf16")
-    if out.shape != q.shape:
+    if out.shape != shape:
         raise ValueError(f"{w}: out must have q's shape")
+    if out.dtype is not qdt or not out.is_contiguous():
+        _not_dense(w, out, "out", qdt)
     Hkv = cache.shape[1]
     page, num_pages, max_pages, Bt = _cache_shape(cache, table, D, Hkv, w)
     if Bt != B:
@@ -702,18 +721,23 @@ def sfx_attn_q4(q, cache, table, lens, out, ws, starts=None, scale=None, lse=Non
     if lse is not None:
         if lse.shape != (B, Hq):
             raise ValueError(f"{w}: lse must be [{B}][{Hq}]")
+        if lse.dtype is not _FP32 or not lse.is_contiguous():
+            _not_dense(w, lse, "lse", _FP32)
         if lse.get_device() != dev:
             _device_error(w, q, lse)
-        pl = _dense(lse, w, "lse", _FP32)
+        pl = lse.data_ptr()
     if ws is not None:
         if ws.get_device() != dev:
             _device_error(w, q, ws)
-        pw, nws = _dense(ws, w, "ws", ws.dtype), ws.numel() * ws.element_size()
-    _run_on(dev, stream, load().sfx_attn_q4,
-            (SFX_F16 if qdt == _F16 else SFX_BF16, B, Hq, Hkv, D, q.data_ptr(), _head_rows(q, w, "q"), max_pages,
-             _dense(table, w, "table", _I32), page, num_pages, _dense(cache, w, "cache", _U8),
+        if not ws.is_contiguous():
+            raise ValueError(f"{w}: ws must be contiguous")
+        pw, nws = ws.data_ptr(), ws.nbytes
+    _run_on(dev, stream, (_lib or load()).sfx_attn_q4,
+            (SFX_F16 if qdt is _F16 else SFX_BF16, B, Hq, Hkv, D, q.data_ptr(),
+             Hq * D if q.is_contiguous() else _head_rows(q, w, "q"), max_pages,
+             table.data_ptr(), page, num_pages, cache.data_ptr(),
              None if starts is None else _tokens(starts, B, dev, w, "starts"), _tokens(lens, B, dev, w, "lens"),
-             D ** -0.5 if scale is None else float(scale), _dense(out, w, "out", qdt), pl, pw, nws), w)
+             D ** -0.5 if scale is None else float(scale), out.data_ptr(), pl, pw, nws), w)
 
 
 STREAM_READ_OUT_WORDS = 16384
