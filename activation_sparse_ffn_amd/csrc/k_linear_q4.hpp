@@ -3,12 +3,16 @@
 // the storage of its int4 rows).
 //
 // Tokens are the rows and 16 weight rows the columns of 16x16x32 products, so a lane
-// meets one weight row only and needs one scale per group.  A lane's 16-byte load is one
-// group of 32 codes of its row (four lanes cover 128 columns of 16 rows); a 4 x 4
-// transposition over the wave's quarters turns the four loaded words into the operands of
-// four products, one per group.  The waves of a workgroup share 16 R rows and deal the
-// 128-column chunks among themselves; their sums are added in wave order through LDS, so
-// y is bitwise reproducible.
+// meets one weight row only and needs one scale per group.  The waves of a workgroup share
+// their rows and deal the columns among themselves; their sums are added in wave order
+// through LDS, so y is bitwise reproducible.  Three kernels, by how much of x there is:
+//   few tokens   all of x in LDS; bound by reading the codes.
+//   wide, rows   x in blocks, 16 or 32 rows per workgroup: each workgroup reads all of x, from
+//                L2, and writes it to LDS; from about 16 tokens on that and the decoding
+//                weigh more than the codes.
+// Measured (one MI355X): 1 x 28672 x 7168, scales per 128: 27.5 us = 3.9 TB/s of 106 MB; 1 x 4096
+// x 4096: 5.8 us; 37 x 8192 x 8192, scales per 64: 24.1 us against 7.1 for its 38.7 MB (VALU 34%
+// of the time busy, MFMA 16%).
 #pragma once
 #include "sfx_launch.hpp"
 #include "sfx_q4.hpp"
@@ -79,18 +83,22 @@ __device__ __forceinline__ float lin_scale(const LinChunk<GSH>& x, int j) {
   else return half_at(x.s[0], 0);
 }
 
+// The operand that takes the codes' offset back, where there is one.
+template <class T>
+__device__ __forceinline__ Raw<16> lin_offset() {
+  if constexpr (Q4<T>::offset) return Q4<T>::minus24();
+  else return zero16();
+}
+
 // Sums of a chunk: `groups` of its 32 columns exist (4 but in the last chunk); k: the codes
 // as loaded; xrow: this lane's slice of the chunk's ordered x per token tile, in LDS.
-template <class T, int NT, int NI, int R, int GSH>
-__device__ __forceinline__ void lin_chunk(LinChunk<GSH> (&w)[R], const uint8_t* const (&xrow)[NT], int groups,
-                                          const Q4<T>& dec, float (&acc)[R][NT][NI]) {
-  uint32_t k[R][4];
+template <class T, int NT, int GSH>
+__device__ __forceinline__ void lin_chunk(const LinChunk<GSH>& w, const uint8_t* const (&xrow)[NT], int groups,
+                                          const Q4<T>& dec, const Raw<16>& m24, float (&acc)[NT][4]) {
+  uint32_t k[4];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) k[r][j] = w[r].q.w[j] ^ 0x88888888u;
-    quarter_transpose(k[r]);
-  }
+  for (int j = 0; j < 4; ++j) k[j] = w.q.w[j] ^ 0x88888888u;
+  quarter_transpose(k);
   // groups that share a scale (1 << GSH of them) are summed in the matrix cores before it
   constexpr int kPer = 1 << GSH;
 #pragma unroll
@@ -99,43 +107,38 @@ __device__ __forceinline__ void lin_chunk(LinChunk<GSH> (&w)[R], const uint8_t* 
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         Raw<16> xp[kPer];
-        f32x4 from = {0.f, 0.f, 0.f, 0.f};
+        f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
           xp[u] = load_raw<16>(xrow[t] + (j + u) * 64);
-          if constexpr (Q4<T>::offset) from = Mma<T>::run(xp[u], Q4<T>::minus24(), from);
+          if constexpr (Q4<T>::offset) p = Mma<T>::run(xp[u], m24, p);
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          f32x4 p = from;
+        for (int u = 0; u < kPer; ++u) p = Mma<T>::run(xp[u], dec.word(k[j + u]), p);
 #pragma unroll
-          for (int u = 0; u < kPer; ++u) p = Mma<T>::run(xp[u], dec.word(k[r][j + u]), p);
-#pragma unroll
-          for (int i = 0; i < NI; ++i) acc[r][t][i] = fmaf(lin_scale<GSH>(w[r], j), p[i], acc[r][t][i]);
-        }
+        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(lin_scale<GSH>(w, j), p[i], acc[t][i]);
       }
     }
   }
 }
 
-// The waves' sums in wave order, bias, y.
-template <int NT, int NI, int R, int W>
-__device__ __forceinline__ void lin_finish(const LinearArgs& a, float* red, int row0, int wave, int m, int c,
-                                           const float (&acc)[R][NT][NI]) {
+// The waves' sums in wave order, bias, y.  RG groups of W waves, 16 rows from row0 on each.
+template <int NT, int NI, int W, int RG>
+__device__ __forceinline__ void lin_finish(const LinearArgs& a, float* red, int row0, int wave, int rg, int m, int c,
+                                           const float (&acc)[NT][NI]) {
   constexpr int TT = 4 * NI * NT;
+  red += rg * (W * 16 * (TT + 1));
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) red[(wave * 16 * R + 16 * r + m) * (TT + 1) + (4 * t + c) * NI + i] = acc[r][t][i];
+    for (int i = 0; i < NI; ++i) red[(wave * 16 + m) * (TT + 1) + (4 * t + c) * NI + i] = acc[t][i];
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * R * TT; e += W * kWave) {
-    const int row = e % (16 * R), tok = e / (16 * R);
+  for (int e = threadIdx.x - rg * W * kWave; e < 16 * TT; e += W * kWave) {
+    const int row = e % 16, tok = e / 16;
     if (row0 + row < a.n && tok < a.B) {
       float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < W; ++k) v += red[(k * 16 * R + row) * (TT + 1) + tok];
+      for (int k = 0; k < W; ++k) v += red[(k * 16 + row) * (TT + 1) + tok];
       if (a.bias) v += a.bias[row0 + row];
       float* y = a.y + (size_t)tok * a.ldy + row0 + row;
       *y = a.accumulate ? *y + v : v;
@@ -236,10 +239,11 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
   __syncthreads();
   const uint8_t* xlane = sh + min(lin_token<NI>(0, m), a.B - 1) * xstride + c * 16;
 
-  float acc[1][1][NI];
+  float acc[1][NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) acc[0][0][i] = 0.f;
+  for (int i = 0; i < NI; ++i) acc[0][i] = 0.f;
   const Q4<T> dec;
+  const Raw<16> m24 = lin_offset<T>();
   for (int i0 = 0; i0 < todo; i0 += kLinSlots) {
 #pragma unroll
     for (int s = 0; s < kLinSlots; ++s) {
@@ -261,12 +265,12 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
             for (int u = 0; u < kPer; ++u) {
               const Raw<16> xp = load_raw<16>(xr + (j + u) * 64);
               const uint32_t k = *reinterpret_cast<const uint32_t*>(w + ((j + u + (m >> 1)) & 7) * 16) ^ 0x88888888u;
-              if constexpr (Q4<T>::offset) p = Mma<T>::run(xp, Q4<T>::minus24(), p);
+              if constexpr (Q4<T>::offset) p = Mma<T>::run(xp, m24, p);
               p = Mma<T>::run(xp, dec.word(k), p);
             }
             const float f = half_at(sc[s].w[(j >> GSH) >> 1], (j >> GSH) & 1);
 #pragma unroll
-            for (int t = 0; t < NI; ++t) acc[0][0][t] = fmaf(f, p[t], acc[0][0][t]);
+            for (int t = 0; t < NI; ++t) acc[0][t] = fmaf(f, p[t], acc[0][t]);
           }
         }
         if (i + kLinSlots < todo) {
@@ -277,31 +281,26 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
     }
   }
   __syncthreads();
-  lin_finish<1, NI, 1, kLinWaves>(a, (float*)&ring[0][0][0], row0, wave, m, c, acc);
+  lin_finish<1, NI, kLinWaves, 1>(a, (float*)&ring[0][0][0], row0, wave, 0, m, c, acc);
 }
 
 // More tokens, or long rows: x passes through LDS in blocks of 1024 columns, a chunk of 128
-// for each wave; the next block's x and weights are on the way in registers meanwhile.
-// 16 R weight rows per workgroup.
-template <class T, int NT, int R, int GSH>
-__global__ __launch_bounds__(kLinWaves * kWave, NT * R <= 2 ? 4 : 2) void k_linear_q4_wide(LinearArgs a) {
+// for each wave; the next block's x and the weights of four blocks are on the way in registers
+// meanwhile.  16 weight rows per workgroup.
+template <class T, int NT, int GSH>
+__global__ __launch_bounds__(kLinWaves * kWave, NT <= 2 ? 4 : 2) void k_linear_q4_wide(LinearArgs a) {
   constexpr int kThreads = kLinWaves * kWave, kCols = 128 * kLinWaves, kRow = kCols * 2 + 16;
-  constexpr int kX = 16 * NT * kRow, kRed = kLinWaves * 16 * R * (16 * NT + 1) * 4;
+  constexpr int kX = 16 * NT * kRow, kRed = kLinWaves * 16 * (16 * NT + 1) * 4;
   constexpr int kPass = 16 * NT * (kCols / 8) / kThreads;       // 16-byte pieces of x per thread and block
-  constexpr int kAhead = NT * R <= 6 ? 4 : 2;                   // blocks of weights on the way (registers)
+  constexpr int kAhead = 4;                                     // blocks of weights on the way (registers)
   __shared__ __attribute__((aligned(16))) uint8_t sh[kX > kRed ? kX : kRed];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, c = lane >> 4;
-  const int row0 = blockIdx.x * 16 * R;
+  const int row0 = blockIdx.x * 16;
   const int ng = a.d >> 5, nblock = (ng + 4 * kLinWaves - 1) / (4 * kLinWaves);
-  const uint8_t* wrow[R];
-  const uint16_t* srow[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = min(row0 + 16 * r + m, a.n - 1);
-    wrow[r] = a.W + (size_t)row * (a.d >> 1);
-    srow[r] = a.s + (size_t)row * (ng >> GSH);
-  }
+  const int row = min(row0 + m, a.n - 1);
+  const uint8_t* wrow = a.W + (size_t)row * (a.d >> 1);
+  const uint16_t* srow = a.s + (size_t)row * (ng >> GSH);
   // thread's pieces of x: piece tid % 128 of tokens tid / 128 + 4 i
   const int piece = threadIdx.x & (kCols / 8 - 1), tok0 = threadIdx.x / (kCols / 8);
   constexpr int kStep = kThreads / (kCols / 8);
@@ -312,13 +311,10 @@ __global__ __launch_bounds__(kLinWaves * kWave, NT * R <= 2 ? 4 : 2) void k_line
     for (int i = 0; i < kPass; ++i)
       xv[i] = load_raw<16>(a.x + (size_t)min(tok0 + kStep * i, a.B - 1) * a.ldx + (size_t)col * 2);
   };
-  LinChunk<GSH> w[kAhead][R];
-  auto load_w = [&](int blk, LinChunk<GSH> (&to)[R]) {
+  LinChunk<GSH> w[kAhead];
+  auto load_w = [&](int blk, LinChunk<GSH>& to) {
     const int ck = blk * kLinWaves + wave;
-    if (4 * ck < ng) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) lin_load<GSH>(wrow[r], srow[r], ck, c, ng, to[r]);
-    }
+    if (4 * ck < ng) lin_load<GSH>(wrow, srow, ck, c, ng, to);
   };
   load_x(0);
 #pragma unroll
@@ -326,14 +322,13 @@ __global__ __launch_bounds__(kLinWaves * kWave, NT * R <= 2 ? 4 : 2) void k_line
   const uint8_t* xrow[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) xrow[t] = sh + min(16 * t + m, a.B - 1) * kRow + wave * 256 + c * 16;
-  float acc[R][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
   const Q4<T> dec;
+  const Raw<16> m24 = lin_offset<T>();
   for (int blk0 = 0; blk0 < nblock; blk0 += kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -344,19 +339,94 @@ __global__ __launch_bounds__(kLinWaves * kWave, NT * R <= 2 ? 4 : 2) void k_line
           *reinterpret_cast<Raw<16>*>(sh + (tok0 + kStep * i) * kRow + piece * 16) = lin_order(xv[i]);
         // x before the weights: loads are waited for in their order, and x is needed first
         if (blk + 1 < nblock) load_x(blk + 1);
-        LinChunk<GSH> now[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) now[r] = w[u][r];
+        const LinChunk<GSH> now = w[u];
         load_w(blk + kAhead, w[u]);
         __syncthreads();
         const int groups = ng - 4 * (blk * kLinWaves + wave);
-        if (groups >= 4) lin_chunk<T, NT, 4, R, GSH>(now, xrow, 4, dec, acc);
-        else lin_chunk<T, NT, 4, R, GSH>(now, xrow, groups, dec, acc);
+        if (groups >= 4) lin_chunk<T, NT, GSH>(now, xrow, 4, dec, m24, acc);
+        else lin_chunk<T, NT, GSH>(now, xrow, groups, dec, m24, acc);
         __syncthreads();
       }
     }
   }
-  lin_finish<NT, 4, R, kLinWaves>(a, (float*)sh, row0, wave, m, c, acc);
+  lin_finish<NT, 4, kLinWaves, 1>(a, (float*)sh, row0, wave, 0, m, c, acc);
+}
+
+// Many weight rows: two groups of four waves, 16 rows each, over blocks of 512 columns.  Two
+// blocks of x lie in LDS: while one is worked on, the next is written from registers and the
+// one behind it is on its way there, with one barrier a block.
+template <class T, int NT, int GSH>
+__global__ __launch_bounds__(kLinWaves * kWave, 2) void k_linear_q4_rows(LinearArgs a) {
+  constexpr int kThreads = kLinWaves * kWave, kChunks = 4, kCols = 128 * kChunks, kRow = kCols * 2 + 16;
+  constexpr int kX = 16 * NT * kRow, kRed = kLinWaves * 16 * (16 * NT + 1) * 4;
+  constexpr int kPass = 16 * NT * (kCols / 8) / kThreads;       // 16-byte pieces of x per thread and block
+  constexpr int kAhead = 4;                                     // blocks of weights on the way (registers)
+  __shared__ __attribute__((aligned(16))) uint8_t sh[2 * kX > kRed ? 2 * kX : kRed];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kc = wave % kChunks, rg = wave / kChunks;
+  const int m = lane & 15, c = lane >> 4;
+  const int row0 = (blockIdx.x * 2 + rg) * 16;
+  const int ng = a.d >> 5, nblock = (ng + 4 * kChunks - 1) / (4 * kChunks);
+  const int row = min(row0 + m, a.n - 1);
+  const uint8_t* wrow = a.W + (size_t)row * (a.d >> 1);
+  const uint16_t* srow = a.s + (size_t)row * (ng >> GSH);
+  // thread's pieces of x: piece tid % 64 of tokens tid / 64 + 8 i
+  const int piece = threadIdx.x & (kCols / 8 - 1), tok0 = threadIdx.x / (kCols / 8);
+  constexpr int kStep = kThreads / (kCols / 8);
+  Raw<16> xv[kPass];
+  auto load_x = [&](int blk) {
+    const int col = min(blk * kCols + piece * 8, a.d - 8);
+#pragma unroll
+    for (int i = 0; i < kPass; ++i)
+      xv[i] = load_raw<16>(a.x + (size_t)min(tok0 + kStep * i, a.B - 1) * a.ldx + (size_t)col * 2);
+  };
+  auto store_x = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kPass; ++i)
+      *reinterpret_cast<Raw<16>*>(sh + buf * kX + (tok0 + kStep * i) * kRow + piece * 16) = lin_order(xv[i]);
+  };
+  LinChunk<GSH> w[kAhead];
+  auto load_w = [&](int blk, LinChunk<GSH>& to) {
+    const int ck = blk * kChunks + kc;
+    if (4 * ck < ng) lin_load<GSH>(wrow, srow, ck, c, ng, to);
+  };
+  load_x(0);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load_w(u, w[u]);
+  int xoff[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) xoff[t] = min(16 * t + m, a.B - 1) * kRow + kc * 256 + c * 16;
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+  const Q4<T> dec;
+  const Raw<16> m24 = lin_offset<T>();
+  store_x(0);
+  if (nblock > 1) load_x(1);
+  __syncthreads();
+  for (int blk0 = 0; blk0 < nblock; blk0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int blk = blk0 + u;
+      if (blk < nblock) {
+        if (blk + 1 < nblock) store_x((u + 1) & 1);
+        // x before the weights: loads are waited for in their order, and x is needed first
+        if (blk + 2 < nblock) load_x(blk + 2);
+        const LinChunk<GSH> now = w[u];
+        load_w(blk + kAhead, w[u]);
+        const uint8_t* xrow[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xrow[t] = sh + (u & 1) * kX + xoff[t];
+        const int groups = ng - 4 * (blk * kChunks + kc);
+        if (groups >= 4) lin_chunk<T, NT, GSH>(now, xrow, 4, dec, m24, acc);
+        else lin_chunk<T, NT, GSH>(now, xrow, groups, dec, m24, acc);
+        __syncthreads();
+      }
+    }
+  }
+  lin_finish<NT, 4, kChunks, 2>(a, (float*)sh, row0, kc, rg, m, c, acc);
 }
 
 constexpr int kLinXLds = 64 << 10;       // x is kept whole in LDS up to here: two workgroups per compute unit
@@ -370,18 +440,23 @@ hipError_t lin_run(hipStream_t s, const LinearArgs& a, int gsh) {
   else k_linear_q4<T, NI, 2><<<grid, blk, lds, s>>>(a);
   return hipGetLastError();
 }
-template <class T, int NT, int R>
+template <class T, int NT>
 hipError_t lin_run_wide(hipStream_t s, const LinearArgs& a, int gsh) {
-  const dim3 grid((a.n + 16 * R - 1) / (16 * R)), blk(kLinWaves * kWave);
-  if (gsh == 0) k_linear_q4_wide<T, NT, R, 0><<<grid, blk, 0, s>>>(a);
-  else if (gsh == 1) k_linear_q4_wide<T, NT, R, 1><<<grid, blk, 0, s>>>(a);
-  else k_linear_q4_wide<T, NT, R, 2><<<grid, blk, 0, s>>>(a);
+  const dim3 grid((a.n + 15) / 16), blk(kLinWaves * kWave);
+  if (gsh == 0) k_linear_q4_wide<T, NT, 0><<<grid, blk, 0, s>>>(a);
+  else if (gsh == 1) k_linear_q4_wide<T, NT, 1><<<grid, blk, 0, s>>>(a);
+  else k_linear_q4_wide<T, NT, 2><<<grid, blk, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <class T, int NT>
+hipError_t lin_run_rows(hipStream_t s, const LinearArgs& a, int gsh) {
+  const dim3 grid((a.n + 31) / 32), blk(kLinWaves * kWave);
+  if (gsh == 0) k_linear_q4_rows<T, NT, 0><<<grid, blk, 0, s>>>(a);
+  else if (gsh == 1) k_linear_q4_rows<T, NT, 1><<<grid, blk, 0, s>>>(a);
+  else k_linear_q4_rows<T, NT, 2><<<grid, blk, 0, s>>>(a);
   return hipGetLastError();
 }
 
-#ifndef LR
-#define LR 8192
-#endif
 template <class T>
 hipError_t lin_launch(hipStream_t s, const LinearArgs& a, int gsh) {
   if (a.B <= 16 && (size_t)a.B * (a.d * 2 + 16) <= (size_t)kLinXLds) {
@@ -389,12 +464,14 @@ hipError_t lin_launch(hipStream_t s, const LinearArgs& a, int gsh) {
     if (a.B <= 8) return lin_run<T, 2>(s, a, gsh);
     return lin_run<T, 4>(s, a, gsh);
   }
-  // two row tiles per wave halve the reads of x; one leaves enough workgroups for few rows
-  const bool two = a.n >= LR;
-  if (a.B <= 16) return two ? lin_run_wide<T, 1, 2>(s, a, gsh) : lin_run_wide<T, 1, 1>(s, a, gsh);
-  if (a.B <= 32) return two ? lin_run_wide<T, 2, 2>(s, a, gsh) : lin_run_wide<T, 2, 1>(s, a, gsh);
-  if (a.B <= 48) return two ? lin_run_wide<T, 3, 2>(s, a, gsh) : lin_run_wide<T, 3, 1>(s, a, gsh);
-  return two ? lin_run_wide<T, 4, 2>(s, a, gsh) : lin_run_wide<T, 4, 1>(s, a, gsh);
+  // 16 rows per workgroup leave enough workgroups for few rows; above one per compute unit,
+  // workgroups of 32 rows read x half as often (64 tokens: 4096 x 4096 14.4 us with 16 rows and
+  // 16.7 with 32; 48 tokens: 6144 x 4096 20.6 and 13.5; 37: 8192 x 8192 38.2 and 24.1)
+  const bool two = a.n > 16 * 256;
+  if (a.B <= 16) return two ? lin_run_rows<T, 1>(s, a, gsh) : lin_run_wide<T, 1>(s, a, gsh);
+  if (a.B <= 32) return two ? lin_run_rows<T, 2>(s, a, gsh) : lin_run_wide<T, 2>(s, a, gsh);
+  if (a.B <= 48) return two ? lin_run_rows<T, 3>(s, a, gsh) : lin_run_wide<T, 3>(s, a, gsh);
+  return two ? lin_run_rows<T, 4>(s, a, gsh) : lin_run_wide<T, 4>(s, a, gsh);
 }
 
 }  // namespace
