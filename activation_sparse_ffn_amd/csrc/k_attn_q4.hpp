@@ -14,6 +14,16 @@
 //   output   codes times scale, rounded once to fp16, as rows of 16 dims x 32 positions.
 // The reference is raised only when a score passes it by 6 (in powers of two), so P stays
 // below 2^15; the 2^9 keeps weights down to 2^-33 of the largest above fp16's last bit.
+//
+// Bound by reading the cache (D + D / 8 bytes per position and kv head, keys and values
+// together); the codes' way into matrix operands is the second load (331 vector operations
+// per wave and tile of 32 positions at D = 128, 45% of the time at 131072 positions).  The
+// cache is copied into LDS without passing through registers, so a wave holds only what it
+// works on and four waves fit a SIMD.  131072 positions x 8 kv heads, step by step: two tiles in
+// registers, the last workgroup joining behind a cache invalidation, 66 us; through LDS, joined
+// without the invalidation, 45; joined by a kernel of its own, 41 (35.0, 4.3 TB/s, and 4.7).
+// 64 sequences of up to 4096 x 8 kv heads of 64: 29 us, of which lengths that differ between
+// the workgroups of a compute unit cost about a third.
 #pragma once
 #include "sfx_kv.hpp"
 #include "sfx_launch.hpp"

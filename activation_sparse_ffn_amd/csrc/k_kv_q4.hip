@@ -8,6 +8,12 @@
 // (the products are exact there) and rounded once to fp32: a quotient next to a rounding
 // border then falls the same way wherever it is computed.  max / 7 and k' / s are
 // correctly rounded fp32 quotients.
+//
+// Both are bound by the 16- or 32-bit rows they read or write.  Measured (one MI355X): 4095
+// tokens of 64 query and 8 kv heads of 128, bf16: append 45 us for 155 MB, of which the 64-bit
+// rotation costs 2.4; one head per wave and token, each lane two dims, took 107, bound by the
+// chain from position to page to data.  Reading 16384 positions of 8 heads of 128 back: 19 us
+// for 86 MB (34 with a wave per head and token).  Eight tokens: 4.2 and 2.2 us, launch latency.
 #include <type_traits>
 
 #include "sfx_kv.hpp"

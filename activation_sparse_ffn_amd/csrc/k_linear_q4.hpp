@@ -10,8 +10,8 @@
 //   wide, rows   x in blocks, 16 or 32 rows per workgroup: each workgroup reads all of x, from
 //                L2, and writes it to LDS; from about 16 tokens on that and the decoding
 //                weigh more than the codes.
-// Measured (one MI355X): 1 x 28672 x 7168, scales per 128: 27.5 us = 3.9 TB/s of 106 MB; 1 x 4096
-// x 4096: 5.8 us; 37 x 8192 x 8192, scales per 64: 24.1 us against 7.1 for its 38.7 MB (VALU 34%
+// Measured (one MI355X): 1 x 28672 x 7168, scales per 128: 25.6 us = 4.1 TB/s of 106 MB; 1 x 4096
+// x 4096: 5.3 us; 37 x 8192 x 8192, scales per 64: 24.1 us against 7.1 for its 38.7 MB (VALU 28%
 // of the time busy, MFMA 16%).
 #pragma once
 #include "sfx_launch.hpp"

@@ -492,8 +492,9 @@ int sfx_ffn_pipeline(void* stream, int wdt, int act, int B, int d, int h, int f,
  *   y         [B] rows of n fp32, ldy elements apart (4-byte aligned).
  * B 1..64, n and d up to 2^24.  Products of a code and x are exact; a group's sum and
  * the sum over groups are fp32, in an order fixed by the shape: y is bitwise
- * reproducible.  Neither infinities nor NaN in x stay confined to finite results:
- * they give a non-finite y for their token only.
+ * reproducible.  An infinity or a NaN in a token's x makes that token's y non-finite
+ * (NaN also where the product with an infinity would be an infinity) and no other's.
+ * No workspace.
  * ------------------------------------------------------------------------------- */
 int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const void* x, size_t ldx,
                   const void* W, const void* W_scales, const float* bias, int accumulate,
@@ -550,9 +551,9 @@ int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const v
  *             logarithm of the sum of exp(scale q . k_p), to join with other positions.
  *   ws        >= sfx_attn_q4_ws(B, Hq, Hkv, D, max_pages * page) bytes.
  * Several query tokens of one sequence (drafted tokens) are rows with the same table
- * entries and their own lens.  Sums are fp32; a weight and a dequantised value are each
- * rounded once to fp16 (weights relative to the largest, down to 2^-33 of it).  Results
- * are bitwise reproducible for the same shapes and lens.
+ * entries and their own lens.  Scores and sums are fp32; a dequantised value is rounded
+ * once to fp16, a weight to one fp16 term (bf16 results) or two (fp16 results), down to
+ * 2^-33 of the largest.  Results are bitwise reproducible for the same shapes and lens.
  * ------------------------------------------------------------------------------- */
 size_t sfx_kv_cache_bytes(int Hkv, int D, int page, int num_pages);
 int sfx_kv_append_q4(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int D,
