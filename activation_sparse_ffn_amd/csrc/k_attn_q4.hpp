@@ -109,6 +109,7 @@ __device__ __forceinline__ int attn_ids(const KvCache& kv, int b, int it, int W,
 template <int NG, int NP>
 __device__ __forceinline__ void attn_copy(const KvCache& kv, int h, int it, int ids, int at, uint8_t* dst, int lane) {
   using P = AttnPieces<NG, NP>;
+  memory_order();                                              // tiles are waited for in this order
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int pos = it * kAttnTile + p * (kAttnTile / NP);

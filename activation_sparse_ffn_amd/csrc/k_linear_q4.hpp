@@ -216,11 +216,13 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
   LinScales<GSH> sc[kLinSlots];
   auto fetch = [&](int i, int slot, LinScales<GSH>& s) {
     const int unit = wave + i * kLinWaves;
+    memory_order();                                            // units are waited for in this order
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       __builtin_amdgcn_global_load_lds((const void*)(from[k] + (size_t)min(8 * unit + piece[k], ng - 1) * 16),
                                        (__attribute__((address_space(3))) void*)(ring[wave][slot] + k * 1024), 16, 0, 0);
     s = lin_scales<GSH>(srow, unit, ng);
+    memory_order();
   };
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -96,6 +96,9 @@ __device__ __forceinline__ void quarter_transpose(uint32_t (&w)[4]) {
   w[3] = d[1];
 }
 
+// Keeps the memory operations before it before those after it in program order: a wait that
+// counts the younger operations is only right if groups of them are issued in their order.
+__device__ __forceinline__ void memory_order() { asm volatile("" ::: "memory"); }
 // Waits of a wave for its own copies into LDS (all but the N youngest memory operations) and
 // for its own LDS reads; the compiler moves no memory access across them.
 template <int N>

@@ -549,7 +549,9 @@ int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const v
  *             included, does not matter.
  *   out       [B][Hq][D] in qdt, dense, written.   lse [B][Hq] fp32 or NULL: the natural
  *             logarithm of the sum of exp(scale q . k_p), to join with other positions.
- *   ws        >= sfx_attn_q4_ws(B, Hq, Hkv, D, max_pages * page) bytes.
+ *   ws        >= sfx_attn_q4_ws(B, Hq, Hkv, D, max_pages * page) bytes, any contents.  Few
+ *             sequences are cut into more runs, so a smaller B can need more: a workspace
+ *             used with several B has the largest size that any of them needs.
  * Several query tokens of one sequence (drafted tokens) are rows with the same table
  * entries and their own lens.  Scores and sums are fp32; a dequantised value is rounded
  * once to fp16, a weight to one fp16 term (bf16 results) or two (fp16 results), down to
