@@ -22,8 +22,8 @@
 // works on and four waves fit a SIMD.  131072 positions x 8 kv heads, step by step: two tiles in
 // registers, the last workgroup joining behind a cache invalidation, 66 us; through LDS, joined
 // without the invalidation, 45; joined by a kernel of its own, 41 (35.0, 4.3 TB/s, and 4.7).
-// 64 sequences of up to 4096 x 8 kv heads of 64: 29 us, of which lengths that differ between
-// the workgroups of a compute unit cost about a third.
+// 64 sequences of up to 4096 x 8 kv heads of 64: 27 us, with sequences of different lengths paired
+// on a compute unit (31 in the caller's order).
 #pragma once
 #include "sfx_kv.hpp"
 #include "sfx_launch.hpp"
@@ -33,6 +33,8 @@ namespace sfx {
 namespace {
 
 constexpr int kAttnTile = 32;          // positions a wave takes at a time
+constexpr int kAttnUnits = 256;        // compute units
+constexpr int kAttnOrder = 1024;       // positions of a table from which sequences are ordered
 constexpr float kRefMin = -3.0e38f;
 // Waves of a workgroup and tiles of LDS per wave: two workgroups fit a compute unit's 160 KB,
 // and a wave always has a tile or more on the way while it works on one.
@@ -49,6 +51,7 @@ struct AttnArgs {
   float* parts;             // [B][Hkv][head tiles][S] x ([HG][D] sums, [HG][2] reference and weight sum)
   float k2;                 // scale log2(e)
   int Hq, G, HT, HG, S;     // HG = heads of a full head tile, min(G, 16)
+  int pass;                 // attn_sequence; 0: sequences in their order
 };
 
 template <int N>
@@ -249,15 +252,57 @@ __device__ __forceinline__ float attn_lse(float ref, float sum) {
 struct AttnSpan {
   int start, end, t0, ntile, per, active;
 };
-__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int b, int W) {
+__device__ __forceinline__ int attn_start(const AttnArgs& a, int b) { return a.starts ? max(a.starts[b], 0) : 0; }
+__device__ __forceinline__ int attn_end(const AttnArgs& a, int b) {
+  return min(a.lens[b], a.kv.max_pages << a.kv.page_shift);
+}
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int start, int end, int W) {
   AttnSpan s;
-  s.end = min(a.lens[b], a.kv.max_pages << a.kv.page_shift);
-  s.start = a.starts ? max(a.starts[b], 0) : 0;
+  s.end = end;
+  s.start = start;
   s.t0 = s.start / kAttnTile;
   s.ntile = s.end > s.start ? (s.end + kAttnTile - 1) / kAttnTile - s.t0 : 0;
   s.per = max(W, (s.ntile + a.S - 1) / a.S);
   s.active = max(1, (s.ntile + s.per - 1) / s.per);            // an empty sequence has one: its zero row
   return s;
+}
+
+// The sequence that launch position z works on, and its span.  Workgroups are handed out in
+// order, so with two to a compute unit positions z and z + pass share one: the first `pass`
+// positions take the longest sequences, longest first, the others the rest, shortest first.
+// Ranks by counting (equal lengths by index); at most 64 sequences, one to a lane, each wave
+// counting a share of them.  Lengths spread evenly up to 4096, 64 sequences x 8 kv heads of
+// 64: 31.3 us in their order, 27.6 so; up to 2048 of 128: 26.3 and 22.8.  It costs 0.5 us: all
+// 64 of 1500 positions 30.1 and 30.7; up to 600 positions 11.8 and 11.6, up to 300 8.8 and 9.7.
+// Behind more than 512 workgroups the next one starts where one has ended, and the order
+// gains nothing (1024: 19.2 in their order, 21.5 so).
+template <int W>
+__device__ __forceinline__ int attn_sequence(const AttnArgs& a, uint8_t (&count)[W][kWave], int wave, int lane,
+                                             int& start, int& end) {
+  const int B = a.kv.B, z = blockIdx.z;
+  if (a.pass == 0) {
+    start = attn_start(a, z);
+    end = attn_end(a, z);
+    return z;
+  }
+  const int from = lane < B ? attn_start(a, lane) : 0, to = lane < B ? attn_end(a, lane) : 0;
+  const int len = lane >= B ? -1 : to > from ? to - from : 0;
+  int more = 0;
+#pragma unroll
+  for (int i = 0; i < kWave / W; ++i) {
+    const int j = wave * (kWave / W) + i, other = __builtin_amdgcn_readlane(len, j);
+    more += other > len || (other == len && j < lane);
+  }
+  count[wave][lane] = (uint8_t)more;
+  __syncthreads();
+  int rank = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) rank += count[w][lane];
+  const int want = z < a.pass ? z : B - 1 - (z - a.pass);
+  const int b = __builtin_ctzll(__ballot(rank == want));       // ranks are 0..63, each once
+  start = __builtin_amdgcn_readlane(from, b);
+  end = __builtin_amdgcn_readlane(to, b);
+  return b;
 }
 
 // The tiles of one wave: tb + wave, then every W-th.
@@ -317,13 +362,16 @@ __global__ __launch_bounds__(attn_waves(NG) * kWave, NG <= 4 ? 4 : 2) void k_att
   constexpr int W = attn_waves(NG), D = 32 * NG, kThreads = W * kWave;
   constexpr int kRing = W * attn_slots(NG) * (kAttnTile / 8) * 9 * D, kJoin = W * 16 * (D + 4) * 4;
   __shared__ float sh_ref[W][16], sh_sum[W][16];
+  __shared__ uint8_t sh_count[W][kWave];
   __shared__ __attribute__((aligned(16))) uint8_t sh_mem[kRing > kJoin ? kRing : kJoin];
   float* sh_acc = (float*)sh_mem;
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, c = lane >> 4;
-  const int split = blockIdx.x, ht = blockIdx.y % a.HT, h = blockIdx.y / a.HT, b = blockIdx.z;
+  const int split = blockIdx.x, ht = blockIdx.y % a.HT, h = blockIdx.y / a.HT;
   const int heads = min(16, a.G - 16 * ht);                    // query heads of this workgroup
-  const AttnSpan sp = attn_span(a, b, W);
+  int start, end;
+  const int b = attn_sequence<W>(a, sh_count, wave, lane, start, end);
+  const AttnSpan sp = attn_span(a, start, end, W);
   const int active = sp.active;
   if (split >= active) return;
   const int tb = sp.t0 + split * sp.per, te = min(sp.t0 + sp.ntile, tb + sp.per);
@@ -391,7 +439,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int W = attn_waves(NG), D = 32 * NG, kItems = D / 4, kGroups = 256 / kItems;
   __shared__ __attribute__((aligned(16))) float sh_v[kGroups][D];
   __shared__ float sh_l[kGroups], sh_r[kGroups];
-  const AttnSpan sp = attn_span(a, blockIdx.y, W);
+  const AttnSpan sp = attn_span(a, attn_start(a, blockIdx.y), attn_end(a, blockIdx.y), W);
   if (sp.active == 1) return;                                   // the attention kernel wrote the row
   const int hq = blockIdx.x, h = hq / a.G, ht = (hq % a.G) / 16, hd = (hq % a.G) % 16, b = blockIdx.y;
   const size_t run = (size_t)a.HG * (D + 4);
@@ -443,7 +491,10 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 }
 
 template <class T, int NG>
-hipError_t attn_run(hipStream_t s, const AttnArgs& a) {
+hipError_t attn_run(hipStream_t s, AttnArgs a) {
+  const int each = a.S * a.kv.Hkv * a.HT, all = each * a.kv.B;  // workgroups of a sequence, of the call
+  const bool order = all > kAttnUnits && all <= 2 * kAttnUnits && a.kv.max_pages << a.kv.page_shift >= kAttnOrder;
+  a.pass = order ? kAttnUnits / each : 0;
   k_attn_q4<T, NG><<<dim3(a.S, a.kv.Hkv * a.HT, a.kv.B), dim3(attn_waves(NG) * kWave), 0, s>>>(a);
   if (a.S > 1) k_attn_join<T, NG><<<dim3(a.Hq, a.kv.B), dim3(256), 0, s>>>(a);
   return hipGetLastError();

@@ -598,6 +598,61 @@ def test_attention_largest_batch():
     check_attn(q, kv, lens, None, D ** -0.5, "f16", out, lse)
 
 
+@pytest.mark.parametrize("case", [  # B, Hq, Hkv, D, page, longest: 258, 512, 512, 510, 512 workgroups
+    (43, 51, 3, 32, 8, 1100), (64, 16, 8, 64, 16, 1030), (32, 8, 8, 64, 16, 2100), (3, 170, 170, 32, 64, 1024),
+    (16, 32, 32, 256, 32, 1050)], ids=lambda c: "-".join(map(str, c)))
+def test_attention_order_of_sequences(case):
+    """Batches whose sequences the kernel orders by length: ties, empty ones, windows, and any
+    order of the caller's gives each sequence the same bits."""
+    B, Hq, Hkv, D, page, longest = case
+    say(f"attention order {case}")
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(0, 40, B)]
+    lens[B // 2] = longest
+    lens[1] = lens[0]
+    q, cache, table, kv = make_attn(B, Hq, Hkv, D, page, lens, "bf16", B + D)
+    ws = A.workspace(A.sfx_attn_q4_ws(B, Hq, Hkv, D, table.shape[1] * page))
+    qd, d_lens = q.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for starts in (None, [int(n) for n in rng.integers(-5, 45, B)]):
+        d_starts = None if starts is None else torch.tensor(starts, dtype=torch.int32, device=DEV)
+        out = torch.full((B, Hq, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((B, Hq), float("nan"), device=DEV)
+        A.sfx_attn_q4(qd, cache, table, d_lens, out, ws, starts=d_starts, lse=lse)
+        check_attn(q, kv, lens, starts, D ** -0.5, "bf16", out, lse)
+        perm = torch.from_numpy(rng.permutation(B)).to(DEV)
+        out2, lse2 = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
+        A.sfx_attn_q4(qd[perm].contiguous(), cache, table[perm].contiguous(), d_lens[perm].contiguous(), out2, ws,
+                      starts=None if starts is None else d_starts[perm].contiguous(), lse=lse2)
+        assert torch.equal(out2, out[perm]) and torch.equal(lse2, lse[perm])
+    # lengths and starts at the ends of their type: clamped, nothing to attend to
+    ends = torch.tensor([[-2 ** 31, 2 ** 31 - 1], [2 ** 31 - 1, 2 ** 31 - 1], [-1, -2 ** 31]], dtype=torch.int32, device=DEV)
+    d_lens[:3], d_starts = ends[:, 0], torch.zeros_like(d_lens)
+    d_starts[:3] = ends[:, 1]
+    A.sfx_attn_q4(qd, cache, table, d_lens, out, ws, starts=d_starts, lse=lse)
+    assert (out[:3] == 0).all() and torch.isneginf(lse[:3]).all()
+    if B > 3:
+        check_attn(q[3:], kv[3:], lens[3:], None, D ** -0.5, "bf16", out[3:], lse[3:])
+
+
+def test_attention_bad_query_stays_alone():
+    """A NaN or an infinity in one head's query: the other heads and sequences keep their bits."""
+    B, Hq, Hkv, D, lens = 4, 16, 2, 64, [300, 40, 700, 5]
+    q, cache, table, _ = make_attn(B, Hq, Hkv, D, 16, lens, "f16", 5)
+    ws = A.workspace(A.sfx_attn_q4_ws(B, Hq, Hkv, D, table.shape[1] * 16))
+    d_lens, qd = torch.tensor(lens, dtype=torch.int32, device=DEV), q.to(DEV)
+    out = torch.empty(B, Hq, D, dtype=torch.float16, device=DEV)
+    A.sfx_attn_q4(qd, cache, table, d_lens, out, ws)
+    bad = torch.zeros(B, Hq, dtype=torch.bool, device=DEV)
+    for b, h, value in ((0, 3, float("nan")), (2, 8, float("inf")), (1, 15, float("-inf"))):
+        say(f"attention with {value} in query {b}, {h}")
+        qd[b, h, 7] = value
+        bad[b, h] = True
+    out2 = torch.empty_like(out)
+    A.sfx_attn_q4(qd, cache, table, d_lens, out2, ws)
+    assert torch.equal(out2[~bad], out[~bad])
+    assert not torch.isfinite(out2[bad]).any()                 # of 40 keys some have either sign
+
+
 def test_shared_pages_and_drafted_tokens():
     """Two sequences whose tables share a prefix, and several query tokens of one sequence as
     rows with the same pages and their own lens."""
