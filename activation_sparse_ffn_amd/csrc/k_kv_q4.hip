@@ -14,6 +14,7 @@
 // rotation costs 2.4; one head per wave and token, each lane two dims, took 107, bound by the
 // chain from position to page to data.  Reading 16384 positions of 8 heads of 128 back: 19 us
 // for 86 MB (34 with a wave per head and token).  Eight tokens: 4.2 and 2.2 us, launch latency.
+#include <algorithm>
 #include <type_traits>
 
 #include "sfx_kv.hpp"
@@ -322,11 +323,15 @@ KvCache make_cache(const KvGeom& g, const void* cache, const int32_t* table) {
   return KvCache{(uint8_t*)cache, table, g.Hkv, g.D, g.page_shift, g.num_pages, g.max_pages, g.B};
 }
 
+// Workgroups in x: the mapping to tokens permutes each 64 of them and leaves the last of the 64
+// in its place, so the one that would be workgroup kKvMaxTokens stands for no token of a call.
+int token_groups(int T) { return std::min((T + 63) / 64 * 64, kKvMaxTokens); }
+
 template <int DT, int QDT, bool VEC>
 void run_append(hipStream_t s, const AppendArgs& a) {
   const int heads = kBlock / (a.kv.D >> 3);
   const auto columns = [&](int hp, int n) { return (n + heads * hp - 1) / (heads * hp); };
-  const int tokens = (a.T + 63) / 64 * 64;
+  const int tokens = token_groups(a.T);
   // four heads to a thread where that leaves four workgroups per compute unit
   if ((long long)a.T * (columns(4, a.Hq) + columns(4, a.kv.Hkv)) >= 1024) {
     const int qc = columns(4, a.Hq);
@@ -344,7 +349,7 @@ void run_append(hipStream_t s, const AppendArgs& a, int qdt, bool vec) {
 
 template <int DT>
 void run_read(hipStream_t s, const ReadArgs& a) {
-  const int heads = kBlock / (a.kv.D >> 3), tokens = (a.T + 63) / 64 * 64;
+  const int heads = kBlock / (a.kv.D >> 3), tokens = token_groups(a.T);
   const auto columns = [&](int hp) { return (a.kv.Hkv + heads * hp - 1) / (heads * hp); };
   if (a.kv.Hkv >= 2 * heads && (long long)a.T * columns(2) >= 1024)
     k_kv_read<DT, 2><<<dim3(tokens, columns(2)), dim3(kBlock), 0, s>>>(a);

@@ -89,7 +89,6 @@ int kv_geom(int B, int Hkv, int D, int page, int num_pages, int max_pages, sfx::
   *g = sfx::KvGeom{B, Hkv, D, __builtin_ctz((unsigned)page), num_pages, max_pages};
   return SFX_OK;
 }
-constexpr int kKvMaxTokens = (1 << 24) - 1;   // one workgroup column of 256 threads per token
 
 }  // namespace
 
@@ -438,7 +437,7 @@ int sfx_kv_append_q4(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int
   sfx::KvGeom g;
   const int st = kv_geom(B, Hkv, D, page, num_pages, max_pages, &g);
   if (st != SFX_OK) return st;
-  if (T < 1 || T > kKvMaxTokens) return SFX_E_SHAPE;
+  if (T < 1 || T > sfx::kKvMaxTokens) return SFX_E_SHAPE;
   if (q && (Hq < 1 || Hq > sfx::kAttnMaxHeads || ldq < (size_t)Hq * D)) return SFX_E_SHAPE;
   if (ldk < (size_t)Hkv * D || ldv < (size_t)Hkv * D) return SFX_E_SHAPE;
   if (cos_sin && (rot < 2 || rot > D || rot % 2 != 0 || max_pos < 1)) return SFX_E_SHAPE;
@@ -458,7 +457,7 @@ int sfx_kv_read_q4(void* stream, int odt, int T, int Hkv, int D, const int32_t* 
   sfx::KvGeom g;
   const int st = kv_geom(B, Hkv, D, page, num_pages, max_pages, &g);
   if (st != SFX_OK) return st;
-  if (T < 1 || T > kKvMaxTokens) return SFX_E_SHAPE;
+  if (T < 1 || T > sfx::kKvMaxTokens) return SFX_E_SHAPE;
   if (!pos || !table || !cache || !k || !v) return SFX_E_NULL;
   if (!aligned16(cache) || !aligned16(k) || !aligned16(v)) return SFX_E_ALIGN;
   if (!aligned4(pos) || !aligned4(table) || (seq && !aligned4(seq))) return SFX_E_ALIGN;

@@ -82,7 +82,9 @@ hipError_t launch_linear_q4_bf16(hipStream_t s, int gsh, int B, int n, int d, co
                                  const void* W, const void* Ws, const float* bias, int accumulate, float* y,
                                  size_t ldy);
 
-// Paged int4 key/value cache.
+// Paged int4 key/value cache.  Tokens of a call: one workgroup column of 256 threads per token,
+// and a launch holds fewer than 2^32 threads in x.
+constexpr int kKvMaxTokens = (1 << 24) - 1;
 struct KvGeom {
   int B, Hkv, D, page_shift, num_pages, max_pages;
 };
