@@ -49,7 +49,7 @@ struct AttnArgs {
   uint8_t* out;             // [B][Hq][D] 16 bit
   float* lse;               // [B][Hq] or null
   float* parts;             // [B][Hkv][head tiles][S] x ([HG][D] sums, [HG][2] reference and weight sum)
-  float k2;                 // scale log2(e)
+  float k2;                 // scale log2(e), times the unit of the decoded codes
   int Hq, G, HT, HG, S;     // HG = heads of a full head tile, min(G, 16)
   int pass;                 // attn_sequence; 0: sequences in their order
 };
@@ -501,7 +501,8 @@ hipError_t attn_run(hipStream_t s, AttnArgs a) {
 }
 
 template <class T>
-hipError_t attn_launch(hipStream_t s, const AttnArgs& a) {
+hipError_t attn_launch(hipStream_t s, AttnArgs a) {
+  a.k2 *= Q4<T>::unit;
   switch (a.kv.D >> 5) {
     case 1: return attn_run<T, 1>(s, a);
     case 2: return attn_run<T, 2>(s, a);

@@ -123,7 +123,7 @@ __device__ __forceinline__ void lin_chunk(const LinChunk<GSH>& w, const uint8_t*
 }
 
 // The waves' sums in wave order, bias, y.  RG groups of W waves, 16 rows from row0 on each.
-template <int NT, int NI, int W, int RG>
+template <class T, int NT, int NI, int W, int RG>
 __device__ __forceinline__ void lin_finish(const LinearArgs& a, float* red, int row0, int wave, int rg, int m, int c,
                                            const float (&acc)[NT][NI]) {
   constexpr int TT = 4 * NI * NT;
@@ -139,6 +139,7 @@ __device__ __forceinline__ void lin_finish(const LinearArgs& a, float* red, int 
       float v = 0.f;
 #pragma unroll
       for (int k = 0; k < W; ++k) v += red[(k * 16 + row) * (TT + 1) + tok];
+      v *= Q4<T>::unit;
       if (a.bias) v += a.bias[row0 + row];
       float* y = a.y + (size_t)tok * a.ldy + row0 + row;
       *y = a.accumulate ? *y + v : v;
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
     }
   }
   __syncthreads();
-  lin_finish<1, NI, kLinWaves, 1>(a, (float*)&ring[0][0][0], row0, wave, 0, m, c, acc);
+  lin_finish<T, 1, NI, kLinWaves, 1>(a, (float*)&ring[0][0][0], row0, wave, 0, m, c, acc);
 }
 
 // More tokens, or long rows: x passes through LDS in blocks of 1024 columns, a chunk of 128
@@ -351,7 +352,7 @@ __global__ __launch_bounds__(kLinWaves * kWave, NT <= 2 ? 4 : 2) void k_linear_q
       }
     }
   }
-  lin_finish<NT, 4, kLinWaves, 1>(a, (float*)sh, row0, wave, 0, m, c, acc);
+  lin_finish<T, NT, 4, kLinWaves, 1>(a, (float*)sh, row0, wave, 0, m, c, acc);
 }
 
 // Many weight rows: two groups of four waves, 16 rows each, over blocks of 512 columns.  Two
@@ -428,7 +429,7 @@ __global__ __launch_bounds__(kLinWaves * kWave, 2) void k_linear_q4_rows(LinearA
       }
     }
   }
-  lin_finish<NT, 4, kChunks, 2>(a, (float*)sh, row0, kc, rg, m, c, acc);
+  lin_finish<T, NT, 4, kChunks, 2>(a, (float*)sh, row0, kc, rg, m, c, acc);
 }
 
 constexpr int kLinXLds = 64 << 10;       // x is kept whole in LDS up to here: two workgroups per compute unit

@@ -479,7 +479,7 @@ int sfx_attn_q4(void* stream, int qdt, int B, int Hq, int Hkv, int D, const void
   const int st = kv_geom(B, Hkv, D, page, num_pages, max_pages, &g);
   if (st != SFX_OK) return st;
   if (B > SFX_MAX_B || Hq < 1 || Hq > sfx::kAttnMaxHeads || Hq % Hkv != 0 || ldq < (size_t)Hq * D) return SFX_E_SHAPE;
-  if (!(scale > -INFINITY && scale < INFINITY)) return SFX_E_SHAPE;
+  if (!(fabsf(scale) < 0x1p115f)) return SFX_E_SHAPE;           // times 2^12 log2(e) (sfx_q4.hpp) it is finite
   if (!q || !table || !cache || !lens || !out) return SFX_E_NULL;
   if (!aligned16(q) || ldq % 8 != 0 || !aligned16(cache) || !aligned16(out)) return SFX_E_ALIGN;
   if (!aligned4(table) || !aligned4(lens) || (starts && !aligned4(starts)) || (lse && !aligned4(lse))) return SFX_E_ALIGN;

@@ -8,8 +8,12 @@
 //   bf16  has no packed addition.  All four nibble positions are shifted to base 16 and the
 //         24 = 16 + 8 is taken back by the matrix cores: the accumulator starts at
 //         -24 sum(x), a product of x with a constant operand.  sum (16 + u) x - 24 sum x =
-//         sum q x, with exact products and fp32 sums of one group of 32 at a time; the
+//         sum q x, with exact products and fp32 sums of one scale group at a time; the
 //         summed terms are at most 31 |x| instead of 8 |x|, about 2 of an fp32 sum's 24 bits.
+//         Both operands are 2^-12 of these numbers (the exponent of the base is free): 24
+//         sum |x| over 128 columns is then below the largest |x|, so no finite x makes the
+//         sums of a group overflow.  What is summed from them is multiplied by 2^12 (unit)
+//         in the end; powers of two change no bit of it.
 // The scale of a group multiplies its fp32 sum.
 //
 // The masks and bases are kept in registers behind empty asm statements: as literals, two of
@@ -39,6 +43,7 @@ struct Q4;
 template <>
 struct Q4<TF16> {
   static constexpr bool offset = false;
+  static constexpr float unit = 1.f;
   uint32_t m0, m1, o0, o1, d0, d1;
   __device__ __forceinline__ Q4()
       : m0(scalar_const(0x000F000Fu)), m1(scalar_const(0x00F000F0u)), o0(vector_const(0x64006400u)),
@@ -56,9 +61,10 @@ struct Q4<TF16> {
 };
 template <>
 struct Q4<TBF16> {
-  static constexpr bool offset = true;       // word() gives 24 + q
+  static constexpr bool offset = true;       // word() gives (24 + q) / unit
+  static constexpr float unit = 4096.f;
   uint32_t m, o;
-  __device__ __forceinline__ Q4() : m(scalar_const(0x00780078u)), o(vector_const(0x41804180u)) {}
+  __device__ __forceinline__ Q4() : m(scalar_const(0x00780078u)), o(vector_const(0x3B803B80u)) {}
   __device__ __forceinline__ Raw<16> word(uint32_t v) const {
     Raw<16> r;
     r.w[0] = ((v << 3) & m) | o;
@@ -70,7 +76,7 @@ struct Q4<TBF16> {
   // Written anew at each call: a product of it with something fixed is not kept in
   // registers across a loop.
   __device__ __forceinline__ static Raw<16> minus24() {
-    uint32_t k = 0xC1C0C1C0u;
+    uint32_t k = 0xBBC0BBC0u;
     asm volatile("" : "+v"(k));
     Raw<16> r;
     r.w[0] = r.w[1] = r.w[2] = r.w[3] = k;

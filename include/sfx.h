@@ -491,9 +491,13 @@ int sfx_ffn_pipeline(void* stream, int wdt, int act, int B, int d, int h, int f,
  *   accumulate  0: y is overwritten; otherwise the product is added to it.
  *   y         [B] rows of n fp32, ldy elements apart (4-byte aligned).
  * B 1..64, n and d up to 2^24.  Products of a code and x are exact; a group's sum and
- * the sum over groups are fp32, in an order fixed by the shape: y is bitwise
+ * the sum over groups are fp32, in an order fixed by the shape.  With bf16 x a group's sum
+ * runs over (24 + q) x - 24 x: its roundings are relative to 31 |x|, also where a column's
+ * code is 0, instead of |q x|.  y is bitwise
  * reproducible.  An infinity or a NaN in a token's x makes that token's y non-finite
- * (NaN also where the product with an infinity would be an infinity) and no other's.
+ * (NaN also where the product with an infinity would be an infinity) and no other's;
+ * finite x, the largest included, give a finite y unless y or a partial sum of its groups
+ * leaves the range of fp32.
  * No workspace.
  * ------------------------------------------------------------------------------- */
 int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const void* x, size_t ldx,
@@ -549,11 +553,13 @@ int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const v
  *             included, does not matter.
  *   out       [B][Hq][D] in qdt, dense, written.   lse [B][Hq] fp32 or NULL: the natural
  *             logarithm of the sum of exp(scale q . k_p), to join with other positions.
+ *   scale     |scale| < 2^115; the scores scale q . k stay below 2^126 in size.
  *   ws        >= sfx_attn_q4_ws(B, Hq, Hkv, D, max_pages * page) bytes, any contents.  Few
  *             sequences are cut into more runs, so a smaller B can need more: a workspace
  *             used with several B has the largest size that any of them needs.
  * Several query tokens of one sequence (drafted tokens) are rows with the same table
- * entries and their own lens.  Scores and sums are fp32; a dequantised value is rounded
+ * entries and their own lens.  Scores and sums are fp32 (bf16 scores summed as in
+ * sfx_linear_q4); a dequantised value is rounded
  * once to fp16, a weight to one fp16 term (bf16 results) or two (fp16 results), down to
  * 2^-33 of the largest.  Results are bitwise reproducible for the same shapes and lens.
  * ------------------------------------------------------------------------------- */

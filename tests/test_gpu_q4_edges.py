@@ -40,3 +40,74 @@ def test_append_and_read_at_the_largest_token_count():
         want = torch.from_numpy(Q.values(*Q.quantise(rows.float().numpy(), top))).to(torch.float16)
         assert torch.equal(out[stored].cpu(), want)
         assert not out[~stored].any()
+
+
+BF16_MAX = 2.0 ** 127 * (2 - 2.0 ** -7)
+
+
+@pytest.mark.parametrize("case", [(1, 100, 32), (3, 40, 64), (6, 33, 128), (13, 70, 64), (20, 100, 32), (40, 90, 128), (20, 4130, 64),
+                                  (64, 4100, 32)], ids=lambda c: "x".join(map(str, c)))
+def test_linear_takes_the_largest_bf16_numbers(case):
+    """x of the largest finite size: y is finite (its true size is at most 384 * 2^-10 of x's) and
+    within the bound of the fp32 sums."""
+    B, n, group = case
+    d = 384
+    say(f"linear largest bf16 {case}")
+    g = torch.Generator().manual_seed(n + B)
+    sign = lambda *shape: 2.0 * torch.randint(0, 2, shape, generator=g) - 1  # noqa: E731
+    x = (sign(B, d) * BF16_MAX).to(torch.bfloat16)
+    x[0, ::3] = (0.25 * BF16_MAX * torch.rand(d // 3, generator=g)).to(torch.bfloat16)
+    assert torch.isfinite(x).all()
+    q = torch.randint(-1, 2, (n, d), generator=g)
+    W = ((q[:, 0::2] & 15) | ((q[:, 1::2] & 15) << 4)).to(torch.uint8)
+    s = torch.full((n, d // group), 2.0 ** -10).half()
+    y = torch.empty(B, n, device=DEV)
+    A.sfx_linear_q4(x.to(DEV), W.to(DEV), s.to(DEV), y)
+    assert torch.isfinite(y).all()
+    ref = Q.linear_q4(np64(x), W.numpy(), s.numpy())
+    assert (np.abs(np64(y) - ref) <= Q.linear_q4_bound(np64(x), W.numpy(), s.numpy())).all()
+
+
+@pytest.mark.parametrize("B", [2, 20])
+def test_linear_keeps_small_bf16_numbers(B):
+    """x near 2^-110: sums whose terms lie 2^12 lower still keep all but the last bits above
+    fp32's subnormal step, 2^-149 * 2^12 per addition, scales of at most 1."""
+    n, d, group = 90, 256, 64
+    say(f"linear small bf16 {B}")
+    g = torch.Generator().manual_seed(B)
+    x = (torch.randn(B, d, generator=g) * 2.0 ** -110).to(torch.bfloat16)
+    W = torch.randint(0, 256, (n, d // 2), generator=g, dtype=torch.uint8)
+    s = (0.5 + 0.5 * torch.rand(n, d // group, generator=g)).half()
+    y = torch.empty(B, n, device=DEV)
+    A.sfx_linear_q4(x.to(DEV), W.to(DEV), s.to(DEV), y)
+    ref = Q.linear_q4(np64(x), W.numpy(), s.numpy())
+    # the oracle's bound less its allowance of 2^-120, plus a step for each of two additions per
+    # column and 16 more
+    tol = Q.linear_q4_bound(np64(x), W.numpy(), s.numpy()) - 2.0 ** -120 + (2 * d + 16) * 2.0 ** -137
+    assert (np.abs(np64(y) - ref) <= tol).all(), (np.abs(np64(y) - ref) / tol).max()
+
+
+@pytest.mark.parametrize("D", [32, 128, 256])
+def test_attention_takes_the_largest_bf16_queries(D):
+    """Queries of the largest finite size under a small scale: the scores are ordinary."""
+    Hq, Hkv, page, n = 6, 2, 16, 90
+    say(f"attention largest bf16 {D}")
+    g = torch.Generator().manual_seed(D)
+    k, v = (torch.randn(n, Hkv, D, generator=g) for _ in range(2))
+    q = (torch.randn(1, Hq, D, generator=g).clamp(-1, 1) * BF16_MAX).to(torch.bfloat16)
+    assert torch.isfinite(q).all()
+    table = torch.arange(6, dtype=torch.int32, device=DEV).view(1, 6)
+    pos, seq = torch.arange(n, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    cache = torch.full((6, Hkv, page // 8, 9 * D), 0xFF, dtype=torch.uint8, device=DEV)
+    A.sfx_kv_append_q4(None, k.to(DEV), v.to(DEV), pos, table, cache, None, seq=seq)
+    kn, vn = Q.values(*Q.quantise(k.numpy(), 65504.0)), Q.values(*Q.quantise(v.numpy(), 8188.0))
+    out, lse = torch.empty(1, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(1, Hq, device=DEV)
+    scale = 2.0 ** -130
+    A.sfx_attn_q4(q.to(DEV), cache, table, torch.tensor([n], dtype=torch.int32, device=DEV), out,
+                  A.workspace(A.sfx_attn_q4_ws(1, Hq, Hkv, D, 96)), scale=scale, lse=lse)
+    q64 = np64(q[0])
+    o, ls, ab = Q.attention(q64, kn, vn, scale)
+    d = Q.score_bound(q64, np.abs(kn).reshape(n, Hkv, -1, 32).max((0, 1, 3)) / 7, scale) + 2.0 ** -22 * 40
+    assert d < 2.0 ** -6
+    tol = (2 * 2.0 ** -11 + 2 * d + 2.0 ** -18) * ab * 1.01 + 2.0 ** -8 * np.abs(o)
+    assert (np.abs(np64(out[0]) - o) <= tol).all() and (np.abs(np64(lse[0]) - ls) <= d + 2.0 ** -20 * (1 + np.abs(ls))).all()
