@@ -27,7 +27,7 @@ EXPORTS = ("sfx_status_str", "sfx_abi_version", "sfx_predict_ws", "sfx_predict",
            "sfx_topk_now_update", "sfx_hot_update", "sfx_count_active", "sfx_select_kth_ws",
            "sfx_select_kth", "sfx_hot_first_order_ws", "sfx_hot_first_order", "sfx_gather_rows",
            "sfx_dense_ffn_ws", "sfx_dense_ffn", "sfx_linear_q4", "sfx_kv_cache_bytes", "sfx_kv_append_q4",
-           "sfx_kv_read_q4", "sfx_attn_q4_ws", "sfx_attn_q4")
+           "sfx_kv_read_q4", "sfx_kv_lens_q4", "sfx_attn_q4_ws", "sfx_attn_q4")
 HOT_MAX_MATS = 8
 SFX_DOWN_SCRATCH_BYTES = 17 << 20
 
@@ -126,6 +126,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sfx_kv_append_q4.argtypes = [P, I, I, I, I, I, I, P, Z, P, Z, P, Z, P, P, P, I, I, I, I, I, P, I, I, P, P]
     lib.sfx_kv_read_q4.restype = I
     lib.sfx_kv_read_q4.argtypes = [P, I, I, I, I, P, P, I, I, P, I, I, P, P, P]
+    lib.sfx_kv_lens_q4.restype = I
+    lib.sfx_kv_lens_q4.argtypes = [P, I, P, I, I, I, P, I, I, P, P]
     lib.sfx_attn_q4_ws.restype = Z
     lib.sfx_attn_q4_ws.argtypes = [I, I, I, I, I]
     lib.sfx_attn_q4.restype = I
@@ -686,6 +688,23 @@ def sfx_kv_read_q4(pos, table, cache, k_out, v_out, seq=None, stream=None):
              None if seq is None else _tokens(seq, T, dev, w, "seq"), B, max_pages, table.data_ptr(), page,
              num_pages, cache.data_ptr(), k_out.data_ptr(), v_out.data_ptr()),
             w)
+
+
+def sfx_kv_lens_q4(pos, table, page: int, num_pages: int, lens, starts=None, window=0, max_pos=0, stream=None):
+    """lens [B] = pos + 1 where a token at pos [B] is stored by sfx_kv_append_q4 (with angles for
+    `max_pos` positions; 0: no angles), else 0; with a window, starts [B] = max(0, lens - window)."""
+    w = "sfx_kv_lens_q4"
+    if table.dim() != 2:
+        raise ValueError(f"{w}: table must be [B][max pages]")
+    if table.dtype is not _I32 or not table.is_contiguous():
+        _not_dense(w, table, "table", _I32)
+    B, max_pages = table.shape
+    dev = table.get_device()
+    if dev < 0:
+        _device_error(w, table)
+    _run_on(dev, stream, (_lib or load()).sfx_kv_lens_q4,
+            (B, _tokens(pos, B, dev, w, "pos"), max_pos, window, max_pages, table.data_ptr(), page, num_pages,
+             _tokens(lens, B, dev, w, "lens"), None if starts is None else _tokens(starts, B, dev, w, "starts")), w)
 
 
 def sfx_attn_q4_ws(B: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:

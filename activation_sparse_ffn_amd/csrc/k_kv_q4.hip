@@ -319,6 +319,19 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(ReadArgs a) {
   }
 }
 
+// Lengths that a decode step's attention covers, one sequence per thread.
+__global__ __launch_bounds__(kBlock) void k_kv_lens(KvCache kv, const int32_t* pos, int max_pos, int window, int32_t* lens,
+                                                    int32_t* starts) {
+  const int b = blockIdx.x * kBlock + threadIdx.x;
+  if (b >= kv.B) return;
+  const int p = pos[b];
+  // stored by the append: the same conditions
+  const bool stored = p >= 0 && (max_pos == 0 || p < max_pos) && kv_page(kv, b, p) >= 0;
+  const int n = stored ? p + 1 : 0;
+  lens[b] = n;
+  if (starts) starts[b] = max(n - window, 0);
+}
+
 KvCache make_cache(const KvGeom& g, const void* cache, const int32_t* table) {
   return KvCache{(uint8_t*)cache, table, g.Hkv, g.D, g.page_shift, g.num_pages, g.max_pages, g.B};
 }
@@ -371,6 +384,13 @@ hipError_t launch_kv_append_q4(hipStream_t s, const KvGeom& g, int xdt, int qdt,
   if (xdt == DT_F32) run_append<DT_F32>(s, a, qdt, vec);
   else if (xdt == DT_F16) run_append<DT_F16>(s, a, qdt, vec);
   else run_append<DT_BF16>(s, a, qdt, vec);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_lens_q4(hipStream_t s, const KvGeom& g, const int32_t* pos, int max_pos, int window,
+                             const int32_t* table, int32_t* lens, int32_t* starts) {
+  k_kv_lens<<<dim3((g.B + kBlock - 1) / kBlock), dim3(kBlock), 0, s>>>(make_cache(g, nullptr, table), pos, max_pos, window,
+                                                                       lens, starts);
   return hipGetLastError();
 }
 

@@ -464,6 +464,17 @@ int sfx_kv_read_q4(void* stream, int odt, int T, int Hkv, int D, const int32_t* 
   return launch_status(sfx::launch_kv_read_q4((hipStream_t)stream, g, odt, T, pos, seq, table, cache, k, v));
 }
 
+int sfx_kv_lens_q4(void* stream, int B, const int32_t* pos, int max_pos, int window, int max_pages, const int32_t* table,
+                   int page, int num_pages, int32_t* lens, int32_t* starts) {
+  sfx::KvGeom g;
+  const int st = kv_geom(B, 1, 32, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (B > sfx::kKvMaxTokens || max_pos < 0 || window < 0 || (window == 0) != (starts == nullptr)) return SFX_E_SHAPE;
+  if (!pos || !table || !lens) return SFX_E_NULL;
+  if (!aligned4(pos) || !aligned4(table) || !aligned4(lens) || (starts && !aligned4(starts))) return SFX_E_ALIGN;
+  return launch_status(sfx::launch_kv_lens_q4((hipStream_t)stream, g, pos, max_pos, window, table, lens, starts));
+}
+
 size_t sfx_attn_q4_ws(int B, int Hq, int Hkv, int D, int max_len) {
   if (B < 1 || B > SFX_MAX_B || Hkv < 1 || Hq < 1 || Hq > sfx::kAttnMaxHeads || Hq % Hkv != 0 || D < 32 || D > 256 ||
       D % 32 != 0 || max_len < 1 || max_len > (1 << 30))

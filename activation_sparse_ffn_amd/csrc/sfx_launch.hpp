@@ -94,6 +94,8 @@ hipError_t launch_kv_append_q4(hipStream_t s, const KvGeom& g, int xdt, int qdt,
                                const int32_t* table, void* cache, void* q_out);
 hipError_t launch_kv_read_q4(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
                              const int32_t* table, const void* cache, void* k, void* v);
+hipError_t launch_kv_lens_q4(hipStream_t s, const KvGeom& g, const int32_t* pos, int max_pos, int window,
+                             const int32_t* table, int32_t* lens, int32_t* starts);
 
 // Decode attention: heads per workgroup and the number of runs a sequence is split into.
 struct AttnPlan {

@@ -1,13 +1,9 @@
 """Buffers and call order of one layer-step (predict -> compact -> up -> down) and of
 the per-step TAM update, on top of the libsfx binding.  Orchestration only: every
 number is produced by the library's kernels."""
-import contextlib
-
 import torch
 
 from . import _abi as A
-
-_NO_STREAM = contextlib.nullcontext()
 
 TORCH_WDT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 WDT_CODE = {"f32": A.SFX_F32, "f16": A.SFX_F16, "bf16": A.SFX_BF16, "q4": A.SFX_Q4G32}
@@ -81,9 +77,8 @@ class AttnStep:
     `table` [B][max pages] int32 (layers of a model may share it) and `pos` [B] int32, the
     position of each sequence's token (-1: no token; its output is the bias of the output
     projection), are the caller's and may change between steps, also of a captured graph;
-    the attention covers positions max(0, pos + 1 - window) .. pos (window 0: all).  Every
-    pos >= 0 must have a page in `table` and a row in `cos_sin`: a token that is not stored
-    gets no queries of its own either."""
+    the attention covers positions max(0, pos + 1 - window) .. pos (window 0: all).  A pos
+    without a page in `table` or a row in `cos_sin` is no token either."""
 
     def __init__(self, Hq: int, Hkv: int, D: int, B: int, dtype: str, table: torch.Tensor, pos: torch.Tensor,
                  num_pages: int, page: int = 16, cos_sin: torch.Tensor = None, interleaved: bool = False,
@@ -114,10 +109,8 @@ class AttnStep:
     def run(self, layer, x: torch.Tensor, y: torch.Tensor, accumulate: bool = False, stream=None):
         """y [B][d] (+)= the attention half of `layer` on x [B][d] at the positions `pos`."""
         g = layer.get if isinstance(layer, dict) else (lambda k: getattr(layer, k, None))
-        with torch.cuda.stream(stream) if stream is not None else _NO_STREAM:
-            torch.add(self.pos, 1, out=self.lens)
-            if self.starts is not None:
-                torch.sub(self.lens, self.window, out=self.starts)
+        A.sfx_kv_lens_q4(self.pos, self.table, self.cache.shape[2] * 8, self.cache.shape[0], self.lens, starts=self.starts,
+                         window=self.window, max_pos=0 if self.cos_sin is None else self.cos_sin.shape[0], stream=stream)
         A.sfx_linear_q4(x, g("Wqkv"), g("Wqkv_s"), self.qkv, bias=g("bqkv"), stream=stream)
         q, k, v = self._cut(self.qkv)
         A.sfx_kv_append_q4(q, k, v, self.pos, self.table, self.cache, self.q, cos_sin=self.cos_sin,

@@ -14,7 +14,7 @@
  *   sfx_hot_update   hot region slots + copy of entering groups  once per step, all layers
  *   sfx_select_kth, sfx_count_active, sfx_hot_first_order, sfx_gather_rows
  *                    offline calibration: thresholds, frequencies, hot-first order
- *   sfx_linear_q4, sfx_kv_append_q4, sfx_kv_read_q4, sfx_attn_q4
+ *   sfx_linear_q4, sfx_kv_append_q4, sfx_kv_read_q4, sfx_kv_lens_q4, sfx_attn_q4
  *                    the attention half of a layer: int4 projections, paged int4 cache
  *
  * Conventions shared by every entry point
@@ -543,6 +543,13 @@ int sfx_linear_q4(void* stream, int xdt, int group, int B, int n, int d, const v
  * sfx_kv_read_q4 -- values of T listed positions: k, v [T][Hkv][D] in odt (SFX_F32 exact,
  *   SFX_F16 / SFX_BF16 rounded once), written; zeros for a padding token.
  *
+ * sfx_kv_lens_q4 -- the lengths of a decode step with one token per sequence at pos [B]:
+ *   lens[b] = pos[b] + 1 where sfx_kv_append_q4 stores the token (0 <= pos[b], its page is in
+ *   the table, and pos[b] < max_pos unless max_pos is 0: no table of angles), else 0, so that
+ *   a token that is not stored has nothing to attend to either.
+ *   window    positions that the attention covers; 0: all, and starts is NULL.  Otherwise
+ *             starts[b] = max(0, lens[b] - window).   lens, starts [B] int32, written.
+ *
  * sfx_attn_q4 -- o[b][h] = sum_p w_p v_p,  w = softmax over p in [starts[b], lens[b]) of
  *   scale q[b][h] . k_p, with kv head h / (Hq / Hkv).
  *   qdt       SFX_F16 or SFX_BF16 (q and out).   B 1..64, Hq 1..256, Hq % Hkv == 0.
@@ -572,6 +579,8 @@ int sfx_kv_append_q4(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int
 int sfx_kv_read_q4(void* stream, int odt, int T, int Hkv, int D, const int32_t* pos, const int32_t* seq,
                    int B, int max_pages, const int32_t* table, int page, int num_pages,
                    const void* cache, void* k, void* v);
+int sfx_kv_lens_q4(void* stream, int B, const int32_t* pos, int max_pos, int window, int max_pages,
+                   const int32_t* table, int page, int num_pages, int32_t* lens, int32_t* starts);
 size_t sfx_attn_q4_ws(int B, int Hq, int Hkv, int D, int max_len);
 int sfx_attn_q4(void* stream, int qdt, int B, int Hq, int Hkv, int D, const void* q, size_t ldq,
                 int max_pages, const int32_t* table, int page, int num_pages, const void* cache,

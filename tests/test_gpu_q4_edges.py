@@ -111,3 +111,96 @@ def test_attention_takes_the_largest_bf16_queries(D):
     assert d < 2.0 ** -6
     tol = (2 * 2.0 ** -11 + 2 * d + 2.0 ** -18) * ab * 1.01 + 2.0 ** -8 * np.abs(o)
     assert (np.abs(np64(out[0]) - o) <= tol).all() and (np.abs(np64(lse[0]) - ls) <= d + 2.0 ** -20 * (1 + np.abs(ls))).all()
+
+
+@pytest.mark.parametrize("angles", [0, 40])
+def test_lens_follow_what_the_append_stores(angles):
+    """Lengths and starts of a step whose positions have a page and an angle, or lack one: the
+    append stores exactly the tokens that get a length."""
+    page, num_pages, D = 8, 9, 32
+    say(f"lens, angles for {angles}")
+    table = torch.tensor([[0, 1, 2, 3, 4, 5], [6, -1, 7, 9, 8, -3]], dtype=torch.int32).repeat(40, 1)
+    pos = torch.tensor([(5 * i) % 60 - 4 for i in range(80)], dtype=torch.int32)
+    pos[:8] = torch.tensor([0, 7, 8, 15, 39, 40, 47, 48], dtype=torch.int32)
+    pos[8:10] = torch.tensor([-2 ** 31, 2 ** 31 - 1])
+    want = []
+    for b, p in enumerate(pos.tolist()):
+        ok = 0 <= p < 48 and 0 <= int(table[b, p // page]) < num_pages and not (angles and p >= angles)
+        want.append(p + 1 if ok else 0)
+    lens, starts = (torch.full((80,), 7, dtype=torch.int32, device=DEV) for _ in range(2))
+    for window in (0, 1, 5, 1000):
+        A.sfx_kv_lens_q4(pos.to(DEV), table.to(DEV), page, num_pages, lens, starts=starts if window else None, window=window,
+                         max_pos=angles)
+        assert lens.tolist() == want
+        if window:
+            assert starts.tolist() == [max(0, n - window) for n in want]
+    # one token at a time, into a cache of its own: its bytes change where it has a length
+    cs = torch.ones(angles, 2, device=DEV) if angles else None
+    k = torch.ones(1, 1, D, device=DEV)
+    for b in range(10):
+        cache = torch.zeros(num_pages, 1, 1, 9 * D, dtype=torch.uint8, device=DEV)
+        A.sfx_kv_append_q4(None, k, k, pos[b:b + 1].to(DEV), table[b:b + 1].to(DEV), cache, None, cos_sin=cs)
+        assert bool(cache.any()) == (want[b] > 0), (b, int(pos[b]))
+
+
+def attn_weights(d, Hq, Hkv, D, seed):
+    g = torch.Generator().manual_seed(seed)
+    n = (Hq + 2 * Hkv) * D
+    rnd = lambda *shape: torch.randint(0, 256, shape, generator=g, dtype=torch.uint8)  # noqa: E731
+    return {"Wqkv": rnd(n, d // 2).to(DEV), "Wqkv_s": (torch.rand(n, d // 32, generator=g) * 0.03 + 1e-3).half().to(DEV),
+            "Wo": rnd(d, Hq * D // 2).to(DEV), "Wo_s": (torch.rand(d, Hq * D // 64, generator=g) * 0.03 + 1e-3).half().to(DEV),
+            "bqkv": torch.randn(n, generator=g).to(DEV), "bo": torch.randn(d, generator=g).to(DEV)}
+
+
+@pytest.mark.parametrize("window", [0, 6])
+def test_step_treats_what_is_not_stored_as_no_token(window):
+    """A sequence past the angle table, one whose page is missing, one whose page id is outside the
+    cache and one past its table: their rows are the output bias, as for pos = -1, eager and
+    captured, whatever the step before left; the other sequence keeps its bits."""
+    from activation_sparse_ffn_amd import AttnStep
+    d, Hq, Hkv, D, B, page = 256, 4, 2, 64, 5, 8
+    say(f"step, tokens that are not stored, window {window}")
+    w = attn_weights(d, Hq, Hkv, D, 6)
+    table = torch.arange(20, dtype=torch.int32).view(5, 4).to(DEV)
+    angles = torch.ones(22, D, device=DEV) * 0.7
+    pos = torch.full((B,), 3, dtype=torch.int32, device=DEV)
+    step = AttnStep(Hq, Hkv, D, B, "f16", table, pos, 20, page=page, cos_sin=angles, window=window)
+    step.cache.zero_()
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(B, d, generator=g).half().to(DEV)
+    y = torch.empty(B, d, device=DEV)
+    step.run(w, x, y)                                    # leaves queries of every sequence
+    before = step.cache.clone()
+    table[2, 1], table[3, 1] = -1, 20
+    bad = [8, 22, 8, 8, 32]                              # sequence 0 is a good one
+    outs = []
+    for these in (bad, [8, -1, -1, -1, -1]):
+        step.cache.copy_(before)
+        pos.copy_(torch.tensor(these, dtype=torch.int32))
+        step.run(w, x, y)
+        outs.append(y.clone())
+    assert torch.equal(outs[0], outs[1])
+    assert torch.equal(outs[0][1:], w["bo"].expand(B - 1, d)) and not torch.equal(outs[0][0], w["bo"])
+    assert not step.o[1:].any()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run(w, x, y)
+    for these in (bad, [8, 5, 6, 7, 7], bad):
+        step.cache.copy_(before)
+        pos.copy_(torch.tensor(these, dtype=torch.int32))
+        graph.replay()
+        if these == bad:
+            assert torch.equal(y, outs[0])
+        else:
+            assert (y != w["bo"]).any(1).all()
+        _ = torch.randn(1000, device=DEV).sum().item()
+
+
+def test_step_refuses_a_negative_window():
+    from activation_sparse_ffn_amd import AttnStep
+    table, pos = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    w = attn_weights(256, 4, 2, 64, 6)
+    step = AttnStep(4, 2, 64, 1, "f16", table, pos, 1, page=8, window=-1)
+    with pytest.raises(A.SfxError):
+        step.run(w, torch.zeros(1, 256, dtype=torch.float16, device=DEV), torch.zeros(1, 256, device=DEV))
