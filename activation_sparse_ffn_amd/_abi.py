@@ -508,7 +508,9 @@ def _device_error(where, *tensors):
 
 def _run_on(dev, stream, fn, args, where):
     """Call `fn(stream, *args)` with device `dev` current, on its current stream unless
-    `stream` is given."""
+    `stream`, one of its streams, is given."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"{where}: the stream is on device {stream.device_index}, the tensors on {dev}")
     if dev == torch._C._cuda_getDevice():
         st = fn(torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, *args)
     else:

@@ -204,3 +204,37 @@ def test_step_refuses_a_negative_window():
     step = AttnStep(4, 2, 64, 1, "f16", table, pos, 1, page=8, window=-1)
     with pytest.raises(A.SfxError):
         step.run(w, torch.zeros(1, 256, dtype=torch.float16, device=DEV), torch.zeros(1, 256, device=DEV))
+
+
+def test_streams_of_this_and_of_another_device():
+    """Every entry point takes the tensors' device's streams, the default one and others, and
+    refuses a stream that says it is on another device before anything is enqueued."""
+    class Elsewhere:
+        device_index, cuda_stream = 1, torch.cuda.current_stream().cuda_stream
+
+    D, page = 32, 8
+    x, W = torch.zeros(1, 64, dtype=torch.float16, device=DEV), torch.zeros(8, 32, dtype=torch.uint8, device=DEV)
+    s, y = torch.zeros(8, 2, dtype=torch.float16, device=DEV), torch.full((1, 8), 3.0, device=DEV)
+    k, cache = torch.ones(1, 1, D, device=DEV), torch.zeros(1, 1, 1, 9 * D, dtype=torch.uint8, device=DEV)
+    at, table = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    q, ko, lens = torch.ones(1, 1, D, dtype=torch.float16, device=DEV), torch.full_like(k, 3.0), torch.full_like(at, 3)
+    out = torch.full_like(q, 3.0)
+    calls = (lambda st: A.sfx_linear_q4(x, W, s, y, stream=st),
+             lambda st: A.sfx_kv_append_q4(None, k, k, at, table, cache, None, stream=st),
+             lambda st: A.sfx_kv_read_q4(at, table, cache, ko, ko.clone(), stream=st),
+             lambda st: A.sfx_kv_lens_q4(at, table, page, 1, lens, stream=st),
+             lambda st: A.sfx_attn_q4(q, cache, table, lens, out, None, stream=st))
+    for call in calls:
+        with pytest.raises(ValueError, match="stream is on device 1"):
+            call(Elsewhere())
+    torch.cuda.synchronize()
+    assert (y == 3).all() and (ko == 3).all() and (out == 3).all() and not cache.any() and lens.item() == 3
+    for st in (torch.cuda.default_stream(), torch.cuda.Stream()):
+        st.wait_stream(torch.cuda.current_stream())
+        for call in calls:
+            call(st)
+        torch.cuda.current_stream().wait_stream(st)
+    # ones are held as 7 fp16(1 / 7) = 1 - 2^-12; the attention rounds a value and its result to fp16
+    held = float(7 * np.float64(np.float16(np.float32(1) / np.float32(7))))
+    assert held == 1 - 2.0 ** -12
+    assert not y.any() and (ko == held).all() and lens.item() == 1 and (out.double() - held).abs().max() <= 2 * 2.0 ** -11

@@ -45,3 +45,14 @@ def test_lens_binding_refusals():
         A.sfx_kv_lens_q4(pos, table.view(12), 16, 5, pos.clone())
     with pytest.raises(TypeError):
         A.sfx_kv_lens_q4(pos, table.long(), 16, 5, pos.clone())
+
+
+def test_stream_of_another_device_is_refused():
+    """A stream belongs to the tensors' device: nothing is called on another one's."""
+    class Stream:
+        device_index, cuda_stream = 1, 0
+
+    called = []
+    with pytest.raises(ValueError, match="stream is on device 1"):
+        A._run_on(0, Stream(), lambda *a: called.append(a) or 0, (), "f")
+    assert not called
