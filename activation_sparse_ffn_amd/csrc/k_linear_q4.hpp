@@ -6,7 +6,7 @@
 // meets one weight row only and needs one scale per group.  The waves of a workgroup share
 // their rows and deal the columns among themselves; their sums are added in wave order
 // through LDS, so y is bitwise reproducible.  Three kernels, by how much of x there is:
-//   few tokens   all of x in LDS; bound by reading the codes.
+//   few tokens   up to 8, all of x in LDS; bound by reading the codes.
 //   wide, rows   x in blocks, 16 or 32 rows per workgroup: each workgroup reads all of x, from
 //                L2, and writes it to LDS; from about 16 tokens on that and the decoding
 //                weigh more than the codes.
@@ -31,12 +31,12 @@ struct LinearArgs {
   int B, n, d, accumulate;
 };
 
-// Token that row m of token tile nt stands for.  NI accumulator rows per lane are used:
-// below 16 tokens the tokens are spread over the quarters (row 4 c + i is token NI c + i),
-// so only NI of a lane's four sums are scaled.
+// Token that row m stands for where NI < 4 accumulator rows per lane are used: up to 8 tokens
+// are spread over the quarters (row 4 c + i is token NI c + i), so only NI of a lane's four
+// sums are scaled.
 template <int NI>
-__device__ __forceinline__ int lin_token(int nt, int m) {
-  return NI == 4 ? 16 * nt + m : NI * (m >> 2) + (m & (NI - 1));
+__device__ __forceinline__ int lin_token(int m) {
+  return NI * (m >> 2) + (m & (NI - 1));
 }
 
 // Columns of an 8-column slice in the order of the decoder's registers: (0 4) (1 5) (2 6) (3 7).
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
       if (b < a.B) *reinterpret_cast<Raw<16>*>(sh + b * xstride + i * 16) = lin_order(xv[b]);
   }
   __syncthreads();
-  const uint8_t* xlane = sh + min(lin_token<NI>(0, m), a.B - 1) * xstride + c * 16;
+  const uint8_t* xlane = sh + min(lin_token<NI>(m), a.B - 1) * xstride + c * 16;
 
   float acc[1][NI];
 #pragma unroll
@@ -432,7 +432,9 @@ __global__ __launch_bounds__(kLinWaves * kWave, 2) void k_linear_q4_rows(LinearA
   lin_finish<T, NT, 4, kChunks, 2>(a, (float*)sh, row0, kc, rg, m, c, acc);
 }
 
-constexpr int kLinXLds = 64 << 10;       // x is kept whole in LDS up to here: two workgroups per compute unit
+// x is kept whole in LDS, beside the 32 KB ring, up to these sizes: with kLinXTwo two workgroups
+// fit a compute unit's 160 KB, with kLinXOne one does.
+constexpr int kLinXTwo = 48 << 10, kLinXOne = 128 << 10;
 
 template <class T, int NI>
 hipError_t lin_run(hipStream_t s, const LinearArgs& a, int gsh) {
@@ -462,11 +464,17 @@ hipError_t lin_run_rows(hipStream_t s, const LinearArgs& a, int gsh) {
 
 template <class T>
 hipError_t lin_launch(hipStream_t s, const LinearArgs& a, int gsh) {
-  if (a.B <= 16 && (size_t)a.B * (a.d * 2 + 16) <= (size_t)kLinXLds) {
-    if (a.B <= 4) return lin_run<T, 1>(s, a, gsh);
-    if (a.B <= 8) return lin_run<T, 2>(s, a, gsh);
-    return lin_run<T, 4>(s, a, gsh);
-  }
+  // Up to 8 tokens x is kept whole.  A workgroup that has a compute unit to itself pays where
+  // there is no second one for it (up to 4096 rows), and for one or two tokens where there are
+  // up to two.  us, x whole against x in blocks (f16, scales per 32):
+  //   x 24..48 KB    4 x 4096 x 4096 6.0, 7.2;  2 x 8192 x 8192 13.5, 17.3;  4 x 28672 x 4096 20, 25
+  //   x 48..128 KB   4096 rows: 8 x 4096 6.2, 7.2;  2 x 16384 17.0, 19.3;  1 x 28672 26.1, 31.3
+  //                  8192 rows: 4 x 7168 17.1, 15.2;  8 x 4096 10.7, 9.5;  1 x 28672 47.8, 50.1
+  //                  16384 rows: 4 x 7168 31.2, 21.0;  2 x 16384 56.7, 42.3;  1 x 28672 90, 70
+  //   9..16 tokens   16 x 4096 x 1024 4.9, 3.6;  16 x 28672 x 1024 15.2, 8.4;  12 x 4096 x 4096 7.2, 7.4
+  const size_t x = (size_t)a.B * (a.d * 2 + 16);
+  if (a.B <= 8 && x <= (size_t)(a.n <= (a.B <= 2 ? 8192 : 4096) ? kLinXOne : kLinXTwo))
+    return a.B <= 4 ? lin_run<T, 1>(s, a, gsh) : lin_run<T, 2>(s, a, gsh);
   // 16 rows per workgroup leave enough workgroups for few rows; above one per compute unit,
   // workgroups of 32 rows read x half as often (64 tokens: 4096 x 4096 14.4 us with 16 rows and
   // 16.7 with 32; 48 tokens: 6144 x 4096 20.6 and 13.5; 37: 8192 x 8192 38.2 and 24.1)

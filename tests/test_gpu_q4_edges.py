@@ -238,3 +238,29 @@ def test_streams_of_this_and_of_another_device():
     held = float(7 * np.float64(np.float16(np.float32(1) / np.float32(7))))
     assert held == 1 - 2.0 ** -12
     assert not y.any() and (ko == held).all() and lens.item() == 1 and (out.double() - held).abs().max() <= 2 * 2.0 ** -11
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("case", [  # B, n, d, group: x of up to 128 KB in LDS and just past it
+    (1, 50, 24544, 32), (1, 20, 65504, 32), (1, 20, 65536, 64), (2, 8192, 32704, 64), (2, 8193, 12288, 64), (3, 4096, 21824, 64),
+    (3, 4097, 8192, 128), (3, 4097, 8160, 32), (5, 4096, 13088, 32), (8, 31, 8160, 32), (8, 31, 8192, 128), (8, 5000, 3040, 32),
+    (8, 5000, 3200, 128), (9, 4100, 96, 32), (16, 16, 1024, 64)], ids=lambda c: "x".join(map(str, c)))
+def test_linear_at_the_borders_of_its_kernels(case, dt):
+    """Sizes on either side of what decides between keeping x whole in LDS and taking it in blocks."""
+    B, n, d, group = case
+    say(f"linear border {case} {dt}")
+    g = torch.Generator().manual_seed(n + d)
+    x = torch.randn(B, d, generator=g).to(DT[dt])
+    W = torch.randint(0, 256, (n, d // 2), generator=g, dtype=torch.uint8)
+    s = (0.05 * torch.rand(n, d // group, generator=g) + 1e-3).half()
+    y = torch.full((B, n), float("nan"), device=DEV)
+    args = [t.to(DEV) for t in (x, W, s)]
+    A.sfx_linear_q4(*args, y)
+    some = np.unique(np.r_[:min(n, 64), n // 2:min(n, n // 2 + 40), max(0, n - 64):n])
+    ref = Q.linear_q4(np64(x), W.numpy()[some], s.numpy()[some])
+    err = np.abs(np64(y)[:, some] - ref)
+    assert (err <= Q.linear_q4_bound(np64(x), W.numpy()[some], s.numpy()[some])).all()
+    assert torch.isfinite(y).all()
+    y2 = torch.full_like(y, float("nan"))
+    A.sfx_linear_q4(*args, y2)
+    assert torch.equal(y, y2)
