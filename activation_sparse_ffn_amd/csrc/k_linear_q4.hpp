@@ -289,9 +289,11 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
 
 // More tokens, or long rows: x passes through LDS in blocks of 1024 columns, a chunk of 128
 // for each wave; the next block's x and the weights of four blocks are on the way in registers
-// meanwhile.  16 weight rows per workgroup.
+// meanwhile.  16 weight rows per workgroup.  Two row tiles and more need over 128 registers (with
+// that limit they spilled in the loop: 32 x 4096 x 8192 bf16, scales per 64, 23.0 us instead of
+// 15.7); few rows leave a compute unit one workgroup anyway.
 template <class T, int NT, int GSH>
-__global__ __launch_bounds__(kLinWaves * kWave, NT <= 2 ? 4 : 2) void k_linear_q4_wide(LinearArgs a) {
+__global__ __launch_bounds__(kLinWaves * kWave, NT == 1 ? 4 : 2) void k_linear_q4_wide(LinearArgs a) {
   constexpr int kThreads = kLinWaves * kWave, kCols = 128 * kLinWaves, kRow = kCols * 2 + 16;
   constexpr int kX = 16 * NT * kRow, kRed = kLinWaves * 16 * (16 * NT + 1) * 4;
   constexpr int kPass = 16 * NT * (kCols / 8) / kThreads;       // 16-byte pieces of x per thread and block
@@ -477,7 +479,8 @@ hipError_t lin_launch(hipStream_t s, const LinearArgs& a, int gsh) {
     return a.B <= 4 ? lin_run<T, 1>(s, a, gsh) : lin_run<T, 2>(s, a, gsh);
   // 16 rows per workgroup leave enough workgroups for few rows; above one per compute unit,
   // workgroups of 32 rows read x half as often (64 tokens: 4096 x 4096 14.4 us with 16 rows and
-  // 16.7 with 32; 48 tokens: 6144 x 4096 20.6 and 13.5; 37: 8192 x 8192 38.2 and 24.1)
+  // 16.7 with 32; 32: 4096 x 8192 15.7 and 17.8; 48: 6144 x 4096 20.6 and 13.5; 37: 8192 x 8192
+  // 38.2 and 24.1; 12: 8192 x 4096 10.4 and 9.5, 8192 x 1024 4.5 and 4.8)
   const bool two = a.n > 16 * 256;
   if (a.B <= 16) return two ? lin_run_rows<T, 1>(s, a, gsh) : lin_run_wide<T, 1>(s, a, gsh);
   if (a.B <= 32) return two ? lin_run_rows<T, 2>(s, a, gsh) : lin_run_wide<T, 2>(s, a, gsh);
