@@ -116,3 +116,51 @@ def score_bound(q: np.ndarray, k_abs_scale: np.ndarray, scale: float) -> float:
     55 sum|q|, times the largest key scale; then the sum over groups and two products."""
     aq = np.abs(q).reshape(q.shape[0], -1, 32).sum(2)                   # [Hq][ng]
     return float(2.0 ** -23 * (65 * 55 + 8 * (aq.shape[1] + 8)) * abs(scale) * np.max(aq @ k_abs_scale))
+
+
+# ---- limits that a loss of precision does not pass.  linear_q4_bound and score_bound hold for
+# any data; for data of random signs the roundings are independent, and their root mean
+# square over many results is far smaller.
+
+def linear_q4_rms(x: np.ndarray, codes: np.ndarray, scales: np.ndarray, offset: bool) -> np.ndarray:
+    """Root mean square error [B][n] of fp32 sums, for x of random signs.  A group of G columns
+    takes at most 2 G additions, each off by at most 2^-23 of a partial sum of the size
+    |q x| (2-norm over the group), or 31 |x| where the codes' offset is summed too; then one
+    multiply-add per group and 16 additions of the size of the result."""
+    q = unpack_rows(codes).astype(np.float64)
+    n, d = q.shape
+    ng = scales.shape[1]
+    G, s2 = d // ng, scales.astype(np.float64) ** 2                    # [n][ng]
+    x2 = (x ** 2).reshape(x.shape[0], ng, G)
+    r2 = np.einsum("bgc,igc->big", x2, (q ** 2).reshape(n, ng, G))      # |q x|^2 [B][n][ng]
+    p2 = np.broadcast_to((31.0 ** 2 * x2.sum(2))[:, None], r2.shape) if offset else r2
+    return 2.0 ** -23 * np.sqrt(2 * G * (s2 * p2).sum(2) + (ng + 16) * (s2 * r2).sum(2))
+
+
+def attention_rms(q, k, v, scale, offset: bool, weight_steps, value_step, half_step):
+    """o [Hq][D] and the root mean square error [Hq][D] of an evaluation that rounds each weight and
+    each value within the given half steps (relative; uniform errors: half step / sqrt(3)) and the
+    result within `half_step`, with fp32 scores summed as linear_q4_rms says (scale groups of 32)."""
+    Hq, D = q.shape
+    n, Hkv = k.shape[0], k.shape[1]
+    o, rms = np.zeros((Hq, D)), np.zeros((Hq, D))
+    for h in range(Hq):
+        kv = h // (Hq // Hkv)
+        s = scale * (k[:, kv] @ q[h])
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        o[h] = w @ v[:, kv]
+        k32 = k[:, kv].reshape(n, -1, 32)
+        top = np.abs(k32).max(2) / 7                                    # at least the scale, unless all codes are small
+        q2 = (q[h] ** 2).reshape(-1, 32).sum(1)
+        p2 = (top ** 2 * (31.0 ** 2 if offset else 8.0 ** 2) * q2).sum(1)
+        ds = 2.0 ** -23 * np.sqrt(64 * p2 + (q2.size + 8) * (s / scale) ** 2) * abs(scale) + 2.0 ** -23 * (np.abs(s) + 2 * np.abs(s).max())
+        e2 = (w * w * (weight_steps ** 2 / 3 + value_step ** 2 / 3 + ds ** 2)) @ v[:, kv] ** 2
+        rms[h] = np.sqrt(e2 + (half_step * o[h]) ** 2 / 3)
+    return o, rms
+
+
+def rms_ratio(err: np.ndarray, rms: np.ndarray) -> float:
+    """Root mean square of err / rms over the results that have an error at all."""
+    on = rms > 0
+    return float(np.sqrt(np.mean((err[on] / rms[on]) ** 2)))
