@@ -22,7 +22,7 @@
 // works on and four waves fit a SIMD.  131072 positions x 8 kv heads, step by step: two tiles in
 // registers, the last workgroup joining behind a cache invalidation, 66 us; through LDS, joined
 // without the invalidation, 45; joined by a kernel of its own, 41 (35.0, 4.3 TB/s, and 4.7).
-// 64 sequences of up to 4096 x 8 kv heads of 64: 27 us, with sequences of different lengths paired
+// 64 sequences of up to 4096 x 8 kv heads of 64: 26 us, with sequences of different lengths paired
 // on a compute unit (31 in the caller's order).
 #pragma once
 #include "sfx_kv.hpp"
@@ -36,8 +36,10 @@ constexpr int kAttnTile = 32;          // positions a wave takes at a time
 constexpr int kAttnUnits = 256;        // compute units
 constexpr int kAttnOrder = 1024;       // positions of a table from which sequences are ordered
 constexpr float kRefMin = -3.0e38f;
-// Waves of a workgroup and tiles of LDS per wave: two workgroups fit a compute unit's 160 KB,
-// and a wave always has a tile or more on the way while it works on one.
+// Waves of a workgroup and tiles of LDS per wave: two workgroups fit a compute unit's 160 KB.
+// The next tiles are asked for before a tile is waited for.  The counted waits are what a tile
+// needs; the compiler adds a wait for all copies into LDS before the tile's first LDS read, so
+// as compiled a wave's copies overlap with other waves' work and not with its own.
 constexpr int attn_waves(int NG) { return NG <= 4 ? 8 : 4; }
 constexpr int attn_slots(int NG) { return NG <= 2 ? 4 : NG == 5 ? 3 : 2; }
 

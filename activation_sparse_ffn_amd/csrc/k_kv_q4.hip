@@ -9,7 +9,8 @@
 // border then falls the same way wherever it is computed.  max / 7 and k' / s are
 // correctly rounded fp32 quotients.
 //
-// Both are bound by the 16- or 32-bit rows they read or write.  Measured (one MI355X): 4095
+// Both move mostly the 16- or 32-bit rows they read or write; of a thread's 28 vector loads in a
+// bf16 prompt's append 16 are 4-byte loads of the angle table.  Measured (one MI355X): 4095
 // tokens of 64 query and 8 kv heads of 128, bf16: append 45 us for 155 MB, of which the 64-bit
 // rotation costs 2.4; one head per wave and token, each lane two dims, took 107, bound by the
 // chain from position to page to data.  Reading 16384 positions of 8 heads of 128 back: 19 us
@@ -122,8 +123,6 @@ __device__ __forceinline__ bool turn_first(const AppendArgs& a, int d) { return 
 __device__ __forceinline__ int turn_other(const AppendArgs& a, int d) {
   return a.pairs ? d ^ 1 : d < (a.rot >> 1) ? d + (a.rot >> 1) : d - (a.rot >> 1);
 }
-// VEC: the first `rot` dims and their halves are whole slices of 8.
-template <bool VEC>
 __device__ __forceinline__ void load_turn(const AppendArgs& a, const float* cs, int d0, Turn& t) {
   const int half = a.rot >> 1;
 #pragma unroll
@@ -136,6 +135,7 @@ __device__ __forceinline__ void load_turn(const AppendArgs& a, const float* cs, 
 // Where the slice's partners lie, for a whole slice of them in another place.
 __device__ __forceinline__ bool turn_apart(const AppendArgs& a, int d0) { return a.cs && !a.pairs && d0 < a.rot; }
 
+// VEC: the first `rot` dims and their halves are whole slices of 8.
 template <int DT, bool VEC>
 __device__ __forceinline__ void turn8(const AppendArgs& a, const void* p, size_t head, int d0, const Eight<DT>& own,
                                       const Eight<DT>& apart, const Turn& t, float (&y)[8]) {
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a, int qcols) {
   if (pos < 0 || (unsigned)b >= (unsigned)a.kv.B || (a.cs && pos >= a.max_pos)) return;
   const int id = kv_page(a.kv, b, pos);
   Turn turn;
-  if (a.cs && d0 < a.rot) load_turn<VEC>(a, a.cs + (size_t)pos * a.rot, d0, turn);
+  if (a.cs && d0 < a.rot) load_turn(a, a.cs + (size_t)pos * a.rot, d0, turn);
   if (id < 0) return;
   const int in_page = pos & ((1 << a.kv.page_shift) - 1), i = in_page & 7;
 #pragma unroll

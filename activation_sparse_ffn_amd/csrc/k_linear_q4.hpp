@@ -156,8 +156,10 @@ constexpr int kLinWaves = 8;
 // banks.
 constexpr int kLinUnit = 16 * 128;       // bytes
 // Units of a wave in LDS or on the way.  Two, not more: 32 KB leave room for three or four
-// workgroups per compute unit, which hide more than longer queues in two (four units: 8192 x
-// 8192 at one token 16.7 us against 12.2, 16384 x 4096 at four 20.5 against 13.9).
+// workgroups per compute unit (four units: 8192 x 8192 at one token 16.7 us against 12.2, 16384 x
+// 4096 at four 20.5 against 13.9).  A longer queue could not help as compiled: the counted wait
+// is what a unit needs, but the compiler adds a wait for all copies into LDS before the unit's
+// first LDS reads, so a wave's copies overlap with other waves' work only.
 constexpr int kLinSlots = 2;
 
 // A row's scales of one unit, as they lie: 8 >> GSH of them.
@@ -288,8 +290,9 @@ __global__ __launch_bounds__(kLinWaves * kWave) void k_linear_q4(LinearArgs a) {
 }
 
 // More tokens, or long rows: x passes through LDS in blocks of 1024 columns, a chunk of 128
-// for each wave; the next block's x and the weights of four blocks are on the way in registers
-// meanwhile.  16 weight rows per workgroup.  Two row tiles and more need over 128 registers (with
+// for each wave; the next block's x and the weights of four blocks are asked for in registers
+// meanwhile (writing x to LDS waits for all that was asked for before: the compiler keeps no count
+// across the branches of the weights' loads).  16 weight rows per workgroup.  Two row tiles and more need over 128 registers (with
 // that limit they spilled in the loop: 32 x 4096 x 8192 bf16, scales per 64, 23.0 us instead of
 // 15.7); few rows leave a compute unit one workgroup anyway.
 template <class T, int NT, int GSH>
@@ -359,7 +362,7 @@ __global__ __launch_bounds__(kLinWaves * kWave, NT == 1 ? 4 : 2) void k_linear_q
 
 // Many weight rows: two groups of four waves, 16 rows each, over blocks of 512 columns.  Two
 // blocks of x lie in LDS: while one is worked on, the next is written from registers and the
-// one behind it is on its way there, with one barrier a block.
+// one behind it is asked for, with one barrier a block; loads are waited for as above.
 template <class T, int NT, int GSH>
 __global__ __launch_bounds__(kLinWaves * kWave, 2) void k_linear_q4_rows(LinearArgs a) {
   constexpr int kThreads = kLinWaves * kWave, kChunks = 4, kCols = 128 * kChunks, kRow = kCols * 2 + 16;
