@@ -247,12 +247,14 @@ def _make(case, seed):
         st["q"] = (1.3 * rnd(sum(_counts(c)), c["hq"], c["dim"])).to(DT[c["dt"]])
         return st
     T = c["tokens"]
-    st["seq"] = torch.arange(c["B"], dtype=torch.int32, device="cuda").repeat_interleave(T)
     pos = torch.arange(T, dtype=torch.int32, device="cuda").repeat(c["B"]) + c["past"]
     pad = c["pad"] if c["pad"] < c["B"] * T else 0
     if pad:
         pos[-pad:] = -1                              # padding behind the last request's tokens
     st["pos"] = pos
+    counts = (pos >= 0).view(c["B"], T).sum(1).int()
+    st["lens"] = counts + c["past"]
+    st["q_start"] = torch.cat([counts.new_zeros(1), counts.cumsum(0).int()])
     # what is read back: every position of the blocks written to, up to the last token
     first = c["past"] // BLK * BLK
     n = c["past"] + T - first
@@ -458,8 +460,8 @@ def _own(st, c):
         A.sfx_linear_q8(st["x"], st["sx"], st["W"], st["sw"], st["y"], bias=st["bias"], accumulate=c["acc"])
         return st["y"]
     if c["op"] == "append":
-        A.sfx_kv_append_q8(st["q"], st["k"], st["v"], st["pos"], st["table"], st["cache"], st["q_out"], seq=st["seq"],
-                           cos_sin=st["cos_sin"], interleaved=c["rope"] == "pairs")
+        A.sfx_kv_append_q8(st["q"], st["k"], st["v"], st["lens"], st["table"], st["cache"], st["q_out"],
+                           q_start=st["q_start"], cos_sin=st["cos_sin"], interleaved=c["rope"] == "pairs")
         A.sfx_kv_read_q8(st["rpos"], st["table"], st["cache"], st["k_out"], st["v_out"], seq=st["rseq"])
         return [st["q_out"], st["k_out"], st["v_out"]]
     one = c["new"] == 1
