@@ -27,7 +27,8 @@ EXPORTS = ("sfx_status_str", "sfx_abi_version", "sfx_predict_ws", "sfx_predict",
            "sfx_topk_now_update", "sfx_hot_update", "sfx_count_active", "sfx_select_kth_ws",
            "sfx_select_kth", "sfx_hot_first_order_ws", "sfx_hot_first_order", "sfx_gather_rows",
            "sfx_dense_ffn_ws", "sfx_dense_ffn", "sfx_linear_q4", "sfx_kv_cache_bytes", "sfx_kv_append_q4",
-           "sfx_kv_read_q4", "sfx_kv_lens_q4", "sfx_attn_q4_ws", "sfx_attn_q4")
+           "sfx_kv_read_q4", "sfx_kv_lens_q4", "sfx_attn_q4_ws", "sfx_attn_q4", "sfx_norm_q8", "sfx_linear_q8",
+           "sfx_kv_cache_q8_bytes", "sfx_kv_append_q8", "sfx_kv_read_q8", "sfx_attn_q8_ws", "sfx_attn_q8")
 HOT_MAX_MATS = 8
 SFX_DOWN_SCRATCH_BYTES = 17 << 20
 
@@ -132,6 +133,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sfx_attn_q4_ws.argtypes = [I, I, I, I, I]
     lib.sfx_attn_q4.restype = I
     lib.sfx_attn_q4.argtypes = [P, I, I, I, I, I, P, Z, I, P, I, I, P, P, P, F, P, P, P, Z]
+    lib.sfx_norm_q8.restype = I
+    lib.sfx_norm_q8.argtypes = [P, I, I, I, I, I, I, F, P, Z, P, Z, P, Z, P, P, P, P, Z]
+    lib.sfx_linear_q8.restype = I
+    lib.sfx_linear_q8.argtypes = [P, I, I, I, I, P, Z, P, P, P, P, I, P, Z]
+    lib.sfx_kv_cache_q8_bytes.restype = Z
+    lib.sfx_kv_cache_q8_bytes.argtypes = [I, I, I, I]
+    lib.sfx_kv_append_q8.restype = I
+    lib.sfx_kv_append_q8.argtypes = [P, I, I, I, I, I, I, P, Z, P, Z, P, Z, P, P, P, I, I, I, I, I, P, I, I, P, P]
+    lib.sfx_kv_read_q8.restype = I
+    lib.sfx_kv_read_q8.argtypes = [P, I, I, I, I, P, P, I, I, P, I, I, P, P, P]
+    lib.sfx_attn_q8_ws.restype = Z
+    lib.sfx_attn_q8_ws.argtypes = [I, I, I, I, I, I]
+    lib.sfx_attn_q8.restype = I
+    lib.sfx_attn_q8.argtypes = [P, I, I, I, I, I, I, I, P, Z, P, I, P, I, I, P, P, P, I, F, P, P, P, Z]
     _lib = lib
     return lib
 
@@ -759,6 +774,243 @@ def sfx_attn_q4(q, cache, table, lens, out, ws, starts=None, scale=None, lse=Non
              table.data_ptr(), page, num_pages, cache.data_ptr(),
              None if starts is None else _tokens(starts, B, dev, w, "starts"), _tokens(lens, B, dev, w, "lens"),
              D ** -0.5 if scale is None else float(scale), out.data_ptr(), pl, pw, nws), w)
+
+
+# ------------------------------------------------------------------------- 8-bit layer half
+
+_I8 = torch.int8
+
+
+def _dense(t, dtype, dev, w, name):
+    """Pointer of a contiguous tensor of `dtype` on `dev`."""
+    if t.dtype is not dtype or not t.is_contiguous():
+        _not_dense(w, t, name, dtype)
+    if t.get_device() != dev:
+        _device_error(w, t)
+    return t.data_ptr()
+
+
+def sfx_norm_q8(x, q=None, s=None, weight=None, eps=1e-5, residual=None, residual_out=None, y=None, norm=True, stream=None):
+    """h = x + residual (written to residual_out, in place if that is None); n = h's
+    root-mean-square norm times `weight` (norm=False: n = h); int8 codes q [T][d] with a scale
+    s [T] per row, and / or y = n.  x, residual and y [T][d] fp32, fp16 or bf16 (rows may be
+    apart), weight [d] fp32."""
+    w = "sfx_norm_q8"
+    if x.dim() != 2:
+        raise ValueError(f"{w}: x must be [T][d]")
+    T, d = shape = x.shape
+    if x.dtype not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {x.dtype}")
+    dev = x.get_device()
+    if dev < 0:
+        _device_error(w, x)
+    rdt = ydt = ldr = ldro = ldy = 0
+    pr = pro = py = pq = ps = pw = None
+    if residual is not None:
+        ro = residual if residual_out is None else residual_out
+        if residual.shape != shape or ro.shape != shape or ro.dtype is not residual.dtype:
+            raise ValueError(f"{w}: residual and residual_out must be [{T}][{d}] of one dtype")
+        if residual.dtype not in WDT:
+            raise TypeError(f"{w}: unsupported dtype {residual.dtype}")
+        if residual.get_device() != dev or ro.get_device() != dev:
+            _device_error(w, x, residual, ro)
+        rdt, pr, pro = WDT[residual.dtype], residual.data_ptr(), ro.data_ptr()
+        ldr, ldro = _rows(residual, w, "residual"), _rows(ro, w, "residual_out")
+    elif residual_out is not None:
+        raise ValueError(f"{w}: residual_out without a residual")
+    if y is not None:
+        if y.shape != shape:
+            raise ValueError(f"{w}: y must be [{T}][{d}]")
+        if y.dtype not in WDT:
+            raise TypeError(f"{w}: unsupported dtype {y.dtype}")
+        if y.get_device() != dev:
+            _device_error(w, x, y)
+        ydt, py, ldy = WDT[y.dtype], y.data_ptr(), _rows(y, w, "y")
+    if (q is None) != (s is None):
+        raise ValueError(f"{w}: q and s go together")
+    if q is not None:
+        if q.shape != shape or s.numel() != T:
+            raise ValueError(f"{w}: q must be [{T}][{d}] and s hold {T} values")
+        pq, ps = _dense(q, _I8, dev, w, "q"), _dense(s, _FP32, dev, w, "s")
+    if weight is not None:
+        if weight.numel() != d:
+            raise ValueError(f"{w}: weight must hold {d} values")
+        pw = _dense(weight, _FP32, dev, w, "weight")
+    _run_on(dev, stream, (_lib or load()).sfx_norm_q8,
+            (WDT[x.dtype], rdt, ydt, T, d, 1 if norm else 0, eps, x.data_ptr(), _rows(x, w, "x"), pr, ldr, pro, ldro, pw,
+             pq, ps, py, ldy), w)
+
+
+def sfx_linear_q8(x, x_scales, W, W_scales, y, bias=None, accumulate=False, stream=None):
+    """y [T][n] (+)= (x_scales x) (W_scales W)^T + bias for int8 x [T][d] and W [n][d] with fp32
+    scales [T] and [n]; y fp32, fp16 or bf16.  The rows of x and y may be apart."""
+    w = "sfx_linear_q8"
+    if x.dim() != 2 or W.dim() != 2 or y.dim() != 2:
+        raise ValueError(f"{w}: x, W and y must be 2-D")
+    T, d = x.shape
+    n = W.shape[0]
+    if W.shape[1] != d or y.shape != (T, n) or x_scales.numel() != T or W_scales.numel() != n:
+        raise ValueError(f"{w}: shape mismatch")
+    if x.dtype is not _I8:
+        raise TypeError(f"{w}: x is {x.dtype}, expected {_I8}")
+    if y.dtype not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {y.dtype}")
+    dev = x.get_device()
+    if dev < 0 or y.get_device() != dev:
+        _device_error(w, x, y)
+    pb = None
+    if bias is not None:
+        if bias.numel() != n:
+            raise ValueError(f"{w}: bias must hold {n} values")
+        pb = _dense(bias, _FP32, dev, w, "bias")
+    _run_on(dev, stream, (_lib or load()).sfx_linear_q8,
+            (WDT[y.dtype], T, n, d, x.data_ptr(), d if x.is_contiguous() else _rows(x, w, "x"),
+             _dense(x_scales, _FP32, dev, w, "x_scales"), _dense(W, _I8, dev, w, "W"),
+             _dense(W_scales, _FP32, dev, w, "W_scales"), pb, 1 if accumulate else 0, y.data_ptr(),
+             n if y.is_contiguous() else _rows(y, w, "y")), w)
+
+
+def kv_cache_q8(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> torch.Tensor:
+    """Uninitialised int8 key/value cache of one layer: uint8 [num_pages][Hkv][page/16][32 D + 16]."""
+    if load().sfx_kv_cache_q8_bytes(Hkv, D, page, num_pages) == 0:
+        raise SfxError(-2, "kv_cache_q8")
+    return torch.empty(num_pages, Hkv, page // 16, 32 * D + 16, dtype=torch.uint8, device=device)
+
+
+def _cache8_shape(cache, table, D, Hkv, w):
+    """(page, num_pages, max_pages, B) of an int8 cache and its page table."""
+    if cache.dim() != 4 or table.dim() != 2:
+        raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/16][{32 * D + 16}], table [B][max pages]")
+    num_pages, hc, blocks, size = cache.shape
+    if hc != Hkv or size != 32 * D + 16:
+        raise ValueError(f"{w}: cache must be [pages][{Hkv}][page/16][{32 * D + 16}]")
+    if cache.dtype is not _U8 or not cache.is_contiguous():
+        _not_dense(w, cache, "cache", _U8)
+    if table.dtype is not _I32 or not table.is_contiguous():
+        _not_dense(w, table, "table", _I32)
+    B, max_pages = table.shape
+    return blocks * 16, num_pages, max_pages, B
+
+
+def sfx_kv_append_q8(q, k, v, lens, table, cache, q_out, q_start=None, cos_sin=None, interleaved=False, stream=None):
+    """Rotate q [T][Hq][D] and k [T][Hkv][D] by the angles of `cos_sin` [max_pos][rot], store k and
+    v as int8 at the last positions of the sequences (rows q_start[b] .. q_start[b + 1] - 1 of
+    sequence b, which has lens[b] positions with them; without q_start one row each) and
+    write the rotated queries to q_out (fp16 / bf16).  q and q_out may be None."""
+    w = "sfx_kv_append_q8"
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"{w}: k and v must be [T][Hkv][D]")
+    shape = k.shape
+    T, Hkv, D = shape
+    xdt = k.dtype
+    if v.shape != shape or v.dtype is not xdt:
+        raise ValueError(f"{w}: k and v must have one shape and dtype")
+    if xdt not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {xdt}")
+    dev = k.get_device()
+    if dev < 0 or v.get_device() != dev or table.get_device() != dev or cache.get_device() != dev:
+        _device_error(w, k, v, table, cache)
+    Hq, ldq, pq, pqo, qdt = 0, 0, None, None, 0
+    if q is not None:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != D or q.dtype is not xdt:
+            raise ValueError(f"{w}: q must be [{T}][Hq][{D}] in k's dtype")
+        Hq = shape[1]
+        if q_out is None or q_out.shape != shape:
+            raise ValueError(f"{w}: q_out must have q's shape")
+        odt = q_out.dtype
+        if odt is not _F16 and odt is not _BF16:
+            raise TypeError(f"{w}: q_out must be fp16 or bf16")
+        qdt = SFX_F16 if odt is _F16 else SFX_BF16
+        if q.get_device() != dev:
+            _device_error(w, k, q)
+        pq, ldq, pqo = q.data_ptr(), _head_rows(q, w, "q"), _dense(q_out, odt, dev, w, "q_out")
+    rot, max_pos, pcs = 0, 0, None
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError(f"{w}: cos_sin must be [positions][rot]")
+        pcs = _dense(cos_sin, _FP32, dev, w, "cos_sin")
+        max_pos, rot = cos_sin.shape
+    page, num_pages, max_pages, B = _cache8_shape(cache, table, D, Hkv, w)
+    _run_on(dev, stream, (_lib or load()).sfx_kv_append_q8,
+            (WDT[xdt], qdt, T, Hq, Hkv, D, pq, ldq, k.data_ptr(), _head_rows(k, w, "k"), v.data_ptr(),
+             _head_rows(v, w, "v"), None if q_start is None else _tokens(q_start, B + 1, dev, w, "q_start"),
+             _tokens(lens, B, dev, w, "lens"), pcs, rot, max_pos, 1 if interleaved else 0, B, max_pages,
+             table.data_ptr(), page, num_pages, cache.data_ptr(), pqo), w)
+
+
+def sfx_kv_read_q8(pos, table, cache, k_out, v_out, seq=None, stream=None):
+    """Values held at (seq[t], pos[t]): k_out, v_out [T][Hkv][D] (fp32, fp16 or bf16)."""
+    w = "sfx_kv_read_q8"
+    odt, shape = k_out.dtype, k_out.shape
+    if len(shape) != 3 or v_out.shape != shape or v_out.dtype is not odt:
+        raise ValueError(f"{w}: k_out and v_out must be [T][Hkv][D] of one dtype")
+    if odt not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {odt}")
+    if not k_out.is_contiguous() or not v_out.is_contiguous():
+        raise ValueError(f"{w}: k_out and v_out must be contiguous")
+    T, Hkv, D = shape
+    dev = k_out.get_device()
+    if dev < 0 or v_out.get_device() != dev or table.get_device() != dev or cache.get_device() != dev:
+        _device_error(w, k_out, v_out, table, cache)
+    page, num_pages, max_pages, B = _cache8_shape(cache, table, D, Hkv, w)
+    _run_on(dev, stream, (_lib or load()).sfx_kv_read_q8,
+            (WDT[odt], T, Hkv, D, _tokens(pos, T, dev, w, "pos"),
+             None if seq is None else _tokens(seq, T, dev, w, "seq"), B, max_pages, table.data_ptr(), page,
+             num_pages, cache.data_ptr(), k_out.data_ptr(), v_out.data_ptr()),
+            w)
+
+
+def sfx_attn_q8_ws(B: int, max_q: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    """Workspace bytes of sfx_attn_q8 for page tables of up to `max_len` positions."""
+    return load().sfx_attn_q8_ws(B, max_q, Hq, Hkv, D, max_len)
+
+
+def sfx_attn_q8(q, cache, table, lens, out, ws, q_start=None, max_q=1, starts=None, window=0, scale=None, lse=None,
+                stream=None):
+    """Causal attention of the last tokens of each sequence over the int8 cache: q [T][Hq][D]
+    (fp16 / bf16, tokens may be apart), rows q_start[b] .. q_start[b + 1] - 1 (at most max_q) of
+    sequence b with lens[b] positions; without q_start one row each.  out [T][Hq][D] in q's
+    dtype; `window` positions back (0: all), none before starts[b]; scale defaults to
+    D ** -0.5; lse [T][Hq] fp32 optional."""
+    w = "sfx_attn_q8"
+    if q.dim() != 3 or cache.dim() != 4:
+        raise ValueError(f"{w}: q must be [T][Hq][D], cache [pages][Hkv][page/16][32 D + 16]")
+    shape = q.shape
+    T, Hq, D = shape
+    qdt = q.dtype
+    if qdt is not _F16 and qdt is not _BF16:
+        raise TypeError(f"{w}: q must be fp16 or bf16")
+    if out.shape != shape:
+        raise ValueError(f"{w}: out must have q's shape")
+    if out.dtype is not qdt or not out.is_contiguous():
+        _not_dense(w, out, "out", qdt)
+    Hkv = cache.shape[1]
+    page, num_pages, max_pages, B = _cache8_shape(cache, table, D, Hkv, w)
+    if q_start is None and B != T:
+        raise ValueError(f"{w}: table must have {T} rows")
+    dev = q.get_device()
+    if dev < 0 or cache.get_device() != dev or table.get_device() != dev or out.get_device() != dev:
+        _device_error(w, q, cache, table, out)
+    pl = pw = None
+    nws = 0
+    if lse is not None:
+        if lse.shape != (T, Hq):
+            raise ValueError(f"{w}: lse must be [{T}][{Hq}]")
+        pl = _dense(lse, _FP32, dev, w, "lse")
+    if ws is not None:
+        if ws.get_device() != dev:
+            _device_error(w, q, ws)
+        if not ws.is_contiguous():
+            raise ValueError(f"{w}: ws must be contiguous")
+        pw, nws = ws.data_ptr(), ws.nbytes
+    _run_on(dev, stream, (_lib or load()).sfx_attn_q8,
+            (SFX_F16 if qdt is _F16 else SFX_BF16, T, B, max_q, Hq, Hkv, D, q.data_ptr(),
+             Hq * D if q.is_contiguous() else _head_rows(q, w, "q"),
+             None if q_start is None else _tokens(q_start, B + 1, dev, w, "q_start"), max_pages,
+             table.data_ptr(), page, num_pages, cache.data_ptr(),
+             None if starts is None else _tokens(starts, B, dev, w, "starts"), _tokens(lens, B, dev, w, "lens"),
+             window, D ** -0.5 if scale is None else float(scale), out.data_ptr(), pl, pw, nws), w)
 
 
 STREAM_READ_OUT_WORDS = 16384

@@ -3,11 +3,7 @@
 //   k' = R(pos) k,  s = fp16(max |k'| / 7) per 32 dims,  q = clamp(rne(k' / s), -8, 7)
 //   v alike without the rotation;  q_out = R(pos) q
 //
-// R turns pairs of the first `rot` dims by the angles whose cosines and sines the caller's
-// fp32 table holds for the position.  The two products and their sum are taken in 64 bits
-// (the products are exact there) and rounded once to fp32: a quotient next to a rounding
-// border then falls the same way wherever it is computed.  max / 7 and k' / s are
-// correctly rounded fp32 quotients.
+// The rotation is that of sfx_turn.hpp; max / 7 and k' / s are correctly rounded fp32 quotients.
 //
 // Both move mostly the 16- or 32-bit rows they read or write; of a thread's 28 vector loads in a
 // bf16 prompt's append 16 are 4-byte loads of the angle table.  Measured (one MI355X): 4095
@@ -16,152 +12,22 @@
 // chain from position to page to data.  Reading 16384 positions of 8 heads of 128 back: 19 us
 // for 86 MB (34 with a wave per head and token).  Eight tokens: 4.2 and 2.2 us, launch latency.
 #include <algorithm>
-#include <type_traits>
 
 #include "sfx_kv.hpp"
 #include "sfx_launch.hpp"
-#include "sfx_q4.hpp"
+#include "sfx_turn.hpp"
 
 namespace sfx {
 namespace {
 
-template <int DT>
-__device__ __forceinline__ float load_elem(const void* p, size_t i) {
-  if constexpr (DT == DT_F32) return ((const float*)p)[i];
-  else if constexpr (DT == DT_F16) return (float)((const _Float16*)p)[i];
-  else return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
-}
-template <int DT>
-__device__ __forceinline__ void store_elem(void* p, size_t i, float v) {
-  if constexpr (DT == DT_F32) ((float*)p)[i] = v;
-  else if constexpr (DT == DT_F16) ((_Float16*)p)[i] = (_Float16)v;
-  else ((__bf16*)p)[i] = (__bf16)v;
-}
-
-struct AppendArgs {
+struct AppendArgs : Rotation {
   KvCache kv;
   const void *q, *k, *v;
   size_t ldq, ldk, ldv;     // elements between tokens
   const int32_t *pos, *seq;
-  const float* cs;          // [max_pos][rot]: cosines, then sines
   void* q_out;
-  int T, Hq, rot, max_pos, pairs;
+  int T, Hq;
 };
-
-// Eight consecutive elements as they lie; VEC: at 16-byte aligned places.
-template <int DT>
-struct Eight {
-  Raw<16> r[DT == DT_F32 ? 2 : 1];
-};
-template <int DT, bool VEC>
-__device__ __forceinline__ Eight<DT> load8(const void* p, size_t i) {
-  Eight<DT> e;
-  if constexpr (VEC) {
-    const uint8_t* q = (const uint8_t*)p + i * (DT == DT_F32 ? 4 : 2);
-    e.r[0] = load_raw<16>(q);
-    if constexpr (DT == DT_F32) e.r[1] = load_raw<16>(q + 16);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (DT == DT_F32) {
-        e.r[j >> 2].w[j & 3] = ((const uint32_t*)p)[i + j];
-      } else {
-        const uint32_t v = ((const uint16_t*)p)[i + j];
-        e.r[0].w[j >> 1] = (j & 1) ? e.r[0].w[j >> 1] | (v << 16) : v;
-      }
-    }
-  }
-  return e;
-}
-template <int DT>
-__device__ __forceinline__ void widen(const Eight<DT>& e, float (&x)[8]) {
-  if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(e.r[j >> 2].w[j & 3]);
-  } else if constexpr (DT == DT_F16) {
-    unpack<TF16, 4>(e.r[0].w, x);
-  } else {
-    unpack<TBF16, 4>(e.r[0].w, x);
-  }
-}
-
-// x co + turn in 64 bits, where the product and the sum's operands are exact, rounded once.
-// The fp32 value is what is rounded on to 16 bits or quantised: the copy keeps the compiler
-// from converting the 64-bit sum to 16 bits directly.
-__device__ __forceinline__ float turned(float x, float o, float co, float si, bool first) {
-  const double turn = (double)o * (double)si;
-  float y = (float)((double)x * (double)co + (first ? -turn : turn));
-  asm volatile("" : "+v"(y));
-  return y;
-}
-
-template <int DT>
-__device__ __forceinline__ void store8(void* p, size_t i, const float (&x)[8]) {
-  Raw<16> r;
-  if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.w[j] = __float_as_uint(x[4 * k + j]);
-      *(Raw<16>*)((float*)p + i + 4 * k) = r;
-    }
-  } else {
-    using T = std::conditional_t<DT == DT_F16, TF16, TBF16>;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)to_16(T{}, x[2 * j]) | ((uint32_t)to_16(T{}, x[2 * j + 1]) << 16);
-    *(Raw<16>*)((uint16_t*)p + i) = r;
-  }
-}
-
-// What turns a thread's dims d0 .. d0 + 7 at one position: cosine and sine per dim, whether it
-// is the first of its pair, and where the other one is.
-struct Turn {
-  float co[8], si[8];
-};
-__device__ __forceinline__ int turn_pair(const AppendArgs& a, int d) { return a.pairs ? d >> 1 : d < (a.rot >> 1) ? d : d - (a.rot >> 1); }
-__device__ __forceinline__ bool turn_first(const AppendArgs& a, int d) { return a.pairs ? (d & 1) == 0 : d < (a.rot >> 1); }
-__device__ __forceinline__ int turn_other(const AppendArgs& a, int d) {
-  return a.pairs ? d ^ 1 : d < (a.rot >> 1) ? d + (a.rot >> 1) : d - (a.rot >> 1);
-}
-__device__ __forceinline__ void load_turn(const AppendArgs& a, const float* cs, int d0, Turn& t) {
-  const int half = a.rot >> 1;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int i = min(turn_pair(a, d0 + j), half - 1);         // dims past rot are not turned
-    t.co[j] = cs[i];
-    t.si[j] = cs[half + i];
-  }
-}
-// Where the slice's partners lie, for a whole slice of them in another place.
-__device__ __forceinline__ bool turn_apart(const AppendArgs& a, int d0) { return a.cs && !a.pairs && d0 < a.rot; }
-
-// VEC: the first `rot` dims and their halves are whole slices of 8.
-template <int DT, bool VEC>
-__device__ __forceinline__ void turn8(const AppendArgs& a, const void* p, size_t head, int d0, const Eight<DT>& own,
-                                      const Eight<DT>& apart, const Turn& t, float (&y)[8]) {
-  float x[8];
-  widen<DT>(own, x);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = x[j];
-  if (!a.cs || d0 >= a.rot) return;
-  if constexpr (VEC) {
-    if (a.pairs) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = turned(x[j], x[j ^ 1], t.co[j], t.si[j], (j & 1) == 0);
-    } else {
-      float o[8];
-      widen<DT>(apart, o);
-      const bool first = d0 < (a.rot >> 1);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = turned(x[j], o[j], t.co[j], t.si[j], first);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (d0 + j < a.rot)
-        y[j] = turned(x[j], load_elem<DT>(p, head + turn_other(a, d0 + j)), t.co[j], t.si[j], turn_first(a, d0 + j));
-  }
-}
 
 // Scale (fp16 bits) and the codes u = q + 8, one per nibble of the result in element order;
 // the 4 lanes of a quad hold one group of 32.  A group with a NaN or an infinity takes a NaN
@@ -376,8 +242,8 @@ hipError_t launch_kv_append_q4(hipStream_t s, const KvGeom& g, int xdt, int qdt,
                                const void* k, size_t ldk, const void* v, size_t ldv, const int32_t* pos,
                                const int32_t* seq, const float* cos_sin, int rot, int max_pos, int pairs,
                                const int32_t* table, void* cache, void* q_out) {
-  const AppendArgs a{make_cache(g, cache, table), q, k, v, ldq, ldk, ldv, pos, seq, cos_sin, q_out, T, Hq, rot,
-                     max_pos, pairs};
+  const AppendArgs a{{cos_sin, rot, max_pos, pairs}, make_cache(g, cache, table), q, k, v, ldq, ldk, ldv, pos, seq,
+                     q_out, T, Hq};
   const uintptr_t row = xdt == DT_F32 ? 4 : 8;                  // elements of 16 bytes
   const bool vec = (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 15u) == 0 &&
                    ((ldq | ldk | ldv) & (row - 1)) == 0 && (!cos_sin || (pairs ? rot % 8 == 0 : rot % 16 == 0));

@@ -48,6 +48,25 @@ size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D) {
   return (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 4) * 4;
 }
 
+// Runs per tile of 16 rows: two workgroups of eight waves per compute unit, and no run shorter
+// than a tile of positions per wave.
+Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int max_len) {
+  Attn8Plan p;
+  p.Hq = Hq;
+  p.G = Hq / Hkv;
+  p.RT = (int)(((long long)max_q * p.G + 15) / 16);
+  const long long units = (long long)B * Hkv * p.RT;
+  const int most = (max_len + 255) / 256;
+  p.S = units >= 512 ? 1 : (int)((512 + units - 1) / units);
+  if (p.S > most) p.S = most;
+  return p;
+}
+
+size_t attn8_ws_bytes(const Attn8Plan& p, int B, int Hkv, int D) {
+  if (p.S <= 1) return 0;
+  return (size_t)B * Hkv * p.RT * p.S * 16 * (D + 2) * 4;
+}
+
 }  // namespace sfx
 
 namespace {
@@ -89,6 +108,15 @@ int kv_geom(int B, int Hkv, int D, int page, int num_pages, int max_pages, sfx::
   *g = sfx::KvGeom{B, Hkv, D, __builtin_ctz((unsigned)page), num_pages, max_pages};
   return SFX_OK;
 }
+
+// The same of an int8 cache (blocks of 16 positions; q4's limits hold for it too).
+int kv_geom8(int B, int Hkv, int D, int page, int num_pages, int max_pages, sfx::KvGeom* g) {
+  if (page < 16 || B > sfx::kQ8MaxSeqs) return SFX_E_SHAPE;
+  return kv_geom(B, Hkv, D, page, num_pages, max_pages, g);
+}
+
+bool dt16_or_32(int dt) { return dt == SFX_F32 || dt == SFX_F16 || dt == SFX_BF16; }
+bool aligned_elem(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(elem_bytes(dt) - 1)) == 0; }
 
 }  // namespace
 
@@ -500,6 +528,113 @@ int sfx_attn_q4(void* stream, int qdt, int B, int Hq, int Hkv, int D, const void
   const auto f = qdt == SFX_F16 ? sfx::launch_attn_q4_f16 : sfx::launch_attn_q4_bf16;
   return launch_status(f((hipStream_t)stream, p, g, q, ldq * 2, cache, table, starts, lens, scale * 1.44269504088896341f,
                          out, lse, ws));
+}
+
+// ------------------------------------------------------------------------------ 8-bit layer half
+
+int sfx_norm_q8(void* stream, int xdt, int rdt, int ydt, int T, int d, int norm, float eps, const void* x, size_t ldx,
+                const void* res, size_t ldr, void* res_out, size_t ldro, const float* weight, int8_t* q, float* s, void* y,
+                size_t ldy) {
+  if (!dt16_or_32(xdt) || (res && !dt16_or_32(rdt)) || (y && !dt16_or_32(ydt))) return SFX_E_DTYPE;
+  if (T < 1 || T > sfx::kQ8MaxTokens || d < 1 || d > (1 << 24)) return SFX_E_SHAPE;
+  if (norm && !(eps > 0.f && eps < INFINITY)) return SFX_E_SHAPE;
+  if ((!norm && weight) || (!res && res_out) || (q == nullptr) != (s == nullptr)) return SFX_E_SHAPE;
+  if (ldx < (size_t)d || (res && ldr < (size_t)d) || (res_out && ldro < (size_t)d) || (y && ldy < (size_t)d)) return SFX_E_SHAPE;
+  if (!x || (!q && !y && !res_out)) return SFX_E_NULL;
+  if (!aligned_elem(x, xdt) || (res && (!aligned_elem(res, rdt) || !aligned_elem(res_out, rdt))) || (y && !aligned_elem(y, ydt)))
+    return SFX_E_ALIGN;
+  if ((weight && !aligned4(weight)) || (q && !aligned16(q)) || (s && !aligned4(s))) return SFX_E_ALIGN;
+  return launch_status(sfx::launch_norm_q8((hipStream_t)stream, xdt, rdt, ydt, T, d, norm != 0, eps, x, ldx, res, ldr, res_out,
+                                           ldro, weight, q, s, y, ldy));
+}
+
+int sfx_linear_q8(void* stream, int ydt, int T, int n, int d, const int8_t* x, size_t ldx, const float* x_scales,
+                  const int8_t* W, const float* W_scales, const float* bias, int accumulate, void* y, size_t ldy) {
+  if (!dt16_or_32(ydt)) return SFX_E_DTYPE;
+  if (T < 1 || T > sfx::kQ8MaxTokens || n < 1 || n > (1 << 24) || d < 16 || d > 131056 || d % 16 != 0) return SFX_E_SHAPE;
+  if (ldx < (size_t)d || ldy < (size_t)n) return SFX_E_SHAPE;
+  if (!x || !x_scales || !W || !W_scales || !y) return SFX_E_NULL;
+  if (!aligned16(x) || !aligned16(W) || ldx % 16 != 0 || !aligned_elem(y, ydt)) return SFX_E_ALIGN;
+  if (!aligned4(x_scales) || !aligned4(W_scales) || (bias && !aligned4(bias))) return SFX_E_ALIGN;
+  return launch_status(sfx::launch_linear_q8((hipStream_t)stream, ydt, T, n, d, x, ldx, x_scales, W, W_scales, bias,
+                                             accumulate != 0, y, ldy));
+}
+
+size_t sfx_kv_cache_q8_bytes(int Hkv, int D, int page, int num_pages) {
+  sfx::KvGeom g;
+  if (kv_geom8(1, Hkv, D, page, num_pages, 1, &g) != SFX_OK) return 0;
+  return (size_t)num_pages * Hkv * (page / 16) * (32 * (size_t)D + 16);
+}
+
+int sfx_kv_append_q8(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int D, const void* q, size_t ldq,
+                     const void* k, size_t ldk, const void* v, size_t ldv, const int32_t* q_start, const int32_t* lens,
+                     const float* cos_sin, int rot, int max_pos, int interleaved, int B, int max_pages,
+                     const int32_t* table, int page, int num_pages, void* cache, void* q_out) {
+  if (!dt16_or_32(xdt)) return SFX_E_DTYPE;
+  if (q && qdt != SFX_F16 && qdt != SFX_BF16) return SFX_E_DTYPE;
+  sfx::KvGeom g;
+  const int st = kv_geom8(B, Hkv, D, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (T < 1 || T > sfx::kQ8MaxTokens || (!q_start && T != B)) return SFX_E_SHAPE;
+  if (q && (Hq < 1 || Hq > sfx::kAttnMaxHeads || ldq < (size_t)Hq * D)) return SFX_E_SHAPE;
+  if (ldk < (size_t)Hkv * D || ldv < (size_t)Hkv * D) return SFX_E_SHAPE;
+  if (cos_sin && (rot < 2 || rot > D || rot % 2 != 0 || max_pos < 1)) return SFX_E_SHAPE;
+  // workgroups of 256 threads, and a launch holds fewer than 2^32 threads
+  if (sfx::kv_append_q8_groups(g, T, q != nullptr) >= (1 << 24)) return SFX_E_SHAPE;
+  if (!k || !v || !lens || !table || !cache || (q && !q_out)) return SFX_E_NULL;
+  if (!aligned_elem(k, xdt) || !aligned_elem(v, xdt) || !aligned_elem(q, xdt) || !aligned16(cache) || ((uintptr_t)q_out & 1u))
+    return SFX_E_ALIGN;
+  if (!aligned4(lens) || !aligned4(table) || (q_start && !aligned4(q_start)) || (cos_sin && !aligned4(cos_sin)))
+    return SFX_E_ALIGN;
+  return launch_status(sfx::launch_kv_append_q8((hipStream_t)stream, g, xdt, qdt, T, q ? Hq : 0, q, ldq, k, ldk, v, ldv,
+                                                q_start, lens, cos_sin, rot, max_pos, interleaved != 0, table, cache, q_out));
+}
+
+int sfx_kv_read_q8(void* stream, int odt, int T, int Hkv, int D, const int32_t* pos, const int32_t* seq, int B,
+                   int max_pages, const int32_t* table, int page, int num_pages, const void* cache, void* k, void* v) {
+  if (!dt16_or_32(odt)) return SFX_E_DTYPE;
+  sfx::KvGeom g;
+  const int st = kv_geom8(B, Hkv, D, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (T < 1 || T > sfx::kQ8MaxTokens) return SFX_E_SHAPE;
+  if (!pos || !table || !cache || !k || !v) return SFX_E_NULL;
+  if (!aligned16(cache) || !aligned16(k) || !aligned16(v)) return SFX_E_ALIGN;
+  if (!aligned4(pos) || !aligned4(table) || (seq && !aligned4(seq))) return SFX_E_ALIGN;
+  return launch_status(sfx::launch_kv_read_q8((hipStream_t)stream, g, odt, T, pos, seq, table, cache, k, v));
+}
+
+static bool attn8_shape(int B, int max_q, int Hq, int Hkv) {
+  return B >= 1 && B <= sfx::kQ8MaxSeqs && max_q >= 1 && max_q <= sfx::kQ8MaxTokens && Hkv >= 1 && Hq >= 1 &&
+         Hq <= sfx::kAttnMaxHeads && Hq % Hkv == 0 && (long long)max_q * (Hq / Hkv) <= (1 << 26);
+}
+
+size_t sfx_attn_q8_ws(int B, int max_q, int Hq, int Hkv, int D, int max_len) {
+  if (!attn8_shape(B, max_q, Hq, Hkv) || D < 32 || D > 256 || D % 32 != 0 || max_len < 1 || max_len > (1 << 30)) return 0;
+  return sfx::attn8_ws_bytes(sfx::attn8_plan(B, max_q, Hq, Hkv, max_len), B, Hkv, D);
+}
+
+int sfx_attn_q8(void* stream, int qdt, int T, int B, int max_q, int Hq, int Hkv, int D, const void* q, size_t ldq,
+                const int32_t* q_start, int max_pages, const int32_t* table, int page, int num_pages, const void* cache,
+                const int32_t* starts, const int32_t* lens, int window, float scale, void* out, float* lse, void* ws,
+                size_t ws_bytes) {
+  if (qdt != SFX_F16 && qdt != SFX_BF16) return SFX_E_DTYPE;
+  sfx::KvGeom g;
+  const int st = kv_geom8(B, Hkv, D, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (!attn8_shape(B, max_q, Hq, Hkv) || T < 1 || T > sfx::kQ8MaxTokens || ldq < (size_t)Hq * D) return SFX_E_SHAPE;
+  if (!q_start && (T != B || max_q != 1)) return SFX_E_SHAPE;
+  if (window < 0 || !(fabsf(scale) < 0x1p115f)) return SFX_E_SHAPE;
+  if (!q || !table || !cache || !lens || !out) return SFX_E_NULL;
+  if (!aligned16(q) || ldq % 8 != 0 || !aligned16(cache) || !aligned16(out)) return SFX_E_ALIGN;
+  if (!aligned4(table) || !aligned4(lens) || (starts && !aligned4(starts)) || (q_start && !aligned4(q_start)) ||
+      (lse && !aligned4(lse)))
+    return SFX_E_ALIGN;
+  const sfx::Attn8Plan p = sfx::attn8_plan(B, max_q, Hq, Hkv, max_pages * page);
+  const int w = check_ws(ws, ws_bytes, sfx::attn8_ws_bytes(p, B, Hkv, D));
+  if (w != SFX_OK) return w;
+  const auto f = qdt == SFX_F16 ? sfx::launch_attn_q8_f16 : sfx::launch_attn_q8_bf16;
+  return launch_status(f((hipStream_t)stream, p, g, T, max_q, q, ldq * 2, q_start, cache, table, starts, lens, window,
+                         scale * 1.44269504088896341f, out, lse, ws));
 }
 
 // ------------------------------------------------------------------------------ measurement helper

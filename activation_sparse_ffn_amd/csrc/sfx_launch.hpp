@@ -111,4 +111,35 @@ hipError_t launch_attn_q4_bf16(hipStream_t s, const AttnPlan& p, const KvGeom& g
                                const void* cache, const int32_t* table, const int32_t* starts, const int32_t* lens,
                                float k2, void* out, float* lse, void* ws);
 
+// The 8-bit layer half: rows (tokens) and sequences of a call.
+constexpr int kQ8MaxTokens = 1 << 20;
+constexpr int kQ8MaxSeqs = 4096;
+hipError_t launch_norm_q8(hipStream_t s, int xdt, int rdt, int ydt, int T, int d, int norm, float eps, const void* x,
+                          size_t ldx, const void* r, size_t ldr, void* r_out, size_t ldro, const float* w, int8_t* q,
+                          float* sc, void* y, size_t ldy);
+hipError_t launch_linear_q8(hipStream_t s, int ydt, int T, int n, int d, const int8_t* x, size_t ldx, const float* sx,
+                            const int8_t* W, const float* sw, const float* bias, int accumulate, void* y, size_t ldy);
+long long kv_append_q8_groups(const KvGeom& g, int T, bool queries);      // workgroups of the append
+hipError_t launch_kv_append_q8(hipStream_t s, const KvGeom& g, int xdt, int qdt, int T, int Hq, const void* q, size_t ldq,
+                               const void* k, size_t ldk, const void* v, size_t ldv, const int32_t* q_start,
+                               const int32_t* lens, const float* cos_sin, int rot, int max_pos, int pairs,
+                               const int32_t* table, void* cache, void* q_out);
+hipError_t launch_kv_read_q8(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
+                             const int32_t* table, const void* cache, void* k, void* v);
+
+// Attention over the int8 cache: query heads, per kv head, tiles of 16 rows, runs of a tile.
+struct Attn8Plan {
+  int Hq, G, RT, S;
+};
+Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int max_len);
+size_t attn8_ws_bytes(const Attn8Plan& p, int B, int Hkv, int D);
+hipError_t launch_attn_q8_f16(hipStream_t s, const Attn8Plan& p, const KvGeom& g, int T, int max_q, const void* q,
+                              size_t ldq_bytes, const int32_t* q_start, const void* cache, const int32_t* table,
+                              const int32_t* starts, const int32_t* lens, int window, float k2, void* out, float* lse,
+                              void* ws);
+hipError_t launch_attn_q8_bf16(hipStream_t s, const Attn8Plan& p, const KvGeom& g, int T, int max_q, const void* q,
+                               size_t ldq_bytes, const int32_t* q_start, const void* cache, const int32_t* table,
+                               const int32_t* starts, const int32_t* lens, int window, float k2, void* out, float* lse,
+                               void* ws);
+
 }  // namespace sfx

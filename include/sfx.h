@@ -16,6 +16,9 @@
  *                    offline calibration: thresholds, frequencies, hot-first order
  *   sfx_linear_q4, sfx_kv_append_q4, sfx_kv_read_q4, sfx_kv_lens_q4, sfx_attn_q4
  *                    the attention half of a layer: int4 projections, paged int4 cache
+ *   sfx_norm_q8, sfx_linear_q8, sfx_kv_append_q8, sfx_kv_read_q8, sfx_attn_q8
+ *                    the 8-bit layer half: norm to int8 rows, int8 projections, paged int8
+ *                    cache, attention of one or many tokens per sequence
  *
  * Conventions shared by every entry point
  *   - Every pointer argument is a caller-owned DEVICE pointer unless the comment
@@ -586,6 +589,110 @@ int sfx_attn_q4(void* stream, int qdt, int B, int Hq, int Hkv, int D, const void
                 int max_pages, const int32_t* table, int page, int num_pages, const void* cache,
                 const int32_t* starts, const int32_t* lens, float scale, void* out, float* lse,
                 void* ws, size_t ws_bytes);
+
+/* ---------------------------------------------------------------------------------
+ * The 8-bit layer half, for whole prompts as well as single tokens: residual addition with
+ * root-mean-square norm and int8 rows, the int8 projection, a paged int8 key/value cache, and
+ * attention of a sequence's last tokens over it.  T (rows of a call) is 1..2^20 here and B
+ * (sequences) 1..4096.
+ *
+ * sfx_norm_q8 -- h = x + res;  n = h / sqrt(mean h^2 + eps) * weight  (norm 0: n = h);
+ *   s = fp32(max |n| / 127),  q = clamp(rne(n / s), -127, 127) per row;  y = n;  res_out = h.
+ *   xdt, rdt, ydt   SFX_F32, SFX_F16 or SFX_BF16: x; res and res_out; y (of what is NULL: unused).
+ *   x, res, res_out, y  [T] rows of d elements, ldx / ldr / ldro / ldy elements apart, aligned to
+ *             their elements.  res NULL: h = x; res_out NULL: h is not stored; y NULL: n is not.
+ *             res_out may be res; any other overlap of what is written is not allowed.
+ *   weight    [d] fp32 or NULL (1; must be NULL if norm is 0).   eps   > 0 (norm 0: unused).
+ *   q, s      [T][d] int8, dense, and [T] fp32; both NULL: no int8 rows.
+ * d 1..2^24 (sfx_linear_q8 takes rows of a multiple of 16).  Sums, products and quotients are taken
+ * in 64 bits; y and res_out are rounded to fp32 and from there to their type.  The norm is that of the
+ * unrounded h.  A row of zeros has s = 0 and codes 0; so have rows whose s is below fp32's
+ * smallest number.  A row with a NaN, an infinity or a non-finite product with the weight takes s = NaN
+ * and codes 0.  No workspace.
+ *
+ * sfx_linear_q8 -- y[t][i] (+)= x_scales[t] W_scales[i] sum_c x[t][c] W[i][c] + bias[i].
+ *   x         [T] int8 rows of d codes, ldx apart (ldx a multiple of 16).  W [n][d] int8.
+ *   x_scales [T], W_scales [n], bias [n] or NULL: fp32.
+ *   accumulate  0: y is overwritten; otherwise the product is added to it, before it is rounded.
+ *   y         [T] rows of n elements of ydt (SFX_F32, SFX_F16, SFX_BF16), ldy apart.
+ * n 1..2^24, d a multiple of 16 in 16..131056: the sum of products is a 32-bit integer and exact; it
+ * is rounded to fp32 once and multiplied by the rounded product of the scales.  Bitwise
+ * reproducible, and a token's y does not depend on the other tokens.  No workspace.
+ * ------------------------------------------------------------------------------- */
+int sfx_norm_q8(void* stream, int xdt, int rdt, int ydt, int T, int d, int norm, float eps, const void* x, size_t ldx,
+                const void* res, size_t ldr, void* res_out, size_t ldro, const float* weight, int8_t* q, float* s,
+                void* y, size_t ldy);
+int sfx_linear_q8(void* stream, int ydt, int T, int n, int d, const int8_t* x, size_t ldx, const float* x_scales,
+                  const int8_t* W, const float* W_scales, const float* bias, int accumulate, void* y, size_t ldy);
+
+/* ---------------------------------------------------------------------------------
+ * Paged int8 key/value cache of one layer: sfx_kv_cache_q8_bytes(Hkv, D, page, num_pages) bytes of
+ * caller-owned device memory, 16-byte aligned, any contents at the start:
+ * [num_pages][Hkv][page/16] blocks of 32 D + 16 bytes, each 16 consecutive positions of one kv
+ * head: K codes [16][D], V codes [4][D][4] (byte i of dim d in quarter c is position 4c + i), the
+ * fp32 scale of K, that of V, 8 unused bytes.  A code is q + 128, a value q * scale.
+ * Hkv, D, table, max_pages and num_pages as for the int4 cache; page a power of two in 16..1024.
+ *
+ *   q_start, lens   [B + 1] and [B] int32: rows q_start[b] .. q_start[b + 1] - 1 of a call are the
+ *             last positions of sequence b, which has lens[b] of them (these rows among them):
+ *             row i of n is position lens[b] - n + i.  q_start must not fall; rows in front of
+ *             q_start[0] and from q_start[B] on belong to no sequence and are left alone.  q_start NULL: T = B, and
+ *             row b is sequence b's last position (lens[b] <= 0: no token).  sfx_kv_lens_q4 makes
+ *             the lens of a decode step for this cache too.
+ *
+ * sfx_kv_append_q8 -- rotates and stores T tokens.  With k' = R(pos) k, per block and kv head:
+ *   s = max(s_old, max |k'| / 127) over the block's new tokens,  q = rne(k' / s);
+ *   v alike, not rotated;  q_out = R(pos) q.
+ *   s_old is the block's scale so far, or 0 where the call stores the block's first position: that
+ *   starts the block anew (its positions that the call does not store become 0).  Otherwise the
+ *   block keeps its other positions; where s grows, their codes become rne(q s_old / s), which adds at
+ *   most half a step of s to a value each time.  Positions of a block must therefore be stored
+ *   from its first one on: what the block holds before them is taken as stored by earlier calls.
+ *   xdt, q, k, v, ldq, ldk, ldv, cos_sin, rot, max_pos, interleaved, q_out, qdt: as for
+ *             sfx_kv_append_q4.  Rows without a position, without a page or past the table of
+ *             angles are padding: not stored, their rows of q_out left as they were.
+ * The rotation is taken in 64 bits and rounded once to fp32; codes are those of exact quotients.  A
+ * block whose new tokens hold a NaN or an infinity takes a NaN scale, for all it holds, until it is
+ * started anew.  Calls that may run at the same time must not touch the same block, nor may two
+ * sequences of a call.  T and Hkv / D are limited together: the blocks of all heads that T rows
+ * of B sequences can touch stay below 2^24 (SFX_E_SHAPE).
+ *
+ * sfx_kv_read_q8 -- values of T listed positions: k, v [T][Hkv][D] in odt (SFX_F32 rounded once,
+ *   SFX_F16 / SFX_BF16 from there), written; zeros for a padding token (as in sfx_kv_read_q4).
+ *
+ * sfx_attn_q8 -- o[t][h] = sum_p w_p v_p,  w = softmax of scale q[t][h] . k_p over the positions
+ *   max(0, starts[b], pos + 1 - window) .. pos for row t at position pos of sequence b, with kv head
+ *   h / (Hq / Hkv): causal, and with a sliding window (0: none).
+ *   qdt       SFX_F16 or SFX_BF16 (q and out).   Hq 1..256, Hq % Hkv == 0.
+ *   q         [T][Hq][D], tokens ldq elements apart (a multiple of 8).
+ *   max_q     1..2^20, at least the most rows that a sequence has (rows past it are left out); 1
+ *             where q_start is NULL.  max_q Hq / Hkv <= 2^26.
+ *   starts    [B] int32 or NULL (0): left padding.  Nothing to attend to gives a zero row and
+ *             lse = -inf.  Positions without a page are left out; what the cache holds in blocks
+ *             none of whose positions a row covers, NaN included, does not matter to it.
+ *   out       [T][Hq][D] in qdt, dense; rows of no sequence are left as they were.
+ *   lse       [T][Hq] fp32 or NULL, as in sfx_attn_q4.
+ *   scale     |scale| < 2^115; the scores scale q . k stay below 2^126 in size.
+ *   ws        >= sfx_attn_q8_ws(B, max_q, Hq, Hkv, D, max_pages * page) bytes, any contents.  A
+ *             workspace used with several B or max_q has the largest size that any of them needs.
+ * Scores, sums and results are fp32, a weight is rounded once to fp16, down to 2^-33 of the largest
+ * contribution of a block's values; codes are exact.  Bitwise reproducible for the same shapes, lens and
+ * q_start.
+ * ------------------------------------------------------------------------------- */
+size_t sfx_kv_cache_q8_bytes(int Hkv, int D, int page, int num_pages);
+int sfx_kv_append_q8(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int D,
+                     const void* q, size_t ldq, const void* k, size_t ldk, const void* v, size_t ldv,
+                     const int32_t* q_start, const int32_t* lens, const float* cos_sin, int rot, int max_pos,
+                     int interleaved, int B, int max_pages, const int32_t* table, int page, int num_pages,
+                     void* cache, void* q_out);
+int sfx_kv_read_q8(void* stream, int odt, int T, int Hkv, int D, const int32_t* pos, const int32_t* seq,
+                   int B, int max_pages, const int32_t* table, int page, int num_pages,
+                   const void* cache, void* k, void* v);
+size_t sfx_attn_q8_ws(int B, int max_q, int Hq, int Hkv, int D, int max_len);
+int sfx_attn_q8(void* stream, int qdt, int T, int B, int max_q, int Hq, int Hkv, int D, const void* q, size_t ldq,
+                const int32_t* q_start, int max_pages, const int32_t* table, int page, int num_pages,
+                const void* cache, const int32_t* starts, const int32_t* lens, int window, float scale,
+                void* out, float* lse, void* ws, size_t ws_bytes);
 
 /* ---------------------------------------------------------------------------------
  * sfx_stream_read -- measurement helper, not a step of the method.  Reads the nbytes
