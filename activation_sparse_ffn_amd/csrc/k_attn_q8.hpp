@@ -165,6 +165,9 @@ __device__ __forceinline__ void tile8_run(const Tile8<NG>& t, const Raw<16> (&qf
   for (int m = 0; m < 2 * NG; ++m) st.acc[m] = Mma<TF16>::run(codes8(t.v[0][m], t.v[1][m]), p, st.acc[m]);
 }
 
+__device__ __forceinline__ int query8_exponent(float top) {
+  return top > 0.f && top < INFINITY ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 - 14 : 0;
+}
 // The row's eighths of queries for the score products, times 2^-e: returns 2^e.  A row that holds
 // an infinity or a NaN is taken as it is.
 template <class T, int NG>
@@ -177,8 +180,7 @@ __device__ __forceinline__ float query8(const uint8_t* row, bool real, int c, in
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[g][j]));
   }
-  top = quarters_max8(top, lane);
-  const int e = top > 0.f && top < INFINITY ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 - 14 : 0;
+  const int e = query8_exponent(quarters_max8(top, lane));
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -386,24 +388,217 @@ __global__ __launch_bounds__(256) void k_attn8_join(Attn8Args a) {
   }
 }
 
+// ---- many rows of a sequence.  A workgroup takes 256 rows, a wave 32 of them as the columns of
+// 32x32x16 products; 64 positions at a time go through LDS as fp16, decoded once for all waves: K as rows of
+// positions (16 bytes more than D numbers long: 16 lanes that read one piece of 16 rows meet all banks),
+// V as [block][c][dim] of the eight positions that lane quarter c of the second product holds.
+constexpr int kRows8 = 256, kTileR8 = 64;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x16 mma32(const Raw<16>& a, const Raw<16>& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+
 template <class T, int NG>
-hipError_t attn8_run(hipStream_t s, const Attn8Args& a) {
+__global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
+  constexpr int D = 32 * NG, kRow = 2 * D + 16, kK = kTileR8 * kRow, kV = kTileR8 * 2 * D, kPieces = 8 * D, PT = (kPieces + 511) / 512;
+  __shared__ __attribute__((aligned(16))) uint8_t mem[2][kK + kV];
+  __shared__ float4 consts[2][kTileR8 / kBlk8];                // of a block: ks k2, log2 vs, 1 / vs
+  const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, c = lane >> 5;
+  const int h = blockIdx.x % a.kv.Hkv, rt = a.RT - 1 - blockIdx.x / a.kv.Hkv, b = blockIdx.y;   // long tiles first
+  const Seq8 sq = rows8_seq(a.rows, b);
+  const int rows = min(kRows8, sq.n * a.G - kRows8 * rt);
+  if (rows <= 0) return;
+  const int start = a.starts ? max(a.starts[b], 0) : 0, first = sq.len - sq.n;
+  const int i0 = kRows8 * rt / a.G, i1 = (kRows8 * rt + rows - 1) / a.G;
+  const int p_lo = max(0, row8_lo(a, start, first + i0)), p_hi = min(first + i1 + 1, a.kv.max_pages << a.kv.page_shift);
+  const int t0 = p_lo / kTileR8, t1 = p_hi > p_lo ? (p_hi + kTileR8 - 1) / kTileR8 : t0;
+
+  // this wave's rows and this lane's
+  const int w0 = kRows8 * rt + 32 * wave, wrows = min(32, kRows8 * rt + rows - w0);
+  const int r = w0 + min(n, max(wrows, 1) - 1), tok = min(r / a.G, sq.n - 1), head = h * a.G + r % a.G;
+  const int pos = first + tok, lo = row8_lo(a, start, pos), hi = pos + 1;
+  const int any_lo = row8_lo(a, start, first + w0 / a.G), any_hi = first + (w0 + max(wrows, 1) - 1) / a.G + 1;
+  const int all_lo = row8_lo(a, start, any_hi - 1), all_hi = first + w0 / a.G + 1;
+  Raw<16> qf[2 * NG];
+  float qs;
+  {
+    const uint8_t* row = a.q + (size_t)(sq.first + tok) * a.ldq + (size_t)head * D * 2;
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < 2 * NG; ++g) {
+      qf[g] = load_raw<16>(row + (16 * g + 8 * c) * 2);
+      float x[8];
+      unpack<T, 4>(qf[g].w, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+    }
+    top = fmaxf(top, __uint_as_float(lane_xor_u32<32>(__float_as_uint(top), lane)));
+    const int e = query8_exponent(top);
+#pragma unroll
+    for (int g = 0; g < 2 * NG; ++g) {
+      float x[8];
+      unpack<T, 4>(qf[g].w, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qf[g].w[j] = pack8_f16(ldexpf(x[2 * j], -e), ldexpf(x[2 * j + 1], -e));
+    }
+    qs = ldexpf(1.f, e);
+  }
+  float ref = kRefMin8, sum = 0.f;
+  f32x16 acc[NG];
+#pragma unroll
+  for (int m = 0; m < NG; ++m) acc[m] = f32x16{0.f};
+
+  // pieces of 16 bytes: K of the tile's four blocks, then V
+  Raw<16> piece[PT];
+  float2 scales = make_float2(0.f, 0.f);
+  int ids = 0, next_consts = -1;
+  const auto fetch = [&](int t) {
+    if (((t - t0) & 15) == 0) {                                // page ids of 16 tiles, a block to a lane
+      const int p = (min(t + (lane >> 2), t1 - 1)) * kTileR8 + (lane & 3) * kBlk8;
+      ids = kv_page(a.kv, b, p);
+    }
+    const int at = ((t - t0) & 15) * 4;
+#pragma unroll
+    for (int j = 0; j < PT; ++j) {
+      const int e = min(j * 512 + (int)threadIdx.x, kPieces - 1), part = e / (4 * D), u = (e % (4 * D)) / D;
+      const int id = __shfl(ids, at + u);
+      piece[j] = load_raw<16>(attn8_block(a.kv, h, id, t * kTileR8 + u * kBlk8) + part * 16 * D + 16 * (e % D));
+    }
+    next_consts = __shfl(ids, at + (lane & 3));
+    if (threadIdx.x < kTileR8 / kBlk8)
+      scales = *(const float2*)(attn8_block(a.kv, h, next_consts, t * kTileR8 + lane * kBlk8) + 32 * D);
+  };
+  const auto decode = [&](int buf) {
+    uint8_t* kb = mem[buf];
+    uint8_t* vb = kb + kK;
+#pragma unroll
+    for (int j = 0; j < PT; ++j) {
+      const int e = j * 512 + threadIdx.x;
+      if (e >= kPieces) continue;
+      const int part = e / (4 * D), u = (e % (4 * D)) / D, o = 16 * (e % D);
+      const Raw<16> x = codes8(piece[j].w[0], piece[j].w[1]), y = codes8(piece[j].w[2], piece[j].w[3]);
+      if (part == 0) {
+        uint8_t* to = kb + (u * kBlk8 + o / D) * kRow + (o % D) * 2;
+        *(Raw<16>*)to = x;
+        *(Raw<16>*)(to + 16) = y;
+      } else {
+        const int q = o / (4 * D), d = (o % (4 * D)) / 4;
+        uint8_t* to = vb + ((u * 2 + (q & 1)) * D + d) * 16 + (q >> 1) * 8;
+        *(Raw<8>*)to = Raw<8>{{x.w[0], x.w[1]}};
+        *(Raw<8>*)(to + 16) = Raw<8>{{x.w[2], x.w[3]}};
+        *(Raw<8>*)(to + 32) = Raw<8>{{y.w[0], y.w[1]}};
+        *(Raw<8>*)(to + 48) = Raw<8>{{y.w[2], y.w[3]}};
+      }
+    }
+    if (threadIdx.x < kTileR8 / kBlk8) {
+      const float vs = scales.y != 0.f ? scales.y : kNoScale;
+      // a block without a page counts nowhere
+      consts[buf][threadIdx.x] = next_consts >= 0 ? make_float4(scales.x * a.k2, log2f(vs), 1.0f / vs, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+
+  if (t0 < t1) fetch(t0);
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1;
+    decode(buf);
+    __syncthreads();
+    if (t + 1 < t1) fetch(t + 1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int p0 = t * kTileR8 + 32 * s;
+      if (wrows <= 0 || p0 >= any_hi || p0 + 32 <= any_lo) continue;
+      const uint8_t* kr = mem[buf] + (32 * s + n) * kRow + 16 * c;
+      f32x16 sc = {0.f};
+#pragma unroll
+      for (int g = 0; g < 2 * NG; ++g) sc = mma32(load_raw<16>(kr + 32 * g), qf[g], sc);
+      const float4 k0 = consts[buf][2 * s], k1 = consts[buf][2 * s + 1];
+      const float kk[2] = {k0.x * qs, k1.x * qs}, lv[2] = {k0.y, k1.y};
+      float iv[2] = {k0.z, k1.z};
+      float e[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) e[i] = fmaf(sc[i], kk[i >> 3], lv[i >> 3]);
+      if (!(p0 >= all_lo && p0 + 32 <= all_hi && k0.w != 0.f && k1.w != 0.f)) {
+        bool on[2] = {false, false};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int p = p0 + 8 * (i >> 2) + 4 * c + (i & 3);
+          const bool in = p >= lo && p < hi && (i < 8 ? k0.w : k1.w) != 0.f;
+          on[i >> 3] |= in;
+          if (!in) e[i] = -INFINITY;
+        }
+        if (!on[0]) iv[0] = 0.f;
+        if (!on[1]) iv[1] = 0.f;
+      }
+      float top = e[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, e[i]);
+      if (__any(top > ref + 6.f)) {
+        const float next = fmaxf(fmaxf(top, __uint_as_float(lane_xor_u32<32>(__float_as_uint(top), lane))), ref);
+        const float f = exp2f(ref - next);
+        ref = next;
+        sum *= f;
+#pragma unroll
+        for (int m = 0; m < NG; ++m)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[m][i] *= f;
+      }
+      const float off = 9.f - ref;
+      Raw<16> p[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e0 = __builtin_amdgcn_exp2f(e[2 * i] + off), e1 = __builtin_amdgcn_exp2f(e[2 * i + 1] + off);
+        sum = fmaf(e0, iv[i >> 2], sum);
+        sum = fmaf(e1, iv[i >> 2], sum);
+        p[i >> 2].w[i & 3] = pack8_f16(e0, e1);
+      }
+      const uint8_t* vr = mem[buf] + kK + ((4 * s + c) * D + n) * 16;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int m = 0; m < NG; ++m) acc[m] = mma32(load_raw<16>(vr + (2 * j * D + 32 * m) * 16), p[j], acc[m]);
+    }
+  }
+
+  if (n >= wrows) return;
+  sum += __uint_as_float(lane_xor_u32<32>(__float_as_uint(sum), lane));
+  const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+  const size_t o = (size_t)(sq.first + tok) * a.Hq + head;
+#pragma unroll
+  for (int m = 0; m < NG; ++m)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      Raw<8> w;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w.w[j] = (uint32_t)to_16(T{}, acc[m][4 * q + 2 * j] * inv) | ((uint32_t)to_16(T{}, acc[m][4 * q + 2 * j + 1] * inv) << 16);
+      *(Raw<8>*)(a.out + (o * D + 32 * m + 8 * q + 4 * c) * 2) = w;
+    }
+  if (a.lse && c == 0) a.lse[o] = attn8_lse(ref, sum);
+}
+
+template <class T, int NG>
+hipError_t attn8_run(hipStream_t s, const Attn8Args& a, bool rows) {
+  if (rows) {
+    k_attn_q8_rows<T, NG><<<dim3(a.RT * a.kv.Hkv, a.kv.B), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
   k_attn_q8<T, NG><<<dim3(a.S * a.RT, a.kv.Hkv, a.kv.B), dim3(attn8_waves(NG) * kWave), 0, s>>>(a);
   if (a.S > 1) k_attn8_join<T, NG><<<dim3(a.kv.Hkv * a.rows.most * a.G, a.kv.B), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t attn8_launch(hipStream_t s, const Attn8Args& a) {
+hipError_t attn8_launch(hipStream_t s, const Attn8Args& a, bool rows) {
   switch (a.kv.D >> 5) {
-    case 1: return attn8_run<T, 1>(s, a);
-    case 2: return attn8_run<T, 2>(s, a);
-    case 3: return attn8_run<T, 3>(s, a);
-    case 4: return attn8_run<T, 4>(s, a);
-    case 5: return attn8_run<T, 5>(s, a);
-    case 6: return attn8_run<T, 6>(s, a);
-    case 7: return attn8_run<T, 7>(s, a);
-    default: return attn8_run<T, 8>(s, a);
+    case 1: return attn8_run<T, 1>(s, a, rows);
+    case 2: return attn8_run<T, 2>(s, a, rows);
+    case 3: return attn8_run<T, 3>(s, a, rows);
+    case 4: return attn8_run<T, 4>(s, a, rows);
+    case 5: return attn8_run<T, 5>(s, a, rows);
+    case 6: return attn8_run<T, 6>(s, a, rows);
+    case 7: return attn8_run<T, 7>(s, a, rows);
+    default: return attn8_run<T, 8>(s, a, rows);
   }
 }
 

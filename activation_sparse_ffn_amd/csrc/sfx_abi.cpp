@@ -54,7 +54,14 @@ Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int max_len) {
   Attn8Plan p;
   p.Hq = Hq;
   p.G = Hq / Hkv;
-  p.RT = (int)(((long long)max_q * p.G + 15) / 16);
+  const long long rows = (long long)max_q * p.G;
+  p.rows = rows >= 128;
+  if (p.rows) {
+    p.RT = (int)((rows + 255) / 256);
+    p.S = 1;
+    return p;
+  }
+  p.RT = (int)((rows + 15) / 16);
   const long long units = (long long)B * Hkv * p.RT;
   const int most = (max_len + 255) / 256;
   p.S = units >= 512 ? 1 : (int)((512 + units - 1) / units);

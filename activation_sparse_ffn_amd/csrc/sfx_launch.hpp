@@ -127,9 +127,11 @@ hipError_t launch_kv_append_q8(hipStream_t s, const KvGeom& g, int xdt, int qdt,
 hipError_t launch_kv_read_q8(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
                              const int32_t* table, const void* cache, void* k, void* v);
 
-// Attention over the int8 cache: query heads, per kv head, tiles of 16 rows, runs of a tile.
+// Attention over the int8 cache: query heads, per kv head, tiles of 16 rows (256 if `rows`), runs of a
+// tile.
 struct Attn8Plan {
   int Hq, G, RT, S;
+  bool rows;
 };
 Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int max_len);
 size_t attn8_ws_bytes(const Attn8Plan& p, int B, int Hkv, int D);
