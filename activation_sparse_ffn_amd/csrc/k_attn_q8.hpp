@@ -37,7 +37,7 @@ struct Attn8Args {
   const int32_t* starts;
   uint8_t* out;             // [T][Hq][D] 16 bit
   float* lse;               // [T][Hq] or null
-  float* parts;             // [B][Hkv][row tiles][S] x ([16][D] sums, [16][2] reference and weight sum)
+  float* parts;             // [B][Hkv][row tiles][S] x ([R][D] sums, [R][2] reference and weight sum), R rows a tile
   float k2;                 // scale log2(e)
   int Hq, G, window, RT, S;
 };
@@ -115,54 +115,70 @@ struct State8 {
   f32x4 acc[2 * NG];        // of product m: dims (4 c + i) 2 NG + m
 };
 
-// `on`: bit 4 u + i says that position 4 c + i of block u counts for this lane's row (all ones
-// where `full`).
-template <int NG>
-__device__ __forceinline__ void tile8_run(const Tile8<NG>& t, const Raw<16> (&qf)[NG], float k2, float qs, bool full,
-                                          uint32_t on, int lane, State8<NG>& st) {
-  float s[8], lv[2], iv[2];
+// NC tiles of 16 rows at once, so that codes are decoded once for them.  `on`: bit 4 u + i says that
+// position 4 c + i of block u counts for this lane's row (all ones where `full`).
+template <int NG, int NC>
+__device__ __forceinline__ void tile8_run(const Tile8<NG>& t, const Raw<16> (&qf)[NC][NG], float k2, const float (&qs)[NC],
+                                          bool full, const uint32_t (&on)[NC], int lane, State8<NG> (&st)[NC]) {
+  float s[NC][8], lv[2], inv[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    f32x4 p = {0.f, 0.f, 0.f, 0.f};
+    f32x4 p[NC];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) p = Mma<TF16>::run(codes8(t.k[u][2 * g], t.k[u][2 * g + 1]), qf[g], p);
-    const float kk = t.s[u].x * k2 * qs, vs = t.s[u].y != 0.f ? t.s[u].y : kNoScale;
+    for (int j = 0; j < NC; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const Raw<16> k = codes8(t.k[u][2 * g], t.k[u][2 * g + 1]);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) p[j] = Mma<TF16>::run(k, qf[j][g], p[j]);
+    }
+    const float vs = t.s[u].y != 0.f ? t.s[u].y : kNoScale;
     lv[u] = log2f(vs);
-    iv[u] = 1.0f / vs;
+    inv[u] = 1.0f / vs;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[4 * u + i] = fmaf(p[i], kk, lv[u]);
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[j][4 * u + i] = fmaf(p[j][i], t.s[u].x * k2 * qs[j], lv[u]);
   }
-  if (!full) {
+  Raw<16> w[NC];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (!((on >> i) & 1u)) s[i] = -INFINITY;
-    // a block none of whose positions counts may hold anything
-    if (!(on & 0x0Fu)) iv[0] = 0.f;
-    if (!(on & 0xF0u)) iv[1] = 0.f;
+  for (int j = 0; j < NC; ++j) {
+    float iv[2] = {inv[0], inv[1]};
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!((on[j] >> i) & 1u)) s[j][i] = -INFINITY;
+      // a block none of whose positions counts may hold anything
+      if (!(on[j] & 0x0Fu)) iv[0] = 0.f;
+      if (!(on[j] & 0xF0u)) iv[1] = 0.f;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, s[j][i]);
+    if (__any(top > st[j].ref + 6.f)) {
+      const float next = fmaxf(quarters_max8(top, lane), st[j].ref), f = exp2f(st[j].ref - next);
+      st[j].ref = next;
+      st[j].sum *= f;
+#pragma unroll
+      for (int m = 0; m < 2 * NG; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[j].acc[m][i] *= f;
+    }
+    const float off = 9.f - st[j].ref;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e0 = __builtin_amdgcn_exp2f(s[j][2 * i] + off), e1 = __builtin_amdgcn_exp2f(s[j][2 * i + 1] + off);
+      st[j].sum = fmaf(e0, iv[i >> 1], st[j].sum);
+      st[j].sum = fmaf(e1, iv[i >> 1], st[j].sum);
+      w[j].w[i] = pack8_f16(e0, e1);
+    }
   }
-  float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, s[i]);
-  if (__any(top > st.ref + 6.f)) {
-    const float next = fmaxf(quarters_max8(top, lane), st.ref), f = exp2f(st.ref - next);
-    st.ref = next;
-    st.sum *= f;
+  for (int m = 0; m < 2 * NG; ++m) {
+    const Raw<16> v = codes8(t.v[0][m], t.v[1][m]);
 #pragma unroll
-    for (int m = 0; m < 2 * NG; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) st.acc[m][i] *= f;
+    for (int j = 0; j < NC; ++j) st[j].acc[m] = Mma<TF16>::run(v, w[j], st[j].acc[m]);
   }
-  const float off = 9.f - st.ref;
-  Raw<16> p;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float e0 = __builtin_amdgcn_exp2f(s[2 * i] + off), e1 = __builtin_amdgcn_exp2f(s[2 * i + 1] + off);
-    st.sum = fmaf(e0, iv[i >> 1], st.sum);
-    st.sum = fmaf(e1, iv[i >> 1], st.sum);
-    p.w[i] = pack8_f16(e0, e1);
-  }
-#pragma unroll
-  for (int m = 0; m < 2 * NG; ++m) st.acc[m] = Mma<TF16>::run(codes8(t.v[0][m], t.v[1][m]), p, st.acc[m]);
 }
 
 __device__ __forceinline__ int query8_exponent(float top) {
@@ -192,23 +208,24 @@ __device__ __forceinline__ float attn8_lse(float ref, float sum) {
   return sum != 0.f ? (ref - 9.f + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Positions [start, end) that some row of a tile covers, as tiles t0 .. t0 + ntile - 1 cut into
-// `active` runs of `per`: S even runs, none shorter than a tile per wave.
+// Positions [start, end) that some row of a tile of rows covers, as tiles t0 .. t0 + ntile - 1 cut into
+// `active` runs of `per`: S even runs, none shorter than `least`.
 struct Span8 {
   int start, end, t0, ntile, per, active;
 };
 __device__ __forceinline__ int row8_lo(const Attn8Args& a, int start, int pos) {
   return a.window ? max(start, pos + 1 - a.window) : start;
 }
-__device__ __forceinline__ Span8 span8(const Attn8Args& a, const Seq8& sq, int start, int rt, int W) {
-  const int i0 = 16 * rt / a.G, i1 = min(sq.n - 1, (16 * rt + 15) / a.G);       // first and last token of the tile
+// The same for `R` rows at a time, `step` positions to a tile and runs of at least `least` tiles.
+__device__ __forceinline__ Span8 span8(const Attn8Args& a, const Seq8& sq, int start, int rt, int R, int step, int least) {
+  const int i0 = R * rt / a.G, i1 = min(sq.n - 1, (R * rt + R - 1) / a.G);      // first and last token of the tile
   const int first = sq.len - sq.n;
   Span8 s;
   s.start = max(0, row8_lo(a, start, first + i0));
   s.end = min(first + i1 + 1, a.kv.max_pages << a.kv.page_shift);
-  s.t0 = s.start / kTile8;
-  s.ntile = s.end > s.start ? (s.end + kTile8 - 1) / kTile8 - s.t0 : 0;
-  s.per = max(W, (s.ntile + a.S - 1) / a.S);
+  s.t0 = s.start / step;
+  s.ntile = s.end > s.start ? (s.end + step - 1) / step - s.t0 : 0;
+  s.per = max(least, (s.ntile + a.S - 1) / a.S);
   s.active = max(1, (s.ntile + s.per - 1) / s.per);            // an empty tile has one: its zero rows
   return s;
 }
@@ -222,35 +239,43 @@ __device__ __forceinline__ const uint8_t* attn8_block(const KvCache& kv, int h, 
   return kv.base + kv8_block(kv, max(id, 0), h, (pos & ((1 << kv.page_shift) - 1)) >> 4);
 }
 
-template <class T, int NG>
+template <class T, int NG, int NC>
 __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a) {
-  constexpr int W = attn8_waves(NG), D = 32 * NG, kThreads = W * kWave;
+  constexpr int W = attn8_waves(NG), D = 32 * NG, kThreads = W * kWave, R = 16 * NC;
   __shared__ float sh_ref[W][16], sh_sum[W][16];
   __shared__ __attribute__((aligned(16))) float sh_acc[W * 16 * (D + 4)];
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, c = lane >> 4;
   const int split = blockIdx.x % a.S, rt = blockIdx.x / a.S, h = blockIdx.y, b = blockIdx.z;
   const Seq8 sq = rows8_seq(a.rows, b);
-  const int rows = min(16, sq.n * a.G - 16 * rt);              // of this tile
+  const int rows = min(R, sq.n * a.G - R * rt);                // of this tile
   if (rows <= 0) return;
-  const int start = a.starts ? max(a.starts[b], 0) : 0;
-  const Span8 sp = span8(a, sq, start, rt, W);
+  const int start = a.starts ? max(a.starts[b], 0) : 0, first = sq.len - sq.n;
+  const Span8 sp = span8(a, sq, start, rt, R, kTile8, W);
   if (split >= sp.active) return;
   const int tb = sp.t0 + split * sp.per, te = min(sp.t0 + sp.ntile, tb + sp.per);
 
-  // this lane's row
-  const int r = 16 * rt + min(n, rows - 1), tok = r / a.G, head = h * a.G + r % a.G;
-  const int pos = sq.len - sq.n + tok;
-  const int lo = row8_lo(a, start, pos), hi = pos + 1;          // columns past the last row repeat it
-  const int all_lo = row8_lo(a, start, sq.len - sq.n + (16 * rt + rows - 1) / a.G);   // what every row covers
-  const int all_hi = sq.len - sq.n + 16 * rt / a.G + 1;
-  Raw<16> qf[NG];
-  const float qs = query8<T, NG>(a.q + (size_t)(sq.first + tok) * a.ldq + (size_t)head * D * 2, n < rows, c, lane, qf);
-  State8<NG> st;
-  st.ref = kRefMin8;
-  st.sum = 0.f;
+  // this lane's rows; columns past the last one repeat it
+  int lo[NC], hi[NC];
+  float qs[NC];
+  Raw<16> qf[NC][NG];
 #pragma unroll
-  for (int m = 0; m < 2 * NG; ++m) st.acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < NC; ++j) {
+    const int r = R * rt + min(16 * j + n, rows - 1), tok = r / a.G, head = h * a.G + r % a.G;
+    lo[j] = row8_lo(a, start, first + tok);
+    hi[j] = first + tok + 1;
+    qs[j] = query8<T, NG>(a.q + (size_t)(sq.first + tok) * a.ldq + (size_t)head * D * 2, 16 * j + n < rows, c, lane, qf[j]);
+  }
+  // what every row covers
+  const int all_lo = row8_lo(a, start, first + (R * rt + rows - 1) / a.G), all_hi = first + R * rt / a.G + 1;
+  State8<NG> st[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    st[j].ref = kRefMin8;
+    st[j].sum = 0.f;
+#pragma unroll
+    for (int m = 0; m < 2 * NG; ++m) st[j].acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
   int it = tb + wave;
   if (it < te) {
     const int todo = (te - it + W - 1) / W;
@@ -273,126 +298,199 @@ __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a
         tile8_load<NG>(blk, n, c, nxt);
       }
       const bool full = p0 >= all_lo && p0 + kTile8 <= all_hi && id0 >= 0 && id1 >= 0;
-      uint32_t on = 0xFFu;
-      if (!full) {
-        on = 0;
+      uint32_t on[NC];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int p = p0 + (e >> 2) * kBlk8 + 4 * c + (e & 3);
-          if (p >= lo && p < hi && ((e >> 2) ? id1 : id0) >= 0) on |= 1u << e;
+      for (int j = 0; j < NC; ++j) {
+        on[j] = 0xFFu;
+        if (!full) {
+          on[j] = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int p = p0 + (e >> 2) * kBlk8 + 4 * c + (e & 3);
+            if (p >= lo[j] && p < hi[j] && ((e >> 2) ? id1 : id0) >= 0) on[j] |= 1u << e;
+          }
         }
       }
-      tile8_run<NG>(cur, qf, a.k2, qs, full, on, lane, st);
+      tile8_run<NG, NC>(cur, qf, a.k2, qs, full, on, lane, st);
       cur = nxt;
       ids = next_ids;
     }
   }
 
-  // join the waves
-  st.sum = quarters_sum8(st.sum, lane);
-  if (c == 0) {
-    sh_ref[wave][n] = st.ref;
-    sh_sum[wave][n] = st.sum;
-  }
-#pragma unroll
-  for (int m = 0; m < 2 * NG; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sh_acc[(wave * 16 + n) * (D + 4) + (4 * c + i) * 2 * NG + m] = st.acc[m][i];
-  __syncthreads();
-  constexpr size_t run = 16 * (D + 2);
+  // join the waves, 16 rows at a time
+  constexpr size_t run = R * (D + 2);
   float* part = a.parts + ((((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S + split) * run;
-  for (int e = threadIdx.x; e < rows * (D / 2); e += kThreads) {
-    const int rr = e / (D / 2), d = 2 * (e % (D / 2));
-    float ref = sh_ref[0][rr];
 #pragma unroll
-    for (int w = 1; w < W; ++w) ref = fmaxf(ref, sh_ref[w][rr]);
-    float v0 = 0.f, v1 = 0.f, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float f = exp2f(sh_ref[w][rr] - ref);
-      const float* p = sh_acc + (w * 16 + rr) * (D + 4) + d;
-      v0 = fmaf(f, p[0], v0);
-      v1 = fmaf(f, p[1], v1);
-      l = fmaf(f, sh_sum[w][rr], l);
+  for (int j = 0; j < NC; ++j) {
+    if (16 * j >= rows) break;
+    if (j > 0) __syncthreads();
+    const float sum = quarters_sum8(st[j].sum, lane);
+    if (c == 0) {
+      sh_ref[wave][n] = st[j].ref;
+      sh_sum[wave][n] = sum;
     }
-    if (sp.active == 1) {
-      const int q = 16 * rt + rr;
-      const size_t o = (size_t)(sq.first + q / a.G) * a.Hq + h * a.G + q % a.G;
-      const float inv = l != 0.f ? 1.0f / l : 0.f;
-      ((uint32_t*)a.out)[(o * D + d) >> 1] = (uint32_t)to_16(T{}, v0 * inv) | ((uint32_t)to_16(T{}, v1 * inv) << 16);
-      if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
-    } else {
-      *reinterpret_cast<float2*>(part + rr * D + d) = make_float2(v0, v1);
-      if (d == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * rr) = make_float2(ref, l);
+#pragma unroll
+    for (int m = 0; m < 2 * NG; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sh_acc[(wave * 16 + n) * (D + 4) + (4 * c + i) * 2 * NG + m] = st[j].acc[m][i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < min(16, rows - 16 * j) * (D / 2); e += kThreads) {
+      const int rr = e / (D / 2), d = 2 * (e % (D / 2));
+      float ref = sh_ref[0][rr];
+#pragma unroll
+      for (int w = 1; w < W; ++w) ref = fmaxf(ref, sh_ref[w][rr]);
+      float v0 = 0.f, v1 = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = exp2f(sh_ref[w][rr] - ref);
+        const float* p = sh_acc + (w * 16 + rr) * (D + 4) + d;
+        v0 = fmaf(f, p[0], v0);
+        v1 = fmaf(f, p[1], v1);
+        l = fmaf(f, sh_sum[w][rr], l);
+      }
+      if (sp.active == 1) {
+        const int q = R * rt + 16 * j + rr;
+        const size_t o = (size_t)(sq.first + q / a.G) * a.Hq + h * a.G + q % a.G;
+        const float inv = l != 0.f ? 1.0f / l : 0.f;
+        ((uint32_t*)a.out)[(o * D + d) >> 1] = (uint32_t)to_16(T{}, v0 * inv) | ((uint32_t)to_16(T{}, v1 * inv) << 16);
+        if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
+      } else {
+        *reinterpret_cast<float2*>(part + (16 * j + rr) * D + d) = make_float2(v0, v1);
+        if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * (16 * j + rr)) = make_float2(ref, l);
+      }
     }
   }
 }
 
-// Joins the runs of a row, one workgroup per row.  Four dims to a thread; the runs are dealt out
-// over groups of D / 4 threads and the groups' sums added in order.
+// Joins the runs of a row, one workgroup per row: the runs' references first, then four dims to a thread,
+// the runs dealt out over groups of D / 4 threads and the groups' sums added in order.  Tiles of R
+// rows as span8 cuts them.
 template <class T, int NG>
-__global__ __launch_bounds__(256) void k_attn8_join(Attn8Args a) {
-  constexpr int W = attn8_waves(NG), D = 32 * NG, kItems = D / 4, kGroups = 256 / kItems;
+__global__ __launch_bounds__(256) void k_attn8_join(Attn8Args a, int R, int step, int least) {
+  constexpr int D = 32 * NG, kItems = D / 4, kGroups = 256 / kItems;
   __shared__ __attribute__((aligned(16))) float sh_v[kGroups][D];
-  __shared__ float sh_l[kGroups], sh_r[kGroups];
+  __shared__ float sh_f[256], sh_l[256 / kWave], sh_r[256 / kWave];
   const int b = blockIdx.y, per_head = a.rows.most * a.G, h = blockIdx.x / per_head, q = blockIdx.x % per_head;
   const Seq8 sq = rows8_seq(a.rows, b);
   if (q >= sq.n * a.G) return;
-  const int rt = q / 16, rr = q % 16;
-  const Span8 sp = span8(a, sq, a.starts ? max(a.starts[b], 0) : 0, rt, W);
+  const int rt = q / R, rr = q % R;
+  const Span8 sp = span8(a, sq, a.starts ? max(a.starts[b], 0) : 0, rt, R, step, least);
   if (sp.active == 1) return;                                   // the attention kernel wrote the row
-  constexpr size_t run = 16 * (D + 2);
+  const size_t run = (size_t)R * (D + 2);
   const float* part = a.parts + (((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S * run;
-  const float* rs = part + 16 * D + 2 * rr;
-  const int grp = threadIdx.x / kItems, d = 4 * (threadIdx.x % kItems);
-  float r = kRefMin8;
+  const float* rs = part + (size_t)R * D + 2 * rr;
+  const int grp = threadIdx.x / kItems, d = 4 * (threadIdx.x % kItems), wave = threadIdx.x >> 6;
+  float ref = kRefMin8, l = 0.f;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  if (grp < kGroups) {
-#pragma unroll 4
-    for (int k = grp; k < sp.active; k += kGroups) {
-      const f32x4 pk = *reinterpret_cast<const f32x4*>(part + k * run + rr * D + d);
-      const float2 rl = *reinterpret_cast<const float2*>(rs + k * run);
-      const float next = fmaxf(r, rl.x), f0 = exp2f(r - next), f1 = exp2f(rl.x - next);
-      r = next;
-      l = fmaf(f1, rl.y, l * f0);
+  for (int k0 = 0; k0 < sp.active; k0 += 256) {                 // 256 runs at a time (there are hardly more)
+    const int k = k0 + threadIdx.x;
+    const float2 rl = k < sp.active ? *reinterpret_cast<const float2*>(rs + k * run) : make_float2(kRefMin8, 0.f);
+    float top = rl.x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = fmaf(f1, pk[i], v[i] * f0);
+    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if ((threadIdx.x & 63) == 0) sh_r[wave] = top;
+    __syncthreads();
+    float next = ref;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) next = fmaxf(next, sh_r[w]);
+    const float f = exp2f(rl.x - next), back = exp2f(ref - next);
+    sh_f[threadIdx.x] = f;
+    float sum = f * rl.y;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+    if ((threadIdx.x & 63) == 0) sh_l[wave] = sum;
+    __syncthreads();
+    l = l * back + ((sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= back;
+    ref = next;
+    if (grp < kGroups) {
+      const int n = min(256, sp.active - k0);
+#pragma unroll 8
+      for (int k = grp; k < n; k += kGroups) {
+        const f32x4 pk = *reinterpret_cast<const f32x4*>(part + (k0 + k) * run + rr * D + d);
+        const float w = sh_f[k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(w, pk[i], v[i]);
+      }
     }
-    *reinterpret_cast<f32x4*>(&sh_v[grp][d]) = v;
-    if (d == 0) {
-      sh_l[grp] = l;
-      sh_r[grp] = r;
-    }
+    __syncthreads();
   }
+  if (grp < kGroups) *reinterpret_cast<f32x4*>(&sh_v[grp][d]) = v;
   __syncthreads();
   if (threadIdx.x < kItems) {
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) r = fmaxf(r, sh_r[k]);
-    l = 0.f;
     v = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-      const float f = exp2f(sh_r[k] - r);
       const f32x4 o = *reinterpret_cast<const f32x4*>(&sh_v[k][d]);
-      l = fmaf(f, sh_l[k], l);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = fmaf(f, o[i], v[i]);
+      for (int i = 0; i < 4; ++i) v[i] += o[i];
     }
     const size_t o = (size_t)(sq.first + q / a.G) * a.Hq + h * a.G + q % a.G;
     const float inv = l != 0.f ? 1.0f / l : 0.f;
     uint32_t* dst = (uint32_t*)a.out + ((o * D + d) >> 1);
     dst[0] = (uint32_t)to_16(T{}, v[0] * inv) | ((uint32_t)to_16(T{}, v[1] * inv) << 16);
     dst[1] = (uint32_t)to_16(T{}, v[2] * inv) | ((uint32_t)to_16(T{}, v[3] * inv) << 16);
-    if (a.lse && d == 0) a.lse[o] = attn8_lse(r, l);
+    if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
   }
+}
+
+// The same for few runs of many rows (at most kFewRuns8), a wave per row: D / 4 lanes read a run, the
+// others the next ones.
+constexpr int kFewRuns8 = 16;
+template <class T, int NG>
+__global__ __launch_bounds__(256) void k_attn8_join_few(Attn8Args a, int R, int step, int least) {
+  constexpr int D = 32 * NG, kItems = D / 4, kGroups = kWave / kItems;
+  const int lane = opaque_lane(), b = blockIdx.y, per_head = a.rows.most * a.G;
+  const int x = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = x / per_head, q = x % per_head;
+  const Seq8 sq = rows8_seq(a.rows, b);
+  if (h >= a.kv.Hkv || q >= sq.n * a.G) return;
+  const int rt = q / R, rr = q % R;
+  const Span8 sp = span8(a, sq, a.starts ? max(a.starts[b], 0) : 0, rt, R, step, least);
+  if (sp.active == 1) return;                                   // the attention kernel wrote the row
+  const size_t run = (size_t)R * (D + 2);
+  const float* part = a.parts + (((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S * run;
+  const float2 rl = lane < sp.active ? *reinterpret_cast<const float2*>(part + (size_t)R * D + 2 * rr + lane * run) : make_float2(kRefMin8, 0.f);
+  float ref = rl.x;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) ref = fmaxf(ref, __shfl_xor(ref, o));
+  ref = __shfl(ref, 0);
+  const float f = exp2f(rl.x - ref);
+  float l = f * rl.y;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) l += __shfl_xor(l, o);
+  l = __shfl(l, 0);
+  const int grp = lane / kItems, d = 4 * (lane % kItems);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < sp.active; k += kGroups) {
+    const int mine = k + grp;
+    const bool in = grp < kGroups && mine < sp.active;
+    const f32x4 pk = *reinterpret_cast<const f32x4*>(part + (in ? mine : 0) * run + rr * D + d);
+    const float w = __shfl(f, mine & (kWave - 1));
+    if (in)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(w, pk[i], v[i]);
+  }
+  f32x4 o4 = v;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o4[i] += __shfl(v[i], (lane + k * kItems) & (kWave - 1));
+  if (lane >= kItems) return;
+  const size_t o = (size_t)(sq.first + q / a.G) * a.Hq + h * a.G + q % a.G;
+  const float inv = l != 0.f ? 1.0f / l : 0.f;
+  uint32_t* dst = (uint32_t*)a.out + ((o * D + d) >> 1);
+  dst[0] = (uint32_t)to_16(T{}, o4[0] * inv) | ((uint32_t)to_16(T{}, o4[1] * inv) << 16);
+  dst[1] = (uint32_t)to_16(T{}, o4[2] * inv) | ((uint32_t)to_16(T{}, o4[3] * inv) << 16);
+  if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
 }
 
 // ---- many rows of a sequence.  A workgroup takes 256 rows, a wave 32 of them as the columns of
 // 32x32x16 products; 64 positions at a time go through LDS as fp16, decoded once for all waves: K as rows of
 // positions (16 bytes more than D numbers long: 16 lanes that read one piece of 16 rows meet all banks),
 // V as [block][c][dim] of the eight positions that lane quarter c of the second product holds.
-constexpr int kRows8 = 256, kTileR8 = 64;
+constexpr int kRows8 = 256, kTileR8 = 64, kLeastR8 = 4;         // and tiles of positions that a run has at least
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ f32x16 mma32(const Raw<16>& a, const Raw<16>& b, f32x16 c) {
@@ -405,14 +503,15 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
   __shared__ __attribute__((aligned(16))) uint8_t mem[2][kK + kV];
   __shared__ float4 consts[2][kTileR8 / kBlk8];                // of a block: ks k2, log2 vs, 1 / vs
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, c = lane >> 5;
-  const int h = blockIdx.x % a.kv.Hkv, rt = a.RT - 1 - blockIdx.x / a.kv.Hkv, b = blockIdx.y;   // long tiles first
+  // a head's tiles on one XCD where heads are a multiple of 8; tiles with many positions first
+  const int h = blockIdx.x % a.kv.Hkv, split = blockIdx.x / a.kv.Hkv % a.S, rt = a.RT - 1 - blockIdx.x / a.kv.Hkv / a.S, b = blockIdx.y;
   const Seq8 sq = rows8_seq(a.rows, b);
   const int rows = min(kRows8, sq.n * a.G - kRows8 * rt);
   if (rows <= 0) return;
   const int start = a.starts ? max(a.starts[b], 0) : 0, first = sq.len - sq.n;
-  const int i0 = kRows8 * rt / a.G, i1 = (kRows8 * rt + rows - 1) / a.G;
-  const int p_lo = max(0, row8_lo(a, start, first + i0)), p_hi = min(first + i1 + 1, a.kv.max_pages << a.kv.page_shift);
-  const int t0 = p_lo / kTileR8, t1 = p_hi > p_lo ? (p_hi + kTileR8 - 1) / kTileR8 : t0;
+  const Span8 sp = span8(a, sq, start, rt, kRows8, kTileR8, kLeastR8);
+  if (split >= sp.active) return;
+  const int t0 = sp.t0 + split * sp.per, t1 = min(sp.t0 + sp.ntile, t0 + sp.per);
 
   // this wave's rows and this lane's
   const int w0 = kRows8 * rt + 32 * wave, wrows = min(32, kRows8 * rt + rows - w0);
@@ -562,6 +661,19 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
 
   if (n >= wrows) return;
   sum += __uint_as_float(lane_xor_u32<32>(__float_as_uint(sum), lane));
+  if (sp.active > 1) {
+    const int rr = 32 * wave + n;
+    float* part = a.parts + ((((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S + split) * (size_t)(kRows8 * (D + 2));
+#pragma unroll
+    for (int m = 0; m < NG; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = {acc[m][4 * q], acc[m][4 * q + 1], acc[m][4 * q + 2], acc[m][4 * q + 3]};
+        *reinterpret_cast<f32x4*>(part + rr * D + 32 * m + 8 * q + 4 * c) = v;
+      }
+    if (c == 0) *reinterpret_cast<float2*>(part + kRows8 * D + 2 * rr) = make_float2(ref, sum);
+    return;
+  }
   const float inv = sum != 0.f ? 1.0f / sum : 0.f;
   const size_t o = (size_t)(sq.first + tok) * a.Hq + head;
 #pragma unroll
@@ -577,28 +689,33 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
   if (a.lse && c == 0) a.lse[o] = attn8_lse(ref, sum);
 }
 
+template <class T, int NG, int NC>
+void attn8_few(hipStream_t s, const Attn8Args& a) {
+  k_attn_q8<T, NG, NC><<<dim3(a.S * a.RT, a.kv.Hkv, a.kv.B), dim3(attn8_waves(NG) * kWave), 0, s>>>(a);
+}
 template <class T, int NG>
-hipError_t attn8_run(hipStream_t s, const Attn8Args& a, bool rows) {
-  if (rows) {
-    k_attn_q8_rows<T, NG><<<dim3(a.RT * a.kv.Hkv, a.kv.B), dim3(512), 0, s>>>(a);
-    return hipGetLastError();
-  }
-  k_attn_q8<T, NG><<<dim3(a.S * a.RT, a.kv.Hkv, a.kv.B), dim3(attn8_waves(NG) * kWave), 0, s>>>(a);
-  if (a.S > 1) k_attn8_join<T, NG><<<dim3(a.kv.Hkv * a.rows.most * a.G, a.kv.B), dim3(256), 0, s>>>(a);
+hipError_t attn8_run(hipStream_t s, const Attn8Args& a, int R) {
+  if (R == kRows8) k_attn_q8_rows<T, NG><<<dim3(a.RT * a.S * a.kv.Hkv, a.kv.B), dim3(512), 0, s>>>(a);
+  else if (R == 32) attn8_few<T, NG, 2>(s, a);
+  else attn8_few<T, NG, 1>(s, a);
+  const int step = R == kRows8 ? kTileR8 : kTile8, least = R == kRows8 ? kLeastR8 : attn8_waves(NG);
+  const int rows = a.kv.Hkv * a.rows.most * a.G;
+  if (a.S > kFewRuns8) k_attn8_join<T, NG><<<dim3(rows, a.kv.B), dim3(256), 0, s>>>(a, R, step, least);
+  else if (a.S > 1) k_attn8_join_few<T, NG><<<dim3((rows + 3) / 4, a.kv.B), dim3(256), 0, s>>>(a, R, step, least);
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t attn8_launch(hipStream_t s, const Attn8Args& a, bool rows) {
+hipError_t attn8_launch(hipStream_t s, const Attn8Args& a, int R) {
   switch (a.kv.D >> 5) {
-    case 1: return attn8_run<T, 1>(s, a, rows);
-    case 2: return attn8_run<T, 2>(s, a, rows);
-    case 3: return attn8_run<T, 3>(s, a, rows);
-    case 4: return attn8_run<T, 4>(s, a, rows);
-    case 5: return attn8_run<T, 5>(s, a, rows);
-    case 6: return attn8_run<T, 6>(s, a, rows);
-    case 7: return attn8_run<T, 7>(s, a, rows);
-    default: return attn8_run<T, 8>(s, a, rows);
+    case 1: return attn8_run<T, 1>(s, a, R);
+    case 2: return attn8_run<T, 2>(s, a, R);
+    case 3: return attn8_run<T, 3>(s, a, R);
+    case 4: return attn8_run<T, 4>(s, a, R);
+    case 5: return attn8_run<T, 5>(s, a, R);
+    case 6: return attn8_run<T, 6>(s, a, R);
+    case 7: return attn8_run<T, 7>(s, a, R);
+    default: return attn8_run<T, 8>(s, a, R);
   }
 }
 

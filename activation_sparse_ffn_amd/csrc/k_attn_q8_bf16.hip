@@ -10,7 +10,7 @@ hipError_t launch_attn_q8_bf16(hipStream_t s, const Attn8Plan& p, const KvGeom& 
   const KvCache kv{(uint8_t*)cache, table, g.Hkv, g.D, g.page_shift, g.num_pages, g.max_pages, g.B};
   const Attn8Args a{kv, {q_start, lens, T, max_q}, (const uint8_t*)q, ldq_bytes, starts, (uint8_t*)out, lse, (float*)ws,
                     k2, p.Hq, p.G, window, p.RT, p.S};
-  return attn8_launch<TBF16>(s, a, p.rows);
+  return attn8_launch<TBF16>(s, a, p.R);
 }
 
 }  // namespace sfx

@@ -48,30 +48,27 @@ size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D) {
   return (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 4) * 4;
 }
 
-// Runs per tile of 16 rows: two workgroups of eight waves per compute unit, and no run shorter
-// than a tile of positions per wave.
-Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int max_len) {
+// Rows of a tile and runs of its positions.  Few rows (16 or 32 at a time, waves deal the positions among
+// themselves): two workgroups of eight waves per compute unit, no run shorter than a tile of
+// positions per wave.  Many rows (256 at a time): one workgroup per compute unit, no run shorter than 256
+// positions, and at most 248 runs in all, whose parts are joined (64 MiB at D = 256).
+Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int D, int max_len) {
   Attn8Plan p;
   p.Hq = Hq;
   p.G = Hq / Hkv;
   const long long rows = (long long)max_q * p.G;
-  p.rows = rows >= 128;
-  if (p.rows) {
-    p.RT = (int)((rows + 255) / 256);
-    p.S = 1;
-    return p;
-  }
-  p.RT = (int)((rows + 15) / 16);
+  p.R = rows <= 16 ? 16 : rows < 128 ? 32 : 256;
+  p.RT = (int)((rows + p.R - 1) / p.R);
   const long long units = (long long)B * Hkv * p.RT;
   const int most = (max_len + 255) / 256;
-  p.S = units >= 512 ? 1 : (int)((512 + units - 1) / units);
-  if (p.S > most) p.S = most;
+  const long long want = p.R == 256 ? 248 / units : units >= 256 ? 1 : (512 + units - 1) / units;
+  p.S = (int)(want < 1 ? 1 : want > most ? most : want);
   return p;
 }
 
 size_t attn8_ws_bytes(const Attn8Plan& p, int B, int Hkv, int D) {
   if (p.S <= 1) return 0;
-  return (size_t)B * Hkv * p.RT * p.S * 16 * (D + 2) * 4;
+  return (size_t)B * Hkv * p.RT * p.S * p.R * (D + 2) * 4;
 }
 
 }  // namespace sfx
@@ -617,7 +614,7 @@ static bool attn8_shape(int B, int max_q, int Hq, int Hkv) {
 
 size_t sfx_attn_q8_ws(int B, int max_q, int Hq, int Hkv, int D, int max_len) {
   if (!attn8_shape(B, max_q, Hq, Hkv) || D < 32 || D > 256 || D % 32 != 0 || max_len < 1 || max_len > (1 << 30)) return 0;
-  return sfx::attn8_ws_bytes(sfx::attn8_plan(B, max_q, Hq, Hkv, max_len), B, Hkv, D);
+  return sfx::attn8_ws_bytes(sfx::attn8_plan(B, max_q, Hq, Hkv, D, max_len), B, Hkv, D);
 }
 
 int sfx_attn_q8(void* stream, int qdt, int T, int B, int max_q, int Hq, int Hkv, int D, const void* q, size_t ldq,
@@ -636,7 +633,7 @@ int sfx_attn_q8(void* stream, int qdt, int T, int B, int max_q, int Hq, int Hkv,
   if (!aligned4(table) || !aligned4(lens) || (starts && !aligned4(starts)) || (q_start && !aligned4(q_start)) ||
       (lse && !aligned4(lse)))
     return SFX_E_ALIGN;
-  const sfx::Attn8Plan p = sfx::attn8_plan(B, max_q, Hq, Hkv, max_pages * page);
+  const sfx::Attn8Plan p = sfx::attn8_plan(B, max_q, Hq, Hkv, D, max_pages * page);
   const int w = check_ws(ws, ws_bytes, sfx::attn8_ws_bytes(p, B, Hkv, D));
   if (w != SFX_OK) return w;
   const auto f = qdt == SFX_F16 ? sfx::launch_attn_q8_f16 : sfx::launch_attn_q8_bf16;

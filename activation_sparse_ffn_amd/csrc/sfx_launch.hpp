@@ -127,13 +127,12 @@ hipError_t launch_kv_append_q8(hipStream_t s, const KvGeom& g, int xdt, int qdt,
 hipError_t launch_kv_read_q8(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
                              const int32_t* table, const void* cache, void* k, void* v);
 
-// Attention over the int8 cache: query heads, per kv head, tiles of 16 rows (256 if `rows`), runs of a
-// tile.
+// Attention over the int8 cache: query heads, per kv head, rows of a tile (16, 32 or 256), tiles of
+// rows, runs of positions that a tile is cut into.
 struct Attn8Plan {
-  int Hq, G, RT, S;
-  bool rows;
+  int Hq, G, R, RT, S;
 };
-Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int max_len);
+Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int D, int max_len);
 size_t attn8_ws_bytes(const Attn8Plan& p, int B, int Hkv, int D);
 hipError_t launch_attn_q8_f16(hipStream_t s, const Attn8Plan& p, const KvGeom& g, int T, int max_q, const void* q,
                               size_t ldq_bytes, const int32_t* q_start, const void* cache, const int32_t* table,
