@@ -489,7 +489,7 @@ __global__ __launch_bounds__(256) void k_attn8_join_few(Attn8Args a, int R, int 
 // ---- many rows of a sequence.  A workgroup takes 256 rows, a wave 32 of them as the columns of
 // 32x32x16 products; 64 positions at a time go through LDS as fp16, decoded once for all waves: K as rows of
 // positions (16 bytes more than D numbers long: 16 lanes that read one piece of 16 rows meet all banks),
-// V as [block][c][dim] of the eight positions that lane quarter c of the second product holds.
+// V as [block][c][dim] of the eight positions that lane half c of the second product holds.
 constexpr int kRows8 = 256, kTileR8 = 64, kLeastR8 = 4;         // and tiles of positions that a run has at least
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -499,7 +499,8 @@ __device__ __forceinline__ f32x16 mma32(const Raw<16>& a, const Raw<16>& b, f32x
 
 template <class T, int NG>
 __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
-  constexpr int D = 32 * NG, kRow = 2 * D + 16, kK = kTileR8 * kRow, kV = kTileR8 * 2 * D, kPieces = 8 * D, PT = (kPieces + 511) / 512;
+  constexpr int D = 32 * NG, kRow = 2 * D + 16, kK = kTileR8 * kRow, kV = kTileR8 * 2 * D, kPieces = 4 * D, PT = (kPieces + 511) / 512;
+  constexpr bool kWhole = D % 64 == 0;                         // a wave's pieces are of one block
   __shared__ __attribute__((aligned(16))) uint8_t mem[2][kK + kV];
   __shared__ float4 consts[2][kTileR8 / kBlk8];                // of a block: ks k2, log2 vs, 1 / vs
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, c = lane >> 5;
@@ -548,10 +549,12 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
 #pragma unroll
   for (int m = 0; m < NG; ++m) acc[m] = f32x16{0.f};
 
-  // pieces of 16 bytes: K of the tile's four blocks, then V
-  Raw<16> piece[PT];
+  // Pieces of 16 bytes of the tile's four blocks, K by the threads from the first on, V by the same
+  // threads half the workgroup further, so that narrow heads give every thread one.
+  Raw<16> pk[PT], pv8[PT];
   float2 scales = make_float2(0.f, 0.f);
-  int ids = 0, next_consts = -1;
+  int ids = 0, const_id = -1;
+  const auto place = [&](int j, int turn) { return j * 512 + (((int)threadIdx.x + turn) & 511); };   // piece number
   const auto fetch = [&](int t) {
     if (((t - t0) & 15) == 0) {                                // page ids of 16 tiles, a block to a lane
       const int p = (min(t + (lane >> 2), t1 - 1)) * kTileR8 + (lane & 3) * kBlk8;
@@ -559,41 +562,53 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
     }
     const int at = ((t - t0) & 15) * 4;
 #pragma unroll
-    for (int j = 0; j < PT; ++j) {
-      const int e = min(j * 512 + (int)threadIdx.x, kPieces - 1), part = e / (4 * D), u = (e % (4 * D)) / D;
-      const int id = __shfl(ids, at + u);
-      piece[j] = load_raw<16>(attn8_block(a.kv, h, id, t * kTileR8 + u * kBlk8) + part * 16 * D + 16 * (e % D));
-    }
-    next_consts = __shfl(ids, at + (lane & 3));
+    for (int j = 0; j < PT; ++j)
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int e = min(place(j, part * 256), kPieces - 1);
+        int u = e / D, id;
+        if constexpr (kWhole) {
+          u = __builtin_amdgcn_readfirstlane(u);
+          id = __builtin_amdgcn_readlane(ids, at + u);
+        } else {
+          id = __shfl(ids, at + u);
+        }
+        const uint8_t* src = attn8_block(a.kv, h, id, t * kTileR8 + u * kBlk8);
+        if (part == 0) {
+          pk[j] = load_raw<16>(src + (size_t)(uint32_t)(16 * (e % D)));
+        } else {                                               // quarters cq and cq + 2 of two dims
+          const uint32_t at8 = 16 * D + ((e % D) / (D / 2) * D + (e % D) % (D / 2) * 2) * 4;
+          const Raw<8> v0 = load_raw<8>(src + (size_t)at8), v1 = load_raw<8>(src + (size_t)at8 + 8 * D);
+          pv8[j] = Raw<16>{{v0.w[0], v0.w[1], v1.w[0], v1.w[1]}};
+        }
+      }
+    const_id = __shfl(ids, at + (lane & 3));
     if (threadIdx.x < kTileR8 / kBlk8)
-      scales = *(const float2*)(attn8_block(a.kv, h, next_consts, t * kTileR8 + lane * kBlk8) + 32 * D);
+      scales = *(const float2*)(attn8_block(a.kv, h, const_id, t * kTileR8 + lane * kBlk8) + 32 * D);
   };
   const auto decode = [&](int buf) {
     uint8_t* kb = mem[buf];
     uint8_t* vb = kb + kK;
 #pragma unroll
     for (int j = 0; j < PT; ++j) {
-      const int e = j * 512 + threadIdx.x;
-      if (e >= kPieces) continue;
-      const int part = e / (4 * D), u = (e % (4 * D)) / D, o = 16 * (e % D);
-      const Raw<16> x = codes8(piece[j].w[0], piece[j].w[1]), y = codes8(piece[j].w[2], piece[j].w[3]);
-      if (part == 0) {
+      int e = place(j, 0);
+      if (e < kPieces) {
+        const int u = e / D, o = 16 * (e % D);
         uint8_t* to = kb + (u * kBlk8 + o / D) * kRow + (o % D) * 2;
-        *(Raw<16>*)to = x;
-        *(Raw<16>*)(to + 16) = y;
-      } else {
-        const int q = o / (4 * D), d = (o % (4 * D)) / 4;
-        uint8_t* to = vb + ((u * 2 + (q & 1)) * D + d) * 16 + (q >> 1) * 8;
-        *(Raw<8>*)to = Raw<8>{{x.w[0], x.w[1]}};
-        *(Raw<8>*)(to + 16) = Raw<8>{{x.w[2], x.w[3]}};
-        *(Raw<8>*)(to + 32) = Raw<8>{{y.w[0], y.w[1]}};
-        *(Raw<8>*)(to + 48) = Raw<8>{{y.w[2], y.w[3]}};
+        *(Raw<16>*)to = codes8(pk[j].w[0], pk[j].w[1]);
+        *(Raw<16>*)(to + 16) = codes8(pk[j].w[2], pk[j].w[3]);
+      }
+      e = place(j, 256);
+      if (e < kPieces) {
+        uint8_t* to = vb + e * 32;                             // [block][c][dim] of 16 bytes
+        *(Raw<16>*)to = codes8(pv8[j].w[0], pv8[j].w[2]);
+        *(Raw<16>*)(to + 16) = codes8(pv8[j].w[1], pv8[j].w[3]);
       }
     }
     if (threadIdx.x < kTileR8 / kBlk8) {
       const float vs = scales.y != 0.f ? scales.y : kNoScale;
       // a block without a page counts nowhere
-      consts[buf][threadIdx.x] = next_consts >= 0 ? make_float4(scales.x * a.k2, log2f(vs), 1.0f / vs, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      consts[buf][threadIdx.x] = const_id >= 0 ? make_float4(scales.x * a.k2, log2f(vs), 1.0f / vs, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
 
@@ -613,40 +628,48 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
       for (int g = 0; g < 2 * NG; ++g) sc = mma32(load_raw<16>(kr + 32 * g), qf[g], sc);
       const float4 k0 = consts[buf][2 * s], k1 = consts[buf][2 * s + 1];
       const float kk[2] = {k0.x * qs, k1.x * qs}, lv[2] = {k0.y, k1.y};
-      float iv[2] = {k0.z, k1.z};
-      float e[16];
+      float iv[2] = {k0.z, k1.z}, e[16];
+      const float base = 9.f - ref;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) e[i] = fmaf(sc[i], kk[i >> 3], lv[i >> 3]);
+      for (int i = 0; i < 16; ++i) e[i] = fmaf(sc[i], kk[i >> 3], lv[i >> 3] + base);
       if (!(p0 >= all_lo && p0 + 32 <= all_hi && k0.w != 0.f && k1.w != 0.f)) {
         bool on[2] = {false, false};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int p = p0 + 8 * (i >> 2) + 4 * c + (i & 3);
-          const bool in = p >= lo && p < hi && (i < 8 ? k0.w : k1.w) != 0.f;
+          const bool in = (int)(p >= lo) & (int)(p < hi) & (int)((i < 8 ? k0.w : k1.w) != 0.f);
           on[i >> 3] |= in;
-          if (!in) e[i] = -INFINITY;
+          e[i] = in ? e[i] : -INFINITY;
         }
-        if (!on[0]) iv[0] = 0.f;
-        if (!on[1]) iv[1] = 0.f;
+        iv[0] = on[0] ? iv[0] : 0.f;
+        iv[1] = on[1] ? iv[1] : 0.f;
       }
       float top = e[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = fmaxf(top, e[i]);
-      if (__any(top > ref + 6.f)) {
+      if (__any(top > 15.f)) {
+        // the scores themselves, what does not count left at -inf
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          e[i] = e[i] == -INFINITY ? -INFINITY : fmaf(sc[i], kk[i >> 3], lv[i >> 3]);
+          top = fmaxf(top, e[i]);
+        }
         const float next = fmaxf(fmaxf(top, __uint_as_float(lane_xor_u32<32>(__float_as_uint(top), lane))), ref);
-        const float f = exp2f(ref - next);
+        const float f = exp2f(ref - next), off = 9.f - next;
         ref = next;
         sum *= f;
 #pragma unroll
         for (int m = 0; m < NG; ++m)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[m][i] *= f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] += off;
       }
-      const float off = 9.f - ref;
       Raw<16> p[2];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float e0 = __builtin_amdgcn_exp2f(e[2 * i] + off), e1 = __builtin_amdgcn_exp2f(e[2 * i + 1] + off);
+        const float e0 = __builtin_amdgcn_exp2f(e[2 * i]), e1 = __builtin_amdgcn_exp2f(e[2 * i + 1]);
         sum = fmaf(e0, iv[i >> 2], sum);
         sum = fmaf(e1, iv[i >> 2], sum);
         p[i >> 2].w[i & 3] = pack8_f16(e0, e1);
