@@ -486,11 +486,11 @@ __global__ __launch_bounds__(256) void k_attn8_join_few(Attn8Args a, int R, int 
   if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
 }
 
-// ---- many rows of a sequence.  A workgroup takes 256 rows, a wave 32 of them as the columns of
-// 32x32x16 products; 64 positions at a time go through LDS as fp16, decoded once for all waves: K as rows of
+// ---- many rows of a sequence.  A workgroup takes 128 or 256 rows (attn8_rows), a wave 32 of them as the
+// columns of 32x32x16 products; 64 positions at a time go through LDS as fp16, decoded once for all waves: K as rows of
 // positions (16 bytes more than D numbers long: 16 lanes that read one piece of 16 rows meet all banks),
 // V as [block][c][dim] of the eight positions that lane half c of the second product holds.
-constexpr int kRows8 = 256, kTileR8 = 64, kLeastR8 = 4;         // and tiles of positions that a run has at least
+constexpr int kTileR8 = 64, kLeastR8 = 4;         // and tiles of positions that a run has at least
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ f32x16 mma32(const Raw<16>& a, const Raw<16>& b, f32x16 c) {
@@ -498,8 +498,9 @@ __device__ __forceinline__ f32x16 mma32(const Raw<16>& a, const Raw<16>& b, f32x
 }
 
 template <class T, int NG>
-__global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
-  constexpr int D = 32 * NG, kRow = 2 * D + 16, kK = kTileR8 * kRow, kV = kTileR8 * 2 * D, kPieces = 4 * D, PT = (kPieces + 511) / 512;
+__global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Args a) {
+  constexpr int kRows8 = attn8_rows(NG), NTH = 2 * kRows8;
+  constexpr int D = 32 * NG, kRow = 2 * D + 16, kK = kTileR8 * kRow, kV = kTileR8 * 2 * D, kPieces = 4 * D, PT = (kPieces + NTH - 1) / NTH;
   constexpr bool kWhole = D % 64 == 0;                         // a wave's pieces are of one block
   __shared__ __attribute__((aligned(16))) uint8_t mem[2][kK + kV];
   __shared__ float4 consts[2][kTileR8 / kBlk8];                // of a block: ks k2, log2 vs, 1 / vs
@@ -554,7 +555,7 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
   Raw<16> pk[PT], pv8[PT];
   float2 scales = make_float2(0.f, 0.f);
   int ids = 0, const_id = -1;
-  const auto place = [&](int j, int turn) { return j * 512 + (((int)threadIdx.x + turn) & 511); };   // piece number
+  const auto place = [&](int j, int turn) { return j * NTH + (((int)threadIdx.x + turn) & (NTH - 1)); };   // piece number
   const auto fetch = [&](int t) {
     if (((t - t0) & 15) == 0) {                                // page ids of 16 tiles, a block to a lane
       const int p = (min(t + (lane >> 2), t1 - 1)) * kTileR8 + (lane & 3) * kBlk8;
@@ -565,7 +566,7 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
     for (int j = 0; j < PT; ++j)
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
-        const int e = min(place(j, part * 256), kPieces - 1);
+        const int e = min(place(j, part * (NTH / 2)), kPieces - 1);
         int u = e / D, id;
         if constexpr (kWhole) {
           u = __builtin_amdgcn_readfirstlane(u);
@@ -598,7 +599,7 @@ __global__ __launch_bounds__(512) void k_attn_q8_rows(Attn8Args a) {
         *(Raw<16>*)to = codes8(pk[j].w[0], pk[j].w[1]);
         *(Raw<16>*)(to + 16) = codes8(pk[j].w[2], pk[j].w[3]);
       }
-      e = place(j, 256);
+      e = place(j, NTH / 2);
       if (e < kPieces) {
         uint8_t* to = vb + e * 32;                             // [block][c][dim] of 16 bytes
         *(Raw<16>*)to = codes8(pv8[j].w[0], pv8[j].w[2]);
@@ -718,7 +719,8 @@ void attn8_few(hipStream_t s, const Attn8Args& a) {
 }
 template <class T, int NG>
 hipError_t attn8_run(hipStream_t s, const Attn8Args& a, int R) {
-  if (R == kRows8) k_attn_q8_rows<T, NG><<<dim3(a.RT * a.S * a.kv.Hkv, a.kv.B), dim3(512), 0, s>>>(a);
+  constexpr int kRows8 = attn8_rows(NG);
+  if (R == kRows8) k_attn_q8_rows<T, NG><<<dim3(a.RT * a.S * a.kv.Hkv, a.kv.B), dim3(2 * kRows8), 0, s>>>(a);
   else if (R == 32) attn8_few<T, NG, 2>(s, a);
   else attn8_few<T, NG, 1>(s, a);
   const int step = R == kRows8 ? kTileR8 : kTile8, least = R == kRows8 ? kLeastR8 : attn8_waves(NG);

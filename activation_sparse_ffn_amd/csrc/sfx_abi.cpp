@@ -48,20 +48,24 @@ size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D) {
   return (size_t)B * Hkv * p.HT * p.S * p.HG * (D + 4) * 4;
 }
 
-// Rows of a tile and runs of its positions.  Few rows (16 or 32 at a time, waves deal the positions among
-// themselves): two workgroups of eight waves per compute unit, no run shorter than a tile of
-// positions per wave.  Many rows (256 at a time): one workgroup per compute unit, no run shorter than 256
-// positions, and at most 248 runs in all, whose parts are joined (64 MiB at D = 256).
+// Rows of a tile and runs of its positions.  Up to 96 rows of a sequence and kv head: 16 or 32 at a time,
+// waves deal the positions among themselves, two workgroups of eight waves per compute unit and no run
+// shorter than a tile of positions per wave; 256 units are left whole.  More rows: 128 or 256 at a time,
+// one or two workgroups per compute unit, no run shorter than 256 positions, and a workspace of at most 64
+// MiB.  16 sequences of 4096 with 8 kv heads of 64, 48, 80 and 112 rows: 32, 58 and 61 us by 32 rows, 48,
+// 51 and 55 by 128; 80 rows of lengths up to 4096 behind a window of 1500: 16 and 26; 131072 positions, 8
+// kv heads of 128, 64 and 120 rows: 100 and 161, 124 and 134.
 Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int D, int max_len) {
   Attn8Plan p;
   p.Hq = Hq;
   p.G = Hq / Hkv;
   const long long rows = (long long)max_q * p.G;
-  p.R = rows <= 16 ? 16 : rows < 128 ? 32 : 256;
+  const int many = attn8_rows(D / 32);
+  p.R = rows <= 16 ? 16 : rows <= 96 ? 32 : many;
   p.RT = (int)((rows + p.R - 1) / p.R);
   const long long units = (long long)B * Hkv * p.RT;
   const int most = (max_len + 255) / 256;
-  const long long want = p.R == 256 ? 248 / units : units >= 256 ? 1 : (512 + units - 1) / units;
+  const long long want = p.R == many ? 63488 / many / units : units >= 256 ? 1 : (512 + units - 1) / units;
   p.S = (int)(want < 1 ? 1 : want > most ? most : want);
   return p;
 }

@@ -127,8 +127,13 @@ hipError_t launch_kv_append_q8(hipStream_t s, const KvGeom& g, int xdt, int qdt,
 hipError_t launch_kv_read_q8(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
                              const int32_t* table, const void* cache, void* k, void* v);
 
-// Attention over the int8 cache: query heads, per kv head, rows of a tile (16, 32 or 256), tiles of
-// rows, runs of positions that a tile is cut into.
+// Rows of a workgroup of the kernel for many of them, D = 32 NG.  256 share the decoding (8192 tokens
+// of 32/8 heads of 128: 581 us, 621 by 128); where that is little, or the registers of a wave per SIMD are
+// needed, two workgroups of 128 are not held up by each other (heads of 64: 201 us and 217, of 256: 249
+// and 323, at 4096).
+constexpr int attn8_rows(int NG) { return NG == 3 || NG == 4 ? 256 : 128; }
+// Attention over the int8 cache: query heads, per kv head, rows of a tile (16, 32 or attn8_rows), tiles
+// of rows, runs of positions that a tile is cut into.
 struct Attn8Plan {
   int Hq, G, R, RT, S;
 };
