@@ -749,9 +749,14 @@ def sfx_attn_q4(q, cache, table, lens, out, ws, starts=None, scale=None, lse=Non
     page, num_pages, max_pages, Bt = _cache_shape(cache, table, D, Hkv, w)
     if Bt != B:
         raise ValueError(f"{w}: table must have {B} rows")
+    if lens.numel() != B:
+        raise ValueError(f"{w}: lens must hold {B} entries")
+    if lens.dtype is not _I32 or not lens.is_contiguous():
+        _not_dense(w, lens, "lens", _I32)
     dev = q.get_device()
-    if dev < 0 or cache.get_device() != dev or table.get_device() != dev or out.get_device() != dev:
-        _device_error(w, q, cache, table, out)
+    if (dev < 0 or cache.get_device() != dev or table.get_device() != dev or out.get_device() != dev or
+            lens.get_device() != dev):
+        _device_error(w, q, cache, table, lens, out)
     pl = pw = None
     nws = 0
     if lse is not None:
@@ -799,8 +804,9 @@ def sfx_norm_q8(x, q=None, s=None, weight=None, eps=1e-5, residual=None, residua
     if x.dim() != 2:
         raise ValueError(f"{w}: x must be [T][d]")
     T, d = shape = x.shape
-    if x.dtype not in WDT:
-        raise TypeError(f"{w}: unsupported dtype {x.dtype}")
+    xdt = x.dtype
+    if xdt not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {xdt}")
     dev = x.get_device()
     if dev < 0:
         _device_error(w, x)
@@ -808,37 +814,50 @@ def sfx_norm_q8(x, q=None, s=None, weight=None, eps=1e-5, residual=None, residua
     pr = pro = py = pq = ps = pw = None
     if residual is not None:
         ro = residual if residual_out is None else residual_out
-        if residual.shape != shape or ro.shape != shape or ro.dtype is not residual.dtype:
+        dt = residual.dtype
+        if residual.shape != shape or ro is not residual and (ro.shape != shape or ro.dtype is not dt):
             raise ValueError(f"{w}: residual and residual_out must be [{T}][{d}] of one dtype")
-        if residual.dtype not in WDT:
-            raise TypeError(f"{w}: unsupported dtype {residual.dtype}")
+        if dt not in WDT:
+            raise TypeError(f"{w}: unsupported dtype {dt}")
         if residual.get_device() != dev or ro.get_device() != dev:
             _device_error(w, x, residual, ro)
-        rdt, pr, pro = WDT[residual.dtype], residual.data_ptr(), ro.data_ptr()
-        ldr, ldro = _rows(residual, w, "residual"), _rows(ro, w, "residual_out")
+        rdt, pr = WDT[dt], residual.data_ptr()
+        ldr = d if residual.is_contiguous() else _rows(residual, w, "residual")
+        pro, ldro = (pr, ldr) if ro is residual else (ro.data_ptr(), d if ro.is_contiguous() else _rows(ro, w, "residual_out"))
     elif residual_out is not None:
         raise ValueError(f"{w}: residual_out without a residual")
     if y is not None:
         if y.shape != shape:
             raise ValueError(f"{w}: y must be [{T}][{d}]")
-        if y.dtype not in WDT:
-            raise TypeError(f"{w}: unsupported dtype {y.dtype}")
+        dt = y.dtype
+        if dt not in WDT:
+            raise TypeError(f"{w}: unsupported dtype {dt}")
         if y.get_device() != dev:
             _device_error(w, x, y)
-        ydt, py, ldy = WDT[y.dtype], y.data_ptr(), _rows(y, w, "y")
+        ydt, py, ldy = WDT[dt], y.data_ptr(), d if y.is_contiguous() else _rows(y, w, "y")
     if (q is None) != (s is None):
         raise ValueError(f"{w}: q and s go together")
     if q is not None:
         if q.shape != shape or s.numel() != T:
             raise ValueError(f"{w}: q must be [{T}][{d}] and s hold {T} values")
-        pq, ps = _dense(q, _I8, dev, w, "q"), _dense(s, _FP32, dev, w, "s")
+        if q.dtype is not _I8 or not q.is_contiguous():
+            _not_dense(w, q, "q", _I8)
+        if s.dtype is not _FP32 or not s.is_contiguous():
+            _not_dense(w, s, "s", _FP32)
+        if q.get_device() != dev or s.get_device() != dev:
+            _device_error(w, x, q, s)
+        pq, ps = q.data_ptr(), s.data_ptr()
     if weight is not None:
         if weight.numel() != d:
             raise ValueError(f"{w}: weight must hold {d} values")
-        pw = _dense(weight, _FP32, dev, w, "weight")
+        if weight.dtype is not _FP32 or not weight.is_contiguous():
+            _not_dense(w, weight, "weight", _FP32)
+        if weight.get_device() != dev:
+            _device_error(w, x, weight)
+        pw = weight.data_ptr()
     _run_on(dev, stream, (_lib or load()).sfx_norm_q8,
-            (WDT[x.dtype], rdt, ydt, T, d, 1 if norm else 0, eps, x.data_ptr(), _rows(x, w, "x"), pr, ldr, pro, ldro, pw,
-             pq, ps, py, ldy), w)
+            (WDT[xdt], rdt, ydt, T, d, 1 if norm else 0, eps, x.data_ptr(),
+             d if x.is_contiguous() else _rows(x, w, "x"), pr, ldr, pro, ldro, pw, pq, ps, py, ldy), w)
 
 
 def sfx_linear_q8(x, x_scales, W, W_scales, y, bias=None, accumulate=False, stream=None):
@@ -848,25 +867,32 @@ def sfx_linear_q8(x, x_scales, W, W_scales, y, bias=None, accumulate=False, stre
     if x.dim() != 2 or W.dim() != 2 or y.dim() != 2:
         raise ValueError(f"{w}: x, W and y must be 2-D")
     T, d = x.shape
-    n = W.shape[0]
-    if W.shape[1] != d or y.shape != (T, n) or x_scales.numel() != T or W_scales.numel() != n:
+    n, dw = W.shape
+    if dw != d or y.shape != (T, n) or x_scales.numel() != T or W_scales.numel() != n:
         raise ValueError(f"{w}: shape mismatch")
     if x.dtype is not _I8:
         raise TypeError(f"{w}: x is {x.dtype}, expected {_I8}")
-    if y.dtype not in WDT:
-        raise TypeError(f"{w}: unsupported dtype {y.dtype}")
+    ydt = y.dtype
+    if ydt not in WDT:
+        raise TypeError(f"{w}: unsupported dtype {ydt}")
+    if W.dtype is not _I8 or not W.is_contiguous():
+        _not_dense(w, W, "W", _I8)
+    if x_scales.dtype is not _FP32 or not x_scales.is_contiguous():
+        _not_dense(w, x_scales, "x_scales", _FP32)
+    if W_scales.dtype is not _FP32 or not W_scales.is_contiguous():
+        _not_dense(w, W_scales, "W_scales", _FP32)
     dev = x.get_device()
-    if dev < 0 or y.get_device() != dev:
-        _device_error(w, x, y)
+    if (dev < 0 or y.get_device() != dev or W.get_device() != dev or x_scales.get_device() != dev or
+            W_scales.get_device() != dev):
+        _device_error(w, x, x_scales, W, W_scales, y)
     pb = None
     if bias is not None:
         if bias.numel() != n:
             raise ValueError(f"{w}: bias must hold {n} values")
         pb = _dense(bias, _FP32, dev, w, "bias")
     _run_on(dev, stream, (_lib or load()).sfx_linear_q8,
-            (WDT[y.dtype], T, n, d, x.data_ptr(), d if x.is_contiguous() else _rows(x, w, "x"),
-             _dense(x_scales, _FP32, dev, w, "x_scales"), _dense(W, _I8, dev, w, "W"),
-             _dense(W_scales, _FP32, dev, w, "W_scales"), pb, 1 if accumulate else 0, y.data_ptr(),
+            (WDT[ydt], T, n, d, x.data_ptr(), d if x.is_contiguous() else _rows(x, w, "x"), x_scales.data_ptr(),
+             W.data_ptr(), W_scales.data_ptr(), pb, 1 if accumulate else 0, y.data_ptr(),
              n if y.is_contiguous() else _rows(y, w, "y")), w)
 
 
@@ -922,21 +948,33 @@ def sfx_kv_append_q8(q, k, v, lens, table, cache, q_out, q_start=None, cos_sin=N
         if odt is not _F16 and odt is not _BF16:
             raise TypeError(f"{w}: q_out must be fp16 or bf16")
         qdt = SFX_F16 if odt is _F16 else SFX_BF16
-        if q.get_device() != dev:
-            _device_error(w, k, q)
-        pq, ldq, pqo = q.data_ptr(), _head_rows(q, w, "q"), _dense(q_out, odt, dev, w, "q_out")
+        if not q_out.is_contiguous():
+            _not_dense(w, q_out, "q_out", odt)
+        if q.get_device() != dev or q_out.get_device() != dev:
+            _device_error(w, k, q, q_out)
+        pq, ldq, pqo = q.data_ptr(), Hq * D if q.is_contiguous() else _head_rows(q, w, "q"), q_out.data_ptr()
     rot, max_pos, pcs = 0, 0, None
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError(f"{w}: cos_sin must be [positions][rot]")
-        pcs = _dense(cos_sin, _FP32, dev, w, "cos_sin")
         max_pos, rot = cos_sin.shape
+        if cos_sin.dtype is not _FP32 or not cos_sin.is_contiguous():
+            _not_dense(w, cos_sin, "cos_sin", _FP32)
+        if cos_sin.get_device() != dev:
+            _device_error(w, k, cos_sin)
+        pcs = cos_sin.data_ptr()
     page, num_pages, max_pages, B = _cache8_shape(cache, table, D, Hkv, w)
+    if lens.numel() != B:
+        raise ValueError(f"{w}: lens must hold {B} entries")
+    if lens.dtype is not _I32 or not lens.is_contiguous():
+        _not_dense(w, lens, "lens", _I32)
+    if lens.get_device() != dev:
+        _device_error(w, k, lens)
     _run_on(dev, stream, (_lib or load()).sfx_kv_append_q8,
-            (WDT[xdt], qdt, T, Hq, Hkv, D, pq, ldq, k.data_ptr(), _head_rows(k, w, "k"), v.data_ptr(),
-             _head_rows(v, w, "v"), None if q_start is None else _tokens(q_start, B + 1, dev, w, "q_start"),
-             _tokens(lens, B, dev, w, "lens"), pcs, rot, max_pos, 1 if interleaved else 0, B, max_pages,
-             table.data_ptr(), page, num_pages, cache.data_ptr(), pqo), w)
+            (WDT[xdt], qdt, T, Hq, Hkv, D, pq, ldq, k.data_ptr(), Hkv * D if k.is_contiguous() else _head_rows(k, w, "k"),
+             v.data_ptr(), Hkv * D if v.is_contiguous() else _head_rows(v, w, "v"),
+             None if q_start is None else _tokens(q_start, B + 1, dev, w, "q_start"), lens.data_ptr(), pcs, rot, max_pos,
+             1 if interleaved else 0, B, max_pages, table.data_ptr(), page, num_pages, cache.data_ptr(), pqo), w)
 
 
 def sfx_kv_read_q8(pos, table, cache, k_out, v_out, seq=None, stream=None):
@@ -954,8 +992,14 @@ def sfx_kv_read_q8(pos, table, cache, k_out, v_out, seq=None, stream=None):
     if dev < 0 or v_out.get_device() != dev or table.get_device() != dev or cache.get_device() != dev:
         _device_error(w, k_out, v_out, table, cache)
     page, num_pages, max_pages, B = _cache8_shape(cache, table, D, Hkv, w)
+    if pos.numel() != T:
+        raise ValueError(f"{w}: pos must hold {T} entries")
+    if pos.dtype is not _I32 or not pos.is_contiguous():
+        _not_dense(w, pos, "pos", _I32)
+    if pos.get_device() != dev:
+        _device_error(w, k_out, pos)
     _run_on(dev, stream, (_lib or load()).sfx_kv_read_q8,
-            (WDT[odt], T, Hkv, D, _tokens(pos, T, dev, w, "pos"),
+            (WDT[odt], T, Hkv, D, pos.data_ptr(),
              None if seq is None else _tokens(seq, T, dev, w, "seq"), B, max_pages, table.data_ptr(), page,
              num_pages, cache.data_ptr(), k_out.data_ptr(), v_out.data_ptr()),
             w)
@@ -989,9 +1033,14 @@ def sfx_attn_q8(q, cache, table, lens, out, ws, q_start=None, max_q=1, starts=No
     page, num_pages, max_pages, B = _cache8_shape(cache, table, D, Hkv, w)
     if q_start is None and B != T:
         raise ValueError(f"{w}: table must have {T} rows")
+    if lens.numel() != B:
+        raise ValueError(f"{w}: lens must hold {B} entries")
+    if lens.dtype is not _I32 or not lens.is_contiguous():
+        _not_dense(w, lens, "lens", _I32)
     dev = q.get_device()
-    if dev < 0 or cache.get_device() != dev or table.get_device() != dev or out.get_device() != dev:
-        _device_error(w, q, cache, table, out)
+    if (dev < 0 or cache.get_device() != dev or table.get_device() != dev or out.get_device() != dev or
+            lens.get_device() != dev):
+        _device_error(w, q, cache, table, lens, out)
     pl = pw = None
     nws = 0
     if lse is not None:
@@ -1009,8 +1058,8 @@ def sfx_attn_q8(q, cache, table, lens, out, ws, q_start=None, max_q=1, starts=No
              Hq * D if q.is_contiguous() else _head_rows(q, w, "q"),
              None if q_start is None else _tokens(q_start, B + 1, dev, w, "q_start"), max_pages,
              table.data_ptr(), page, num_pages, cache.data_ptr(),
-             None if starts is None else _tokens(starts, B, dev, w, "starts"), _tokens(lens, B, dev, w, "lens"),
-             window, D ** -0.5 if scale is None else float(scale), out.data_ptr(), pl, pw, nws), w)
+             None if starts is None else _tokens(starts, B, dev, w, "starts"), lens.data_ptr(), window,
+             D ** -0.5 if scale is None else float(scale), out.data_ptr(), pl, pw, nws), w)
 
 
 STREAM_READ_OUT_WORDS = 16384
