@@ -62,11 +62,23 @@ __device__ __forceinline__ Found find_block(const Append8Args& a, int x, int lan
   return Found{-1, 0, {0, 0, 0}};
 }
 
-__device__ __forceinline__ int code8(float x, float s, float inv) {
-  const float t = x * inv;
-  float c = rintf(t);
-  if (!(fabsf(fabsf(t - c) - 0.5f) >= 0x1p-13f)) c = (float)rint((double)x / (double)s);
-  return (int)fminf(fmaxf(c, -127.f), 127.f);
+// u[j] = rne(x[j] a / s) + 128, a = 1 or the scale that integer x[j] had; r: a / s in fp32.
+__device__ __forceinline__ void codes8(const float (&x)[8], float a, float s, float r, uint32_t (&w)[2]) {
+  float c[8];
+  bool far = true;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = x[j] * r;
+    c[j] = rintf(t);
+    far = far && fabsf(fabsf(t - c[j]) - 0.5f) >= 0x1p-13f;
+  }
+  if (!far) {
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) c[j] = (float)rint((double)x[j] * (double)a / (double)s);
+  }
+  w[0] = w[1] = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)((int)fminf(fmaxf(c[j], -127.f), 127.f) + 128) << (8 * (j & 3));
 }
 
 // The larger of the kept scale and the new rows' (m: bits of their largest size).
@@ -141,7 +153,6 @@ __device__ __forceinline__ void append_block(const Append8Args& a, int x, int hg
   __syncthreads();
   // where a scale grows, and in a fresh block, every position is written
   const bool allk = fresh || ks != old.x, allv = fresh || vs != old.y;
-  const float ki = 1.0f / ks, vi = 1.0f / vs;
   uint8_t* cv = codes + (mine ? hs : 0) * 16 * D;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -151,33 +162,20 @@ __device__ __forceinline__ void append_block(const Append8Args& a, int x, int hg
     uint32_t kw[2] = {0x80808080u, 0x80808080u}, vw[2] = {0x80808080u, 0x80808080u};
     uint8_t *kp = blk + i * D + d0, *vp = blk + 16 * D + ((i >> 2) * D + d0) * 4 + (i & 3);
     if (is_new) {
-      if (ks > 0.f) {
-        kw[0] = kw[1] = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) kw[j >> 2] |= (uint32_t)(code8(y[p][j], ks, ki) + 128) << (8 * (j & 3));
-      }
-      if (vs > 0.f) {
-        vw[0] = vw[1] = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vw[j >> 2] |= (uint32_t)(code8(v[p][j], vs, vi) + 128) << (8 * (j & 3));
-      }
+      if (ks > 0.f) codes8(y[p], 1.0f, ks, 1.0f / ks, kw);
+      if (vs > 0.f) codes8(v[p], 1.0f, vs, 1.0f / vs, vw);
     } else if (!fresh) {
+      float was[8];
       if (allk && ks > 0.f) {
-        const Raw<8> was = load_raw<8>(kp);
-        kw[0] = kw[1] = 0;
+        const Raw<8> c = load_raw<8>(kp);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float q = (float)((int)((was.w[j >> 2] >> (8 * (j & 3))) & 255u) - 128);
-          kw[j >> 2] |= (uint32_t)((int)rint((double)q * (double)old.x / (double)ks) + 128) << (8 * (j & 3));
-        }
+        for (int j = 0; j < 8; ++j) was[j] = (float)((int)((c.w[j >> 2] >> (8 * (j & 3))) & 255u) - 128);
+        codes8(was, old.x, ks, old.x / ks, kw);
       }
       if (allv && vs > 0.f) {
-        vw[0] = vw[1] = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float q = (float)((int)vp[4 * j] - 128);
-          vw[j >> 2] |= (uint32_t)((int)rint((double)q * (double)old.y / (double)vs) + 128) << (8 * (j & 3));
-        }
+        for (int j = 0; j < 8; ++j) was[j] = (float)((int)vp[4 * j] - 128);
+        codes8(was, old.y, vs, old.y / vs, vw);
       }
     }
     if (allk || is_new) *(Raw<8>*)kp = Raw<8>{{kw[0], kw[1]}};
@@ -223,19 +221,29 @@ __device__ __forceinline__ void append_query(const Append8Args& a, int t) {
   Turn turn;
   if (a.cs && d0 < a.rot) load_turn(a, a.cs + (size_t)pos * a.rot, d0, turn);
   const bool apart = VEC && turn_apart(a, d0);
-  for (int h = threadIdx.x / slices; h < a.Hq; h += step) {
-    const size_t row = (size_t)t * a.ldq + (size_t)h * D;
-    const Eight<DT> own = load8<DT, VEC>(a.q, row + d0);
-    Eight<DT> oth = {};
-    if (apart) oth = load8<DT, VEC>(a.q, row + turn_other(a, d0));
-    float y[8];
-    turn8<DT, VEC>(a, a.q, row, d0, own, oth, turn, y);
-    const size_t out = ((size_t)t * a.Hq + h) * D + d0;
-    if constexpr (VEC) {
-      store8<QDT>(a.q_out, out, y);
-    } else {
+  constexpr int U = 4;                                         // heads on their way
+  for (int h0 = threadIdx.x / slices; h0 < a.Hq; h0 += U * step) {
+    Eight<DT> own[U], oth[U];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) store_elem<QDT>(a.q_out, out + j, y[j]);
+    for (int u = 0; u < U; ++u) {
+      const size_t row = (size_t)t * a.ldq + (size_t)min(h0 + u * step, a.Hq - 1) * D;
+      own[u] = load8<DT, VEC>(a.q, row + d0);
+      oth[u] = {};
+      if (apart) oth[u] = load8<DT, VEC>(a.q, row + turn_other(a, d0));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * step;
+      if (h >= a.Hq) break;
+      float y[8];
+      turn8<DT, VEC>(a, a.q, (size_t)t * a.ldq + (size_t)h * D, d0, own[u], oth[u], turn, y);
+      const size_t out = ((size_t)t * a.Hq + h) * D + d0;
+      if constexpr (VEC) {
+        store8<QDT>(a.q_out, out, y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) store_elem<QDT>(a.q_out, out + j, y[j]);
+      }
     }
   }
 }

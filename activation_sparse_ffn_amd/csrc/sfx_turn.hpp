@@ -105,8 +105,27 @@ __device__ __forceinline__ bool turn_first(const Rotation& a, int d) { return a.
 __device__ __forceinline__ int turn_other(const Rotation& a, int d) {
   return a.pairs ? d ^ 1 : d < (a.rot >> 1) ? d + (a.rot >> 1) : d - (a.rot >> 1);
 }
+// A slice's cosines and its sines are eight (pairs: four) neighbours each, except where a half ends
+// inside it.
+struct alignas(4) Four {
+  float v[4];
+};
 __device__ __forceinline__ void load_turn(const Rotation& a, const float* cs, int d0, Turn& t) {
-  const int half = a.rot >> 1;
+  const int half = a.rot >> 1, i0 = turn_pair(a, d0), n = a.pairs ? 4 : 8;
+  if (i0 + n <= half && (a.pairs || d0 + 8 <= half || d0 >= half)) {
+    const Four c = *(const Four*)(cs + i0), s = *(const Four*)(cs + half + i0);
+    Four c2 = c, s2 = s;
+    if (!a.pairs) {
+      c2 = *(const Four*)(cs + i0 + 4);
+      s2 = *(const Four*)(cs + half + i0 + 4);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      t.co[j] = a.pairs ? c.v[j >> 1] : j < 4 ? c.v[j & 3] : c2.v[j & 3];
+      t.si[j] = a.pairs ? s.v[j >> 1] : j < 4 ? s.v[j & 3] : s2.v[j & 3];
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int i = min(turn_pair(a, d0 + j), half - 1);         // dims past rot are not turned
