@@ -50,11 +50,11 @@ class StepBuffers:
 
 
 def run_layer(buf: StepBuffers, layer, x: torch.Tensor, threshold: float, act: str,
-              tok_bits: bool = True, stream=None, attn: "AttnStep" = None):
+              tok_bits: bool = True, stream=None, attn=None):
     """predict -> compact -> up -> down for one layer.  `layer` holds the device
     tensors W1, W2, Wa, ba, Wd (Wl, Wa_s, Wl_s, Wd_s when present).  With `attn` the
-    layer is a parallel block: its attention half (weights Wqkv, Wqkv_s, Wo, Wo_s, biases
-    bqkv, bo when present) reads the same x and is added to buf.y."""
+    layer is a parallel block: its attention half (an AttnStep or AttnStep8; weights Wqkv,
+    Wqkv_s, Wo, Wo_s, biases bqkv, bo when present) reads the same x and is added to buf.y."""
     g = layer.get if isinstance(layer, dict) else (lambda k: getattr(layer, k, None))
     if g("W1_s") is not None:
         A.sfx_predict_q4(x, g("W1"), g("W1_s"), g("W2"), g("W2_s"), buf.scores, buf.ws_pred, stream=stream)
@@ -119,6 +119,102 @@ class AttnStep:
                       stream=stream)
         A.sfx_linear_q4(self.o.view(self.B, -1), g("Wo"), g("Wo_s"), y, bias=g("bo"), accumulate=accumulate,
                         stream=stream)
+
+
+def rows_q8(w: torch.Tensor, stream=None):
+    """int8 codes [n][d] and fp32 row scales [n] of a matrix, as sfx_linear_q8 takes its weights."""
+    q = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+    s = torch.empty(w.shape[0], dtype=torch.float32, device=w.device)
+    A.sfx_norm_q8(w, q, s, norm=False, stream=stream)
+    return q, s
+
+
+class AttnStep8:
+    """The attention half of one layer in int8, for decode steps and for prompts: rows to int8
+    (normed first where the layer has the norm's weight `wn`), projection to queries, keys and
+    values, append to the layer's paged cache, attention over it, rows to int8, output projection.
+
+    Weights Wqkv, Wo int8 with row scales Wqkv_s, Wo_s (see rows_q8), biases bqkv, bo when present.
+    `table` [B][max pages] int32 (layers of a model may share it) and `pos` [B] int32, the position of
+    each sequence's token in a decode step (-1: no token; its output is the bias of the output
+    projection), are the caller's and may change between steps, also of a captured graph; the attention
+    covers positions max(0, pos + 1 - window) .. pos (window 0: all).  A pos without a page in `table`
+    or a row in `cos_sin` is no token either.  Prompts of up to `max_tokens` rows together.  `ffn_dtype`: that of the
+    rows that run_block's FFN reads."""
+
+    def __init__(self, d: int, Hq: int, Hkv: int, D: int, B: int, dtype: str, table: torch.Tensor, pos: torch.Tensor,
+                 num_pages: int, page: int = 16, cos_sin: torch.Tensor = None, interleaved: bool = False,
+                 scale: float = None, window: int = 0, eps: float = 1e-5, max_tokens: int = 0, ffn_dtype: str = None, device="cuda"):
+        self.d, self.Hq, self.Hkv, self.D, self.B, self.window, self.eps = d, Hq, Hkv, D, B, window, eps
+        self.table, self.pos, self.cos_sin, self.interleaved, self.scale = table, pos, cos_sin, interleaved, scale
+        dev = torch.device(device)
+        dt = TORCH_WDT[dtype]
+        rows = max(B, max_tokens)
+        self.cache = A.kv_cache_q8(num_pages, Hkv, page, D, dev)
+        self.xq = torch.empty(rows, d, dtype=torch.int8, device=dev)
+        self.xs = torch.empty(rows, dtype=torch.float32, device=dev)
+        self.qkv = torch.empty(rows, (Hq + 2 * Hkv) * D, dtype=torch.float32, device=dev)
+        self.q = torch.zeros(rows, Hq, D, dtype=dt, device=dev)
+        self.o = torch.zeros(rows, Hq, D, dtype=dt, device=dev)
+        self.oq = torch.empty(rows, Hq * D, dtype=torch.int8, device=dev)
+        self.os = torch.empty(rows, dtype=torch.float32, device=dev)
+        self.xf = torch.empty(B, d, dtype=dt if ffn_dtype is None else TORCH_WDT[ffn_dtype], device=dev)
+        self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.max_tokens = max_tokens
+        # decode steps and prompts may run on different streams, each with its workspace; calls of more
+        # than 65536 tokens per sequence take none
+        need = [A.sfx_attn_q8_ws(B, n, Hq, Hkv, D, table.shape[1] * page) for n in range(1, min(max_tokens, 65536) + 1)]
+        self.ws = A.workspace(A.sfx_attn_q8_ws(B, 1, Hq, Hkv, D, table.shape[1] * page), dev)
+        self.ws_prompt = A.workspace(max(need, default=0), dev)
+
+    def run(self, layer, x: torch.Tensor, y: torch.Tensor, accumulate: bool = False, add: torch.Tensor = None,
+            stream=None):
+        """y [B][d] (+)= the attention half of `layer` on x [B][d] at the positions `pos`; with `add`
+        x += add first (in place)."""
+        if x.shape != (self.B, self.d) or y.shape != x.shape:
+            raise ValueError(f"AttnStep8: x and y must be [{self.B}][{self.d}]")
+        A.sfx_kv_lens_q4(self.pos, self.table, self.cache.shape[2] * 16, self.cache.shape[0], self.lens,
+                         max_pos=0 if self.cos_sin is None else self.cos_sin.shape[0], stream=stream)
+        self._half(layer, x, y, None, self.lens, 1, self.ws, accumulate, add, stream)
+
+    def prompt(self, layer, x: torch.Tensor, y: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor, max_q: int,
+               accumulate: bool = False, add: torch.Tensor = None, stream=None):
+        """The same for rows q_start[b] .. q_start[b + 1] - 1 (at most max_q) of x [T][d], the last
+        tokens of sequence b, which has lens[b] positions with them (int32 device tensors [B + 1] and
+        [B]).  Rows of no sequence hold no result."""
+        if x.dim() != 2 or x.shape[1] != self.d or y.shape != x.shape:
+            raise ValueError(f"AttnStep8: x and y must be [rows][{self.d}]")
+        if x.shape[0] > self.max_tokens or max_q > self.max_tokens:
+            raise ValueError(f"AttnStep8: {x.shape[0]} rows, up to {max_q} of a sequence; room for {self.max_tokens}")
+        self._half(layer, x, y, q_start, lens, max_q, self.ws_prompt, accumulate, add, stream)
+
+    def _half(self, layer, x, y, q_start, lens, max_q, ws, accumulate, add, stream):
+        g = layer.get if isinstance(layer, dict) else (lambda k: getattr(layer, k, None))
+        T, a, b = x.shape[0], self.Hq * self.D, self.Hkv * self.D
+        wn = g("wn")
+        xq, xs, qkv, q, o, oq, os = (t[:T] for t in (self.xq, self.xs, self.qkv, self.q, self.o, self.oq, self.os))
+        A.sfx_norm_q8(x if add is None else add, xq, xs, weight=wn, eps=self.eps, residual=None if add is None else x,
+                      norm=wn is not None, stream=stream)
+        A.sfx_linear_q8(xq, xs, g("Wqkv"), g("Wqkv_s"), qkv, bias=g("bqkv"), stream=stream)
+        A.sfx_kv_append_q8(qkv[:, :a].unflatten(1, (self.Hq, self.D)), qkv[:, a:a + b].unflatten(1, (self.Hkv, self.D)),
+                           qkv[:, a + b:].unflatten(1, (self.Hkv, self.D)), lens, self.table, self.cache, q,
+                           q_start=q_start, cos_sin=self.cos_sin, interleaved=self.interleaved, stream=stream)
+        A.sfx_attn_q8(q, self.cache, self.table, lens, o, ws, q_start=q_start, max_q=max_q, window=self.window,
+                      scale=self.scale, stream=stream)
+        A.sfx_norm_q8(o.view(T, a), oq, os, norm=False, stream=stream)
+        A.sfx_linear_q8(oq, os, g("Wo"), g("Wo_s"), y, bias=g("bo"), accumulate=accumulate, stream=stream)
+
+
+def run_block(buf: StepBuffers, layer, res: torch.Tensor, attn: AttnStep8, threshold: float, act: str,
+              add: torch.Tensor = None, tok_bits: bool = True, stream=None):
+    """One decode step of a sequential pre-norm block on the residual stream res [B][d] (fp32, fp16 or
+    bf16), in place: res += add, res += attention half of norm(res) by the weight `wn`, then the
+    sparse FFN of norm(res) by the weight `wf` into buf.y, which is the next block's `add` (its norm adds
+    it).  The FFN reads rows of attn's `ffn_dtype` (its dtype where that is None)."""
+    g = layer.get if isinstance(layer, dict) else (lambda k: getattr(layer, k, None))
+    attn.run(layer, res, res, accumulate=True, add=add, stream=stream)
+    A.sfx_norm_q8(res, weight=g("wf"), eps=attn.eps, y=attn.xf, stream=stream)
+    run_layer(buf, layer, attn.xf, threshold, act, tok_bits=tok_bits, stream=stream)
 
 
 class TamState:
