@@ -8,8 +8,12 @@
 // ones here.  Codes are those of the exact quotient: fp32 decides them unless it comes to rest next to
 // a border.
 //
-// Rows of up to 32768 elements whose pieces of 8 are aligned stay in registers between the two
-// passes; workgroups take several rows and keep the weight.  Other rows are read twice.
+// A row is read twice, the second time out of a cache, in pieces of 8 at any place.  Where the rows
+// together are more than the last-level cache (256 MB) holds, they stay in registers between the two
+// passes instead, and workgroups take several, with the weight kept and the next one on its way.
+// Measured with fp32 weights (rows x length, types of x, residual, y; us by the first and the second):
+// 1 x 4096 f32 f32 f16 4.9 and 5.6; 512 x 8192 f32 16.7 and 20.9; 4099 x 8192 bf16 bf16 -
+// (235 MB, 4.3 TB/s) 54 and 57; 16384 x 4096 bf16 bf16 - 110 and 96; 4099 x 8192 f32 135 and 116.
 #include <type_traits>
 
 #include "sfx_launch.hpp"
@@ -92,6 +96,47 @@ __device__ __forceinline__ int row_code(const RowScale& c, double n) {
   return c.s > 0.f ? min(max(i + step, -127), 127) : 0;
 }
 
+// Rows may lie at any element: the copies below are one wide access each, which takes any address.
+template <int N>
+__device__ __forceinline__ Raw<N> load_at(const uint8_t* p) {
+  Raw<N> r;
+  __builtin_memcpy(&r, p, N);
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void store8_at(void* p, size_t i, const float (&x)[8]) {
+  constexpr int N = DT == DT_F32 ? 32 : 16;
+  Raw<16> r[N / 16];
+  store8<DT>(r, 0, x);
+  __builtin_memcpy((uint8_t*)p + i * (N / 8), r, N);
+}
+
+// Codes of eight n, from fp32 values m of n / s: four roundings of 2^-24 of at most 127, 2^-15, unless a
+// code comes to rest nearer to a border than 2^-14: then from n64(j), in 64 bits.  Adding 1.5 2^23
+// rounds to a whole number and leaves its low byte in place.
+template <class F>
+__device__ __forceinline__ Raw<8> codes8(const RowScale& c, const float (&m)[8], F n64) {
+  uint32_t u[8];
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float k = m[j] + 12582912.f;
+    near |= !(fabsf(m[j] - (k - 12582912.f)) <= 0.5f - 0x1p-14f);
+    u[j] = __float_as_uint(k);
+  }
+  Raw<8> q;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    q.w[k] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[4 * k + 3], u[4 * k + 2], 0x0c0c0400u),
+                                   __builtin_amdgcn_perm(u[4 * k + 1], u[4 * k], 0x0c0c0400u), 0x05040100u);
+  if (near || !(c.s > 0.f)) {
+    q = Raw<8>{{0, 0}};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q.w[j >> 2] |= ((uint32_t)row_code(c, n64(j)) & 255u) << (8 * (j & 3));
+  }
+  return q;
+}
+
 // Eight elements of a type known at run time as they lie; fp32 (WIDE) takes both registers' worth.
 template <bool WIDE>
 struct Any8 {
@@ -100,9 +145,9 @@ struct Any8 {
 template <bool WIDE>
 __device__ __forceinline__ void load_any(int dt, const void* p, size_t i, Any8<WIDE>& e) {
   const uint8_t* b = (const uint8_t*)p + i * (WIDE && dt == DT_F32 ? 4 : 2);
-  e.r[0] = load_raw<16>(b);
+  e.r[0] = load_at<16>(b);
   if constexpr (WIDE)
-    if (dt == DT_F32) e.r[1] = load_raw<16>(b + 16);
+    if (dt == DT_F32) e.r[1] = load_at<16>(b + 16);
 }
 template <bool WIDE>
 __device__ __forceinline__ void widen_any(int dt, const Any8<WIDE>& e, float (&x)[8]) {
@@ -116,18 +161,24 @@ __device__ __forceinline__ void widen_any(int dt, const Any8<WIDE>& e, float (&x
   else unpack<TBF16, 4>(e.r[0].w, x);
 }
 
+__device__ __forceinline__ void load_weights(const NormArgs& a, int i, float (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = 1.f;
+  if (a.w) __builtin_memcpy(w, a.w + i, 32);
+}
+
 // NT threads to a row, V pieces of 8 to a thread; the next row is on its way while one is worked on.
-// WIDE: x or the residual is fp32.
+// WIDE: x or the residual is fp32.  The last piece of a row whose length is no multiple of 8
+// starts inside the one before: what both have counts once in the sum and is stored twice alike.
 template <int NT, int V, bool WIDE>
-__global__ __launch_bounds__(NT) void k_norm_q8(NormArgs a) {
+__global__ __launch_bounds__(NT) void k_norm_q8_held(NormArgs a) {
   __shared__ double sh[2][NT / kWave];
   float w[V][8];
   bool bad_w = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = (v * NT + threadIdx.x) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[v][j] = a.w ? a.w[min(i, a.d - 8) + j] : 1.f;
+    load_weights(a, min(i, a.d - 8), w[v]);
     if (i < a.d)
 #pragma unroll
       for (int j = 0; j < 8; ++j) bad_w |= !(fabsf(w[v][j]) < INFINITY);
@@ -161,7 +212,13 @@ __global__ __launch_bounds__(NT) void k_norm_q8(NormArgs a) {
       float xf[8], rf[8];
       widen_any(a.xdt, x[v], xf);
       if (a.r) widen_any(a.rdt, r[v], rf);
-      if ((v * NT + (int)threadIdx.x) * 8 < a.d)
+      const int i = (v * NT + (int)threadIdx.x) * 8, twice = i - (a.d - 8);
+      if (twice > 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < twice) xf[j] = rf[j] = 0.f;
+      }
+      if (i < a.d)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const double h = a.r ? (double)xf[j] + (double)rf[j] : (double)xf[j];
@@ -178,8 +235,8 @@ __global__ __launch_bounds__(NT) void k_norm_q8(NormArgs a) {
     const float g = (float)(c.f * c.inv);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int i = (v * NT + threadIdx.x) * 8;
-      if (i >= a.d) continue;
+      if ((v * NT + (int)threadIdx.x) * 8 >= a.d) continue;
+      const int i = min((v * NT + (int)threadIdx.x) * 8, a.d - 8);
       float xf[8], rf[8], hf[8];
       widen_any(a.xdt, x[v], xf);
       if (a.r) widen_any(a.rdt, r[v], rf);
@@ -190,35 +247,18 @@ __global__ __launch_bounds__(NT) void k_norm_q8(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) hf[j] = a.r ? xf[j] + rf[j] : xf[j];
       if (a.q) {
-        // in fp32: four roundings of 2^-24 of at most 127, 2^-15, unless a code comes to rest nearer
-        // to a border than 2^-14: then in 64 bits.  Adding 1.5 2^23 rounds to a whole number and
-        // leaves its low byte in place.
-        uint32_t u[8];
-        bool near = false;
+        float mf[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float m = hf[j] * (g * w[v][j]), k = m + 12582912.f;
-          near |= !(fabsf(m - (k - 12582912.f)) <= 0.5f - 0x1p-14f);
-          u[j] = __float_as_uint(k);
-        }
-        uint32_t q[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          q[k] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[4 * k + 3], u[4 * k + 2], 0x0c0c0400u),
-                                       __builtin_amdgcn_perm(u[4 * k + 1], u[4 * k], 0x0c0c0400u), 0x05040100u);
-        if (near || !(c.s > 0.f)) {
-          q[0] = q[1] = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) q[j >> 2] |= ((uint32_t)row_code(c, n64(j)) & 255u) << (8 * (j & 3));
-        }
-        *(Raw<8>*)(a.q + (size_t)t * a.d + i) = Raw<8>{{q[0], q[1]}};
+        for (int j = 0; j < 8; ++j) mf[j] = hf[j] * (g * w[v][j]);
+        const Raw<8> q = codes8(c, mf, n64);
+        __builtin_memcpy(a.q + (size_t)t * a.d + i, &q, 8);
       }
-      if (a.r_out) by_type(a.rdt, [&](auto dt) { store8<decltype(dt)::value>(a.r_out, (size_t)t * a.ldro + i, hf); });
+      if (a.r_out) by_type(a.rdt, [&](auto dt) { store8_at<decltype(dt)::value>(a.r_out, (size_t)t * a.ldro + i, hf); });
       if (a.y) {
         float nf[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) nf[j] = (float)n64(j);
-        by_type(a.ydt, [&](auto dt) { store8<decltype(dt)::value>(a.y, (size_t)t * a.ldy + i, nf); });
+        by_type(a.ydt, [&](auto dt) { store8_at<decltype(dt)::value>(a.y, (size_t)t * a.ldy + i, nf); });
       }
       __builtin_amdgcn_sched_barrier(0);                       // one piece's temporaries at a time
     }
@@ -231,44 +271,106 @@ __device__ __forceinline__ float load_one(int dt, const void* p, size_t i) {
   return v;
 }
 
-// Any row, read twice.
-__global__ __launch_bounds__(kBlock) void k_norm_q8_any(NormArgs a) {
-  __shared__ double sh[2][kWavesPerBlock];
-  const int t = blockIdx.x;
+// A row to a workgroup of NT threads, read twice, with U pieces of 8 on their way to a thread; the
+// elements behind the last whole piece go one to a thread.
+template <int NT, bool WIDE>
+__global__ __launch_bounds__(NT) void k_norm_q8_twice(NormArgs a) {
+  constexpr int U = 2;
+  __shared__ double sh[2][NT / kWave];
+  const size_t t = blockIdx.x;
+  const int whole = a.d & ~7;
+  struct Piece {
+    Any8<WIDE> x, r;
+    float w[8];
+  };
+  const auto fetch = [&](int i, Piece& p) {
+    load_any(a.xdt, a.x, t * a.ldx + i, p.x);
+    if (a.r) load_any(a.rdt, a.r, t * a.ldr + i, p.r);
+    load_weights(a, i, p.w);
+  };
+  const auto widen_both = [&](const Piece& p, float (&x)[8], float (&r)[8]) {
+    widen_any(a.xdt, p.x, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = 0.f;
+    if (a.r) widen_any(a.rdt, p.r, r);
+  };
   const auto sum_of = [&](int i) {
-    double h = (double)load_one(a.xdt, a.x, (size_t)t * a.ldx + i);
-    if (a.r) h += (double)load_one(a.rdt, a.r, (size_t)t * a.ldr + i);
+    double h = (double)load_one(a.xdt, a.x, t * a.ldx + i);
+    if (a.r) h += (double)load_one(a.rdt, a.r, t * a.ldr + i);
     return h;
   };
   double sum = 0., top = 0.;
   bool bad = false;
-  for (int i = threadIdx.x; i < a.d; i += kBlock) {
-    const double h = sum_of(i), m = fabs(a.w ? h * (double)a.w[i] : h);
+  const auto count = [&](double h, float w) {
+    const double m = fabs(h * (double)w);
     sum = fma(h, h, sum);
     bad |= !(m < INFINITY);
     top = fmax(top, m);
+  };
+  const int tail = whole + (int)threadIdx.x;
+  if (tail < a.d) count(sum_of(tail), a.w ? a.w[tail] : 1.f);
+  for (int i0 = (int)threadIdx.x * 8; i0 < whole; i0 += U * NT * 8) {
+    Piece p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * NT * 8 < whole) fetch(i0 + u * NT * 8, p[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * NT * 8 >= whole) continue;
+      float x[8], r[8];
+      widen_both(p[u], x, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) count((double)x[j] + (double)r[j], p[u].w[j]);
+    }
   }
-  row_totals<kBlock>(sum, top, bad, sh);
+  row_totals<NT>(sum, top, bad, sh);
   const RowScale c = row_scale(a, sum, top, bad);
   if (a.s && threadIdx.x == 0) a.s[t] = c.s;
-  for (int i = threadIdx.x; i < a.d; i += kBlock) {
-    const double h = sum_of(i);                                // before res_out, which may be res, is written
-    double n = h * c.f;
-    if (a.w) n *= (double)a.w[i];
-    if (a.r_out) by_type(a.rdt, [&](auto dt) { store_elem<decltype(dt)::value>(a.r_out, (size_t)t * a.ldro + i, (float)h); });
-    if (a.y) by_type(a.ydt, [&](auto dt) { store_elem<decltype(dt)::value>(a.y, (size_t)t * a.ldy + i, (float)n); });
-    if (a.q) a.q[(size_t)t * a.d + i] = (int8_t)row_code(c, n);
+  const float g = (float)(c.f * c.inv);
+  for (int i = (int)threadIdx.x * 8; i < whole; i += NT * 8) {
+    Piece p;
+    fetch(i, p);                                               // before r_out, which may be r, is written
+    float x[8], r[8], hf[8], mf[8];
+    widen_both(p, x, r);
+    const auto n64 = [&](int j) { return ((double)x[j] + (double)r[j]) * c.f * (double)p.w[j]; };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      hf[j] = x[j] + r[j];
+      mf[j] = hf[j] * (g * p.w[j]);
+    }
+    if (a.q) {
+      const Raw<8> q = codes8(c, mf, n64);
+      __builtin_memcpy(a.q + t * a.d + i, &q, 8);
+    }
+    if (a.r_out) by_type(a.rdt, [&](auto dt) { store8_at<decltype(dt)::value>(a.r_out, t * a.ldro + i, hf); });
+    if (a.y) {
+      float nf[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) nf[j] = (float)n64(j);
+      by_type(a.ydt, [&](auto dt) { store8_at<decltype(dt)::value>(a.y, t * a.ldy + i, nf); });
+    }
+  }
+  if (tail < a.d) {
+    const double h = sum_of(tail), n = a.w ? h * c.f * (double)a.w[tail] : h * c.f;
+    if (a.q) a.q[t * a.d + tail] = (int8_t)row_code(c, n);
+    if (a.r_out) by_type(a.rdt, [&](auto dt) { store_elem<decltype(dt)::value>(a.r_out, t * a.ldro + tail, (float)h); });
+    if (a.y) by_type(a.ydt, [&](auto dt) { store_elem<decltype(dt)::value>(a.y, t * a.ldy + tail, (float)n); });
   }
 }
 
-// As many workgroups as the device holds at once, each with as many rows as any other or one less
-// (4099 x 8192, bf16 with residual: 59 us; one row to a workgroup, 87).
+template <int NT>
+void norm_twice(hipStream_t st, const NormArgs& a, bool wide) {
+  if (wide) k_norm_q8_twice<NT, true><<<dim3(a.T), dim3(NT), 0, st>>>(a);
+  else k_norm_q8_twice<NT, false><<<dim3(a.T), dim3(NT), 0, st>>>(a);
+}
+
+// As many workgroups as the device holds at once, each with as many rows as any other or one less.
 template <int NT, int V>
-void norm_run(hipStream_t st, const NormArgs& a) {
+void norm_held(hipStream_t st, const NormArgs& a, bool wide) {
   const int most = 256 * (V >= 4 ? 1 : 1024 / NT), each = (a.T + most - 1) / most;
-  const dim3 g((a.T + each - 1) / each), b(NT);
-  if (a.xdt == DT_F32 || (a.r && a.rdt == DT_F32)) k_norm_q8<NT, V, true><<<g, b, 0, st>>>(a);
-  else k_norm_q8<NT, V, false><<<g, b, 0, st>>>(a);
+  const dim3 g((a.T + each - 1) / each);
+  if (wide) k_norm_q8_held<NT, V, true><<<g, dim3(NT), 0, st>>>(a);
+  else k_norm_q8_held<NT, V, false><<<g, dim3(NT), 0, st>>>(a);
 }
 
 }  // namespace
@@ -277,23 +379,20 @@ hipError_t launch_norm_q8(hipStream_t st, int xdt, int rdt, int ydt, int T, int 
                           size_t ldx, const void* r, size_t ldr, void* r_out, size_t ldro, const float* w, int8_t* q,
                           float* s, void* y, size_t ldy) {
   const NormArgs a{x, r, r_out, w, q, s, y, ldx, ldr, ldro, ldy, (double)eps, T, d, norm, xdt, rdt, ydt};
-  const auto apart = [](const void* p, size_t ld, int dt) {     // pieces of 8 at 16-byte places
-    return p && (((uintptr_t)p & 15u) || ld * (dt == DT_F32 ? 4 : 2) % 16 != 0);
-  };
-  if (d % 8 != 0 || d > 32768 || ((uintptr_t)w & 15u) || apart(x, ldx, xdt) || apart(r, ldr, rdt) || apart(r_out, ldro, rdt) ||
-      apart(y, ldy, ydt)) {
-    k_norm_q8_any<<<dim3(T), dim3(kBlock), 0, st>>>(a);
-    return hipGetLastError();
-  }
-  const int pieces = d / 8;
-  if (pieces <= 64) norm_run<64, 1>(st, a);
-  else if (pieces <= 128 && T > 512) norm_run<64, 2>(st, a);
-  else if (pieces <= 256) norm_run<256, 1>(st, a);
-  else if (pieces <= 512 && T > 512) norm_run<256, 2>(st, a);
-  else if (pieces <= 512) norm_run<512, 1>(st, a);              // few rows: all the threads they take
-  else if (pieces <= 1024) norm_run<512, 2>(st, a);
-  else if (pieces <= 2048) norm_run<512, 4>(st, a);
-  else norm_run<1024, 4>(st, a);
+  const auto size = [](int dt) { return dt == DT_F32 ? 4 : 2; };
+  const bool wide = xdt == DT_F32 || (r && rdt == DT_F32);
+  if (d >= 8 && d <= 16384 && (long long)T * d * (size(xdt) + (r ? size(rdt) : 0)) > 192ll << 20) {
+    if (d <= 512) norm_held<64, 1>(st, a, wide);
+    else if (d <= 1024) norm_held<64, 2>(st, a, wide);
+    else if (d <= 2048) norm_held<256, 1>(st, a, wide);
+    else if (d <= 4096) norm_held<256, 2>(st, a, wide);
+    else if (d <= 8192) norm_held<512, 2>(st, a, wide);
+    else norm_held<512, 4>(st, a, wide);
+  } else if (d <= 512) norm_twice<64>(st, a, wide);             // a piece or two to a thread
+  else if (d <= 1024) norm_twice<128>(st, a, wide);             // (2048 x 1024: 7.9 us; by 64 or 256 threads 8.1, 10.2)
+  else if (d <= 2048 || (d <= 4096 && T > 512)) norm_twice<256>(st, a, wide);   // 4096 x 4096: 32 us, by 512 40
+  else if (d <= 16384 || T > 256) norm_twice<512>(st, a, wide);                 // 1 x 4096: 4.9 us, by 256 5.5
+  else norm_twice<1024>(st, a, wide);                           // 1 x 32768: 14.1 us, by 512 15.7
   return hipGetLastError();
 }
 

@@ -102,6 +102,34 @@ def test_norm(case):
         assert torch.equal(y, y4)
 
 
+NORM_MANY = [  # T, d, x, residual, y: more than the last-level cache holds
+    (76000, 333, "f32", "f32", "bf16"), (51000, 1000, "f16", "bf16", None), (12400, 2041, "f32", "f32", "f16"),
+    (12300, 4096, "bf16", "bf16", "f32"), (8200, 8190, "f32", None, None), (3200, 16384, "f16", "f16", "f16")]
+
+
+@pytest.mark.parametrize("case", NORM_MANY, ids=lambda c: "-".join(map(str, c)))
+def test_norm_many_rows(case):
+    """Rows spread over the call against the oracle; codes and scales of all against calls of fewer rows
+    (a scale could differ where two orders of a 64-bit sum fall on two sides of a border: about 2^-28 a row)."""
+    T, d, xt, rt, yt = case
+    say(f"norm {case}")
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x = (torch.randn(T, d, generator=g, device=DEV) * 2).to(DT[xt])
+    r = torch.randn(T, d, generator=g, device=DEV).to(DT[rt]) if rt else None
+    w = 1 + 0.3 * torch.randn(d, generator=g, device=DEV)
+    q, s = torch.full((T, d), 99, dtype=torch.int8, device=DEV), torch.full((T,), -1.0, device=DEV)
+    y = torch.full((T, d), 5.0, dtype=DT[yt], device=DEV) if yt else None
+    ro = None if r is None else r.clone()
+    A.sfx_norm_q8(x, q, s, weight=w, residual=ro, y=y)
+    rows = torch.from_numpy(np.unique(np.linspace(0, T - 1, 37).astype(int)))
+    at = lambda t: None if t is None else t.cpu()[rows]  # noqa: E731
+    check_norm((len(rows), d, xt, rt, yt, True, True), at(x), at(r), w.cpu(), at(q), at(s), at(ro), at(y))
+    for t in range(0, T, 2000):
+        q1, s1 = torch.empty_like(q[t:t + 2000]), torch.empty_like(s[t:t + 2000])
+        A.sfx_norm_q8(x[t:t + 2000], q1, s1, weight=w, residual=None if r is None else r[t:t + 2000])
+        assert torch.equal(q1, q[t:t + 2000]) and torch.equal(s1, s[t:t + 2000]), t
+
+
 @pytest.mark.parametrize("d", [40, 1000, 4096, 9000])
 def test_norm_special_rows(d):
     """Zeros, ties between codes, one value alone, the largest and smallest numbers, and rows with
