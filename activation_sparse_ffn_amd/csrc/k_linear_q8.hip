@@ -327,11 +327,10 @@ __global__ __launch_bounds__(WN * WT * kWave) void k_linear_q8_tiles(Linear8Args
 
   // out by way of LDS, 32 tokens x 64 rows of a wave at a time: straight from the registers a
   // store instruction would write 64 pieces of 8 bytes (240 us of 780 at 8192 x 16384 x 4096)
-  constexpr int LS = 68, esz = YT == DT_F32 ? 4 : 2;
+  constexpr int LS = 68;
   static_assert(NTH / 128 * 32 * LS * 4 <= (BN + BT) * kBK, "staging");
   __syncthreads();
   float* st = (float*)((wave & 1) ? buf1 : buf0) + (wave >> 1) * (32 * LS);
-  const bool vec = ((uintptr_t)a.y & 15u) == 0 && a.ldy * esz % 16 == 0;
   const int col = (lane & 7) * 8;
 #pragma unroll
   for (int i2 = 0; i2 < MI; i2 += 2) {
@@ -365,14 +364,14 @@ __global__ __launch_bounds__(WN * WT * kWave) void k_linear_q8_tiles(Linear8Args
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = (e < 4 ? v0[e & 3] : v1[e & 3]) * (sx * sw[e]) + bias[e];
         const size_t at = (size_t)t * a.ldy + nb;
-        if (vec && nb + 8 <= a.n) {
+        if (nb + 8 <= a.n) {
           if (a.accumulate) {
             float was[8];
-            widen<YT>(load8<YT, true>(a.y, at), was);
+            widen<YT>(load8_at<YT>(a.y, at), was);
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] += was[e];
           }
-          store8<YT>(a.y, at, o);
+          store8_at<YT>(a.y, at, o);                           // rows may lie at any element
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)

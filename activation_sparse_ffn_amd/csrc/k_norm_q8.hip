@@ -96,21 +96,6 @@ __device__ __forceinline__ int row_code(const RowScale& c, double n) {
   return c.s > 0.f ? min(max(i + step, -127), 127) : 0;
 }
 
-// Rows may lie at any element: the copies below are one wide access each, which takes any address.
-template <int N>
-__device__ __forceinline__ Raw<N> load_at(const uint8_t* p) {
-  Raw<N> r;
-  __builtin_memcpy(&r, p, N);
-  return r;
-}
-template <int DT>
-__device__ __forceinline__ void store8_at(void* p, size_t i, const float (&x)[8]) {
-  constexpr int N = DT == DT_F32 ? 32 : 16;
-  Raw<16> r[N / 16];
-  store8<DT>(r, 0, x);
-  __builtin_memcpy((uint8_t*)p + i * (N / 8), r, N);
-}
-
 // Codes of eight n, from fp32 values m of n / s: four roundings of 2^-24 of at most 127, 2^-15, unless a
 // code comes to rest nearer to a border than 2^-14: then from n64(j), in 64 bits.  Adding 1.5 2^23
 // rounds to a whole number and leaves its low byte in place.
@@ -145,9 +130,9 @@ struct Any8 {
 template <bool WIDE>
 __device__ __forceinline__ void load_any(int dt, const void* p, size_t i, Any8<WIDE>& e) {
   const uint8_t* b = (const uint8_t*)p + i * (WIDE && dt == DT_F32 ? 4 : 2);
-  e.r[0] = load_at<16>(b);
+  e.r[0] = load_raw_at<16>(b);
   if constexpr (WIDE)
-    if (dt == DT_F32) e.r[1] = load_at<16>(b + 16);
+    if (dt == DT_F32) e.r[1] = load_raw_at<16>(b + 16);
 }
 template <bool WIDE>
 __device__ __forceinline__ void widen_any(int dt, const Any8<WIDE>& e, float (&x)[8]) {

@@ -95,6 +95,26 @@ __device__ __forceinline__ void store8(void* p, size_t i, const float (&x)[8]) {
   }
 }
 
+// The same at any element: one wide access each, which takes any address.
+template <int N>
+__device__ __forceinline__ Raw<N> load_raw_at(const uint8_t* p) {
+  Raw<N> r;
+  __builtin_memcpy(&r, p, N);
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ Eight<DT> load8_at(const void* p, size_t i) {
+  Eight<DT> e;
+  __builtin_memcpy(&e, (const uint8_t*)p + i * (DT == DT_F32 ? 4 : 2), sizeof e);
+  return e;
+}
+template <int DT>
+__device__ __forceinline__ void store8_at(void* p, size_t i, const float (&x)[8]) {
+  Eight<DT> e;
+  store8<DT>(&e, 0, x);
+  __builtin_memcpy((uint8_t*)p + i * (DT == DT_F32 ? 4 : 2), &e, sizeof e);
+}
+
 // What turns a thread's dims d0 .. d0 + 7 at one position: cosine and sine per dim, whether it
 // is the first of its pair, and where the other one is.
 struct Turn {
