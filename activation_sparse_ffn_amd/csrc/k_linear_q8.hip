@@ -47,9 +47,11 @@ __device__ __forceinline__ void keep(Raw<16>& x, uint32_t mask) {
   for (int i = 0; i < 4; ++i) x.w[i] &= mask;
 }
 
+// One rounding of scales' product and one with the bias, written out so that every kernel takes the same.
+__device__ __forceinline__ float lin8_value(float sum, float sx, float sw, float bias) { return __builtin_fmaf(sum, sx * sw, bias); }
+
 __device__ __forceinline__ void lin8_store(const Linear8Args& a, int t, int i, int sum) {
-  float v = (float)sum * (a.sx[t] * a.sw[i]);
-  if (a.bias) v += a.bias[i];
+  float v = lin8_value((float)sum, a.sx[t], a.sw[i], a.bias ? a.bias[i] : 0.f);
   const size_t at = (size_t)t * a.ldy + i;
   const auto put = [&](auto dt) {
     constexpr int YT = decltype(dt)::value;
@@ -362,7 +364,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void k_linear_q8_tiles(Linear8Args
         const float sx = a.sx[t];
         float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = (e < 4 ? v0[e & 3] : v1[e & 3]) * (sx * sw[e]) + bias[e];
+        for (int e = 0; e < 8; ++e) o[e] = lin8_value(e < 4 ? v0[e & 3] : v1[e & 3], sx, sw[e], bias[e]);
         const size_t at = (size_t)t * a.ldy + nb;
         if (nb + 8 <= a.n) {
           if (a.accumulate) {

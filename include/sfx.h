@@ -616,7 +616,7 @@ int sfx_attn_q4(void* stream, int qdt, int B, int Hq, int Hkv, int D, const void
  *   accumulate  0: y is overwritten; otherwise the product is added to it, before it is rounded.
  *   y         [T] rows of n elements of ydt (SFX_F32, SFX_F16, SFX_BF16), ldy apart.
  * n 1..2^24, d a multiple of 16 in 16..131056: the sum of products is a 32-bit integer and exact; it
- * is rounded to fp32 once and multiplied by the rounded product of the scales.  Bitwise
+ * is rounded to fp32, multiplied by the rounded product of the scales and added to the bias with one rounding.  Bitwise
  * reproducible, and a token's y does not depend on the other tokens.  No workspace.
  * ------------------------------------------------------------------------------- */
 int sfx_norm_q8(void* stream, int xdt, int rdt, int ydt, int T, int d, int norm, float eps, const void* x, size_t ldx,

@@ -256,6 +256,24 @@ def test_linear_rows_apart(T, dt):
     assert torch.equal(one[0], y[-1])
 
 
+@pytest.mark.parametrize("n,d", [(333, 272), (1024, 4096), (9000, 512)])
+def test_linear_rows_do_not_depend_on_others(n, d):
+    """A token's y has the same bits in calls of any number of tokens, with and without bias and addition."""
+    say(f"linear rows alone {n}x{d}")
+    x, sx, W, sw, bias = (t.to(DEV) for t in make_linear(3000, n, d, n + d))
+    g = torch.Generator(device=DEV).manual_seed(d)
+    for dt in DT:
+        y0 = torch.randn(3000, n, generator=g, device=DEV).to(DT[dt])
+        for b, acc in ((bias, False), (None, True), (bias, True)):
+            ys = []
+            for T in (3000, 1, 4, 5, 16, 17, 64, 130, 600):
+                y = y0[:T].clone()
+                A.sfx_linear_q8(x[:T], sx[:T], W, sw, y, bias=b, accumulate=acc)
+                ys.append(y)
+            for y in ys[1:]:
+                assert torch.equal(y, ys[0][:len(y)]), (dt, acc, len(y))
+
+
 @pytest.mark.parametrize("T", [2, 30, 150, 400])
 def test_linear_bad_scales_stay_alone(T):
     """A NaN scale of a token or of a weight row makes its results NaN and no others'."""
