@@ -70,6 +70,9 @@ Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int D, int max_len) {
   return p;
 }
 
+// Workgroups of a call, also of rows that its sequences do not have.
+bool attn8_fits(const Attn8Plan& p, int B, int Hkv) { return (long long)B * Hkv * p.RT * p.S < (1 << 24); }
+
 size_t attn8_ws_bytes(const Attn8Plan& p, int B, int Hkv, int D) {
   if (p.S <= 1) return 0;
   return (size_t)B * Hkv * p.RT * p.S * p.R * (D + 2) * 4;
@@ -618,7 +621,8 @@ static bool attn8_shape(int B, int max_q, int Hq, int Hkv) {
 
 size_t sfx_attn_q8_ws(int B, int max_q, int Hq, int Hkv, int D, int max_len) {
   if (!attn8_shape(B, max_q, Hq, Hkv) || D < 32 || D > 256 || D % 32 != 0 || max_len < 1 || max_len > (1 << 30)) return 0;
-  return sfx::attn8_ws_bytes(sfx::attn8_plan(B, max_q, Hq, Hkv, D, max_len), B, Hkv, D);
+  const sfx::Attn8Plan p = sfx::attn8_plan(B, max_q, Hq, Hkv, D, max_len);
+  return sfx::attn8_fits(p, B, Hkv) ? sfx::attn8_ws_bytes(p, B, Hkv, D) : 0;
 }
 
 int sfx_attn_q8(void* stream, int qdt, int T, int B, int max_q, int Hq, int Hkv, int D, const void* q, size_t ldq,
@@ -638,6 +642,7 @@ int sfx_attn_q8(void* stream, int qdt, int T, int B, int max_q, int Hq, int Hkv,
       (lse && !aligned4(lse)))
     return SFX_E_ALIGN;
   const sfx::Attn8Plan p = sfx::attn8_plan(B, max_q, Hq, Hkv, D, max_pages * page);
+  if (!sfx::attn8_fits(p, B, Hkv)) return SFX_E_SHAPE;
   const int w = check_ws(ws, ws_bytes, sfx::attn8_ws_bytes(p, B, Hkv, D));
   if (w != SFX_OK) return w;
   const auto f = qdt == SFX_F16 ? sfx::launch_attn_q8_f16 : sfx::launch_attn_q8_bf16;

@@ -102,6 +102,9 @@ def test_attention_validation(lib):
     assert call(T=0) == E_SHAPE and call(T=(1 << 20) + 1) == E_SHAPE and call(max_q=0) == E_SHAPE
     assert call(q_start=None) == E_SHAPE and call(q_start=None, T=2, max_q=2) == E_SHAPE
     assert call(B=0) == E_SHAPE and call(B=4097) == E_SHAPE and call(Hq=7) == E_SHAPE and call(Hq=0) == E_SHAPE
+    # workgroups for rows that no sequence has: 2^12 x 8 x 2^17
+    assert call(B=4096, max_q=1 << 20, Hq=128, Hkv=8, ldq=128 * 64, T=1 << 20) == E_SHAPE
+    assert ws_of(B=4096, max_q=1 << 20, Hq=128, Hkv=8) == 0
     assert call(max_q=1 << 20, Hq=256, ldq=1 << 16, T=1 << 20) == E_SHAPE and call(window=-1) == E_SHAPE
     assert call(Hq=512, ldq=1 << 16) == E_SHAPE and call(ldq=511) == E_SHAPE and call(page=8) == E_SHAPE
     for s in (float("nan"), float("inf"), float("-inf")):
