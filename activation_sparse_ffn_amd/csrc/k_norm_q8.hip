@@ -13,7 +13,7 @@
 // passes instead, and workgroups take several, with the weight kept and the next one on its way.
 // Measured with fp32 weights (rows x length, types of x, residual, y; us by the first and the second):
 // 1 x 4096 f32 f32 f16 4.9 and 5.6; 512 x 8192 f32 16.7 and 20.9; 4099 x 8192 bf16 bf16 -
-// (235 MB, 4.3 TB/s) 54 and 57; 16384 x 4096 bf16 bf16 - 110 and 96; 4099 x 8192 f32 135 and 116.
+// (235 MB, 4.3 TB/s; 70 with nothing in the cache) 54 and 57; 16384 x 4096 bf16 bf16 - 110 and 96; 4099 x 8192 f32 135 and 116.
 #include <type_traits>
 
 #include "sfx_launch.hpp"
