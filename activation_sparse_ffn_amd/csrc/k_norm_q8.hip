@@ -31,7 +31,7 @@ struct NormArgs {
   float* s;
   void* y;
   size_t ldx, ldr, ldro, ldy;   // elements between rows
-  double eps;
+  double eps, per_d;            // per_d: 1 / d
   int T, d, norm, xdt, rdt, ydt;
 };
 
@@ -48,44 +48,58 @@ __device__ __forceinline__ double lane_xor_f64(double v, int o) {
   return __hiloint2double(hi, lo);
 }
 
-// Sum and largest of a workgroup's threads, and whether any holds `bad`.  (The barrier in front of
-// the writes keeps the last row's reads apart from them.)
-template <int NT>
-__device__ __forceinline__ void row_totals(double& sum, double& top, bool& bad, double (*sh)[NT / kWave]) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    sum += lane_xor_f64(sum, o);
-    top = fmax(top, lane_xor_f64(top, o));
-  }
-  if (__any(bad)) top = INFINITY;
-  if constexpr (NT > kWave) {
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-      sh[0][wave] = sum;
-      sh[1][wave] = top;
-    }
-    __syncthreads();
-    sum = top = 0.;
-#pragma unroll
-    for (int k = 0; k < NT / kWave; ++k) {
-      sum += sh[0][k];
-      top = fmax(top, sh[1][k]);
-    }
-  }
-  bad = !(top < INFINITY);
-}
-
 struct RowScale {
   double f, sd, inv;        // n = h f (w); scale and 1 / scale
   float s;
 };
 __device__ __forceinline__ RowScale row_scale(const NormArgs& a, double sum, double top, bool bad) {
   RowScale c;
-  c.f = a.norm ? 1.0 / sqrt(sum / a.d + a.eps) : 1.0;
-  c.s = bad ? __uint_as_float(0x7FC00000u) : (float)(top * c.f / 127.0);
+  c.f = a.norm ? 1.0 / sqrt(sum * a.per_d + a.eps) : 1.0;
+  c.s = bad ? __uint_as_float(0x7FC00000u) : (float)(top * c.f * (1.0 / 127.0));
   c.sd = (double)c.s;
   c.inv = 1.0 / c.sd;
+  return c;
+}
+
+// The scale of a row from its threads' sums, largest values and whether any holds `bad`.  The first wave
+// makes it for all (the divisions and the root are as much work as a few hundred elements); it is
+// stored by its first thread.
+template <int NT>
+__device__ __forceinline__ RowScale row_total(const NormArgs& a, double sum, double top, bool bad, size_t t, double (*sh)[NT / kWave],
+                                              RowScale& out) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    sum += lane_xor_f64(sum, o);
+    top = fmax(top, lane_xor_f64(top, o));
+  }
+  if (__any(bad)) top = INFINITY;
+  RowScale c;
+  if constexpr (NT > kWave) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      sh[0][wave] = sum;
+      sh[1][wave] = top;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      sum = top = 0.;
+#pragma unroll
+      for (int k = 0; k < NT / kWave; ++k) {
+        sum += sh[0][k];
+        top = fmax(top, sh[1][k]);
+      }
+      c = row_scale(a, sum, top, !(top < INFINITY));
+      if (threadIdx.x == 0) {
+        out = c;
+        if (a.s) a.s[t] = c.s;
+      }
+    }
+    __syncthreads();                                           // the next row's totals come behind all reads of sh
+    c = out;
+  } else {
+    c = row_scale(a, sum, top, !(top < INFINITY));
+    if (a.s && threadIdx.x == 0) a.s[t] = c.s;
+  }
   return c;
 }
 // The nearest code (ties to even): the rest n - k s of a candidate decides, exactly, as k s is.
@@ -158,6 +172,7 @@ __device__ __forceinline__ void load_weights(const NormArgs& a, int i, float (&w
 template <int NT, int V, bool WIDE>
 __global__ __launch_bounds__(NT) void k_norm_q8_held(NormArgs a) {
   __shared__ double sh[2][NT / kWave];
+  __shared__ RowScale scale;
   float w[V][8];
   bool bad_w = false;
 #pragma unroll
@@ -214,9 +229,7 @@ __global__ __launch_bounds__(NT) void k_norm_q8_held(NormArgs a) {
     }
     // h is finite where its square is, and h w where w is too
     bool bad = bad_w || !(sum < INFINITY);
-    row_totals<NT>(sum, top, bad, sh);
-    const RowScale c = row_scale(a, sum, top, bad);
-    if (a.s && threadIdx.x == 0) a.s[t] = c.s;
+    const RowScale c = row_total<NT>(a, sum, top, bad, t, sh, scale);
     const float g = (float)(c.f * c.inv);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -262,6 +275,7 @@ template <int NT, bool WIDE>
 __global__ __launch_bounds__(NT) void k_norm_q8_twice(NormArgs a) {
   constexpr int U = 2;
   __shared__ double sh[2][NT / kWave];
+  __shared__ RowScale scale;
   const size_t t = blockIdx.x;
   const int whole = a.d & ~7;
   struct Piece {
@@ -285,12 +299,11 @@ __global__ __launch_bounds__(NT) void k_norm_q8_twice(NormArgs a) {
     return h;
   };
   double sum = 0., top = 0.;
-  bool bad = false;
+  float w_not = 0.f;                                           // NaN behind a weight that is not finite
   const auto count = [&](double h, float w) {
-    const double m = fabs(h * (double)w);
     sum = fma(h, h, sum);
-    bad |= !(m < INFINITY);
-    top = fmax(top, m);
+    top = fmax(top, fabs(h * (double)w));
+    w_not = fmaf(w, 0.f, w_not);
   };
   const int tail = whole + (int)threadIdx.x;
   if (tail < a.d) count(sum_of(tail), a.w ? a.w[tail] : 1.f);
@@ -305,12 +318,19 @@ __global__ __launch_bounds__(NT) void k_norm_q8_twice(NormArgs a) {
       float x[8], r[8];
       widen_both(p[u], x, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) count((double)x[j] + (double)r[j], p[u].w[j]);
+      for (int j = 0; j < 8; ++j) {
+        const double h = a.r ? (double)x[j] + (double)r[j] : (double)x[j];
+        if (a.w) {
+          count(h, p[u].w[j]);
+        } else {
+          sum = fma(h, h, sum);
+          top = fmax(top, fabs(h));
+        }
+      }
     }
   }
-  row_totals<NT>(sum, top, bad, sh);
-  const RowScale c = row_scale(a, sum, top, bad);
-  if (a.s && threadIdx.x == 0) a.s[t] = c.s;
+  // h is finite where its square is, and h w where w is too
+  const RowScale c = row_total<NT>(a, sum, top, !(sum < INFINITY) || w_not != 0.f, t, sh, scale);
   const float g = (float)(c.f * c.inv);
   for (int i = (int)threadIdx.x * 8; i < whole; i += NT * 8) {
     Piece p;
@@ -363,7 +383,7 @@ void norm_held(hipStream_t st, const NormArgs& a, bool wide) {
 hipError_t launch_norm_q8(hipStream_t st, int xdt, int rdt, int ydt, int T, int d, int norm, float eps, const void* x,
                           size_t ldx, const void* r, size_t ldr, void* r_out, size_t ldro, const float* w, int8_t* q,
                           float* s, void* y, size_t ldy) {
-  const NormArgs a{x, r, r_out, w, q, s, y, ldx, ldr, ldro, ldy, (double)eps, T, d, norm, xdt, rdt, ydt};
+  const NormArgs a{x, r, r_out, w, q, s, y, ldx, ldr, ldro, ldy, (double)eps, 1.0 / d, T, d, norm, xdt, rdt, ydt};
   const auto size = [](int dt) { return dt == DT_F32 ? 4 : 2; };
   const bool wide = xdt == DT_F32 || (r && rdt == DT_F32);
   if (d >= 8 && d <= 16384 && (long long)T * d * (size(xdt) + (r ? size(rdt) : 0)) > 192ll << 20) {
