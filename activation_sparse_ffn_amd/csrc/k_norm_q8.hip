@@ -12,8 +12,9 @@
 // together are more than the last-level cache (256 MB) holds, they stay in registers between the two
 // passes instead, and workgroups take several, with the weight kept and the next one on its way.
 // Measured with fp32 weights (rows x length, types of x, residual, y; us by the first and the second):
-// 1 x 4096 f32 f32 f16 4.9 and 5.6; 512 x 8192 f32 16.7 and 20.9; 4099 x 8192 bf16 bf16 -
-// (235 MB, 4.3 TB/s; 70 with nothing in the cache) 54 and 57; 16384 x 4096 bf16 bf16 - 110 and 96; 4099 x 8192 f32 135 and 116.
+// 1 x 4096 f32 f32 f16 4.9 and 5.6; 512 x 8192 f32 16.7 and 20.9; 4099 x 8192 bf16 bf16 - (235 MB) 54 and
+// 57; 16384 x 4096 bf16 bf16 - 110 and 96; 4099 x 8192 f32 135 and 116.  Since, with fewer 64-bit
+// operations in both: 4.6, 17.0, 50 (4.7 TB/s; 65 with nothing in the cache) by the first, 90 by the second.
 #include <type_traits>
 
 #include "sfx_launch.hpp"
@@ -111,28 +112,24 @@ __device__ __forceinline__ int row_code(const RowScale& c, double n) {
 }
 
 // Codes of eight n, from fp32 values m of n / s: four roundings of 2^-24 of at most 127, 2^-15, unless a
-// code comes to rest nearer to a border than 2^-14: then from n64(j), in 64 bits.  Adding 1.5 2^23
-// rounds to a whole number and leaves its low byte in place.
+// code comes to rest nearer to a border than 2^-14, or s is no positive number (m is none then either): then
+// from n64(j), in 64 bits, one element at a time (all eight of a piece at once: 4099 x 8192 bf16 out of memory 74 us
+// instead of 65).  Adding
+// 1.5 2^23 rounds to a whole number and leaves its low byte in place.
 template <class F>
 __device__ __forceinline__ Raw<8> codes8(const RowScale& c, const float (&m)[8], F n64) {
   uint32_t u[8];
-  bool near = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float k = m[j] + 12582912.f;
-    near |= !(fabsf(m[j] - (k - 12582912.f)) <= 0.5f - 0x1p-14f);
     u[j] = __float_as_uint(k);
+    if (!(fabsf(m[j] - (k - 12582912.f)) <= 0.5f - 0x1p-14f)) u[j] = (uint32_t)row_code(c, n64(j));
   }
   Raw<8> q;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     q.w[k] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[4 * k + 3], u[4 * k + 2], 0x0c0c0400u),
                                    __builtin_amdgcn_perm(u[4 * k + 1], u[4 * k], 0x0c0c0400u), 0x05040100u);
-  if (near || !(c.s > 0.f)) {
-    q = Raw<8>{{0, 0}};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q.w[j >> 2] |= ((uint32_t)row_code(c, n64(j)) & 255u) << (8 * (j & 3));
-  }
   return q;
 }
 
