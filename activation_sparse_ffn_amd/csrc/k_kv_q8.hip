@@ -68,21 +68,14 @@ __device__ __forceinline__ Found find_block(const Append8Args& a, int x, int lan
 
 // u[j] = rne(x[j] a / s) + 128, a = 1 or the scale that integer x[j] had; r: a / s in fp32.
 __device__ __forceinline__ void codes8(const float (&x)[8], float a, float s, float r, uint32_t (&w)[2]) {
-  float c[8];
-  bool far = true;
+  w[0] = w[1] = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float t = x[j] * r;
-    c[j] = rintf(t);
-    far = far && fabsf(fabsf(t - c[j]) - 0.5f) >= 0x1p-13f;
+    float c = rintf(t);
+    if (!(fabsf(fabsf(t - c) - 0.5f) >= 0x1p-13f)) c = (float)rint((double)x[j] * (double)a / (double)s);
+    w[j >> 2] |= (uint32_t)((int)fminf(fmaxf(c, -127.f), 127.f) + 128) << (8 * (j & 3));
   }
-  if (!far) {
-#pragma unroll 1
-    for (int j = 0; j < 8; ++j) c[j] = (float)rint((double)x[j] * (double)a / (double)s);
-  }
-  w[0] = w[1] = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)((int)fminf(fmaxf(c[j], -127.f), 127.f) + 128) << (8 * (j & 3));
 }
 
 // The larger of the kept scale and the new rows' (m: bits of their largest size).
