@@ -7,8 +7,8 @@
 // A quotient is decided by an fp32 product with 1 / s unless that comes to rest within 2^-13 of a
 // border, where it is taken in 64 bits: codes are those of the exact quotient.
 //
-// 4095 tokens of 64 query and 8 kv heads of 128 dims, bf16: 37-43 us (160 MB, 3.8-4.3 TB/s); 8 single tokens of 32
-// heads: 6.6 us, offsets, page, rows, scale and kept codes one behind the other.  Reading 4109 positions of
+// 4095 tokens of 64 query and 8 kv heads of 128 dims, bf16: 34-40 us (160 MB, 4.0-4.7 TB/s); 8 single tokens of 32
+// heads: 6.0 us, offsets, page, rows, scale and kept codes one behind the other.  Reading 4109 positions of
 // 8 heads back: 8 us (25 MB).
 //
 // A workgroup takes one block of one head (several heads of fewer than 128 dims): the scale needs
