@@ -145,6 +145,8 @@ class AttnStep8:
     def __init__(self, d: int, Hq: int, Hkv: int, D: int, B: int, dtype: str, table: torch.Tensor, pos: torch.Tensor,
                  num_pages: int, page: int = 16, cos_sin: torch.Tensor = None, interleaved: bool = False,
                  scale: float = None, window: int = 0, eps: float = 1e-5, max_tokens: int = 0, ffn_dtype: str = None, device="cuda"):
+        if not 1 <= B <= 4096 or table.dim() != 2 or table.shape[0] != B:
+            raise ValueError(f"AttnStep8: table must be [{B}][max pages], with 1 to 4096 sequences")
         self.d, self.Hq, self.Hkv, self.D, self.B, self.window, self.eps = d, Hq, Hkv, D, B, window, eps
         self.table, self.pos, self.cos_sin, self.interleaved, self.scale = table, pos, cos_sin, interleaved, scale
         dev = torch.device(device)

@@ -310,3 +310,5 @@ def test_refusals():
         s.run(w, x[:2], y[:2])
     with pytest.raises(ValueError):
         s.run(w, x[:1], y[:1, :128])
+    with pytest.raises(ValueError):
+        AttnStep8(256, 4, 2, 64, 2, "f16", table.to(DEV), i32([0, 0]), pages)
