@@ -111,6 +111,14 @@ __device__ __forceinline__ int row_code(const RowScale& c, double n) {
   return c.s > 0.f ? min(max(i + step, -127), 127) : 0;
 }
 
+// f / s in fp32, what m below is made of.  It is 127 / max |h w|: where that or s is below fp32's normal numbers
+// it has fewer bits than m needs, and quotients by such an s pass 127.5.  NaN then, so that every code of
+// the row is taken in 64 bits.  (A product g w below them is off by 2^-150, times h by less than 2^-22.)
+__device__ __forceinline__ float row_factor(const RowScale& c) {
+  const float g = (float)(c.f * c.inv);
+  return g >= 0x1p-126f && c.s >= 0x1p-126f ? g : __uint_as_float(0x7FC00000u);
+}
+
 // Codes of eight n, from fp32 values m of n / s: four roundings of 2^-24 of at most 127, 2^-15, unless a
 // code comes to rest nearer to a border than 2^-14, or s is no positive number (m is none then either): then
 // from n64(j), in 64 bits, one element at a time (all eight of a piece at once: 4099 x 8192 bf16 out of memory 74 us
@@ -227,7 +235,7 @@ __global__ __launch_bounds__(NT) void k_norm_q8_held(NormArgs a) {
     // h is finite where its square is, and h w where w is too
     bool bad = bad_w || !(sum < INFINITY);
     const RowScale c = row_total<NT>(a, sum, top, bad, t, sh, scale);
-    const float g = (float)(c.f * c.inv);
+    const float g = row_factor(c);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if ((v * NT + (int)threadIdx.x) * 8 >= a.d) continue;
@@ -328,7 +336,7 @@ __global__ __launch_bounds__(NT) void k_norm_q8_twice(NormArgs a) {
   }
   // h is finite where its square is, and h w where w is too
   const RowScale c = row_total<NT>(a, sum, top, !(sum < INFINITY) || w_not != 0.f, t, sh, scale);
-  const float g = (float)(c.f * c.inv);
+  const float g = row_factor(c);
   for (int i = (int)threadIdx.x * 8; i < whole; i += NT * 8) {
     Piece p;
     fetch(i, p);                                               // before r_out, which may be r, is written
