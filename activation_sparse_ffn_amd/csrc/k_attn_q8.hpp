@@ -221,10 +221,9 @@ __device__ __forceinline__ int row8_lo(const Attn8Args& a, int start, int pos) {
 // The same for `R` rows at a time, `step` positions to a tile and runs of at least `least` tiles.
 __device__ __forceinline__ Span8 span8(const Attn8Args& a, const Seq8& sq, int start, int rt, int R, int step, int least) {
   const int i0 = R * rt / a.G, i1 = min(sq.n - 1, (R * rt + R - 1) / a.G);      // first and last token of the tile
-  const int first = sq.len - sq.n;
   Span8 s;
-  s.start = max(0, row8_lo(a, start, first + i0));
-  s.end = min(first + i1 + 1, a.kv.max_pages << a.kv.page_shift);
+  s.start = max(0, row8_lo(a, start, sq.pos + i0));
+  s.end = min(sq.pos + i1 + 1, a.kv.max_pages << a.kv.page_shift);
   s.t0 = s.start / step;
   s.ntile = s.end > s.start ? (s.end + step - 1) / step - s.t0 : 0;
   s.per = max(least, (s.ntile + a.S - 1) / a.S);
@@ -252,7 +251,7 @@ __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a
   const Seq8 sq = rows8_seq(a.rows, b);
   const int rows = min(R, sq.n * a.G - R * rt);                // of this tile
   if (rows <= 0) return;
-  const int start = a.starts ? max(a.starts[b], 0) : 0, first = sq.len - sq.n;
+  const int start = a.starts ? max(a.starts[b], 0) : 0, first = sq.pos;
   const Span8 sp = span8(a, sq, start, rt, R, kTile8, W);
   if (split >= sp.active) return;
   const int tb = sp.t0 + split * sp.per, te = min(sp.t0 + sp.ntile, tb + sp.per);
@@ -512,7 +511,7 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
   const Seq8 sq = rows8_seq(a.rows, b);
   const int rows = min(kRows8, sq.n * a.G - kRows8 * rt);
   if (rows <= 0) return;
-  const int start = a.starts ? max(a.starts[b], 0) : 0, first = sq.len - sq.n;
+  const int start = a.starts ? max(a.starts[b], 0) : 0, first = sq.pos;
   const Span8 sp = span8(a, sq, start, rt, kRows8, kTileR8, kLeastR8);
   if (split >= sp.active) return;
   const int t0 = sp.t0 + split * sp.per, t1 = min(sp.t0 + sp.ntile, t0 + sp.per);

@@ -42,7 +42,7 @@ __device__ __forceinline__ Found find_block(const Append8Args& a, int x, int lan
   int before = 0;
   for (int b0 = 0; b0 < a.kv.B; b0 += kWave) {
     const int b = b0 + lane;
-    Seq8 s{0, 0, 0};
+    Seq8 s{};
     int nb = 0;
     if (b < a.kv.B) {
       s = rows8_seq(a.rows, b);
@@ -63,7 +63,7 @@ __device__ __forceinline__ Found find_block(const Append8Args& a, int x, int lan
     }
     before = __builtin_amdgcn_readlane(upto, kWave - 1);
   }
-  return Found{-1, 0, {0, 0, 0}};
+  return Found{-1, 0, {}};
 }
 
 // u[j] = rne(x[j] a / s) + 128, a = 1 or the scale that integer x[j] had; r: a / s in fp32.
@@ -199,19 +199,20 @@ template <int DT, int QDT, bool VEC>
 __device__ __forceinline__ void append_query(const Append8Args& a, int t) {
   const int D = a.kv.D, slices = D >> 3, lane = threadIdx.x & 63;
   int b = -1;
-  Seq8 s{0, 0, 0};
+  Seq8 s{};
   for (int b0 = 0; b0 < a.kv.B && b < 0; b0 += kWave) {
-    Seq8 m{0, 0, 0};
+    Seq8 m{};
     if (b0 + lane < a.kv.B) m = rows8_seq(a.rows, b0 + lane);
     const uint64_t in = __ballot(t >= m.first && t < m.first + m.n);
     if (in) {
       const int l = __builtin_ctzll(in);
       b = b0 + l;
-      s = Seq8{__builtin_amdgcn_readlane(m.first, l), __builtin_amdgcn_readlane(m.n, l), __builtin_amdgcn_readlane(m.len, l)};
+      s.first = __builtin_amdgcn_readlane(m.first, l);
+      s.pos = __builtin_amdgcn_readlane(m.pos, l);
     }
   }
   if (b < 0) return;
-  const int pos = s.len - s.n + (t - s.first);
+  const int pos = s.pos + (t - s.first);
   if (pos < 0 || (a.cs && pos >= a.max_pos) || kv_page(a.kv, b, pos) < 0) return;
   const int step = kBlock / slices, slice = threadIdx.x % slices, d0 = 8 * slice;
   if ((int)threadIdx.x >= step * slices) return;

@@ -23,13 +23,15 @@ __device__ __forceinline__ size_t kv8_block(const KvCache& kv, int id, int h, in
 
 // Rows of a call: sequence b has rows first .. first + n - 1, the last n of its `len` positions.
 // Without offsets row b is sequence b's last position.  A sequence with n > len has rows in front
-// of position 0: they have no position.
+// of position 0: they have no position.  Of a sequence with more than `most` rows the first ones are taken, at
+// the positions that they have among all.
 struct Rows8 {
   const int32_t *start, *lens;   // [B + 1] or null; [B]
   int T, most;                   // rows of the call, at most `most` of a sequence
 };
 struct Seq8 {
   int first, n, len;
+  int pos;                       // position of row `first`
 };
 __device__ __forceinline__ Seq8 rows8_seq(const Rows8& r, int b) {
   Seq8 s;
@@ -37,9 +39,12 @@ __device__ __forceinline__ Seq8 rows8_seq(const Rows8& r, int b) {
   if (!r.start) {
     s.first = b;
     s.n = 1;
+    s.pos = s.len - 1;
   } else {
     s.first = min(max(r.start[b], 0), r.T);
-    s.n = min(max(r.start[b + 1] - s.first, 0), min(r.T - s.first, r.most));
+    const int all = min(max(r.start[b + 1] - s.first, 0), r.T - s.first);
+    s.n = min(all, r.most);
+    s.pos = s.len - all;
   }
   return s;
 }

@@ -665,8 +665,9 @@ int sfx_linear_q8(void* stream, int ydt, int T, int n, int d, const int8_t* x, s
  *   h / (Hq / Hkv): causal, and with a sliding window (0: none).
  *   qdt       SFX_F16 or SFX_BF16 (q and out).   Hq 1..256, Hq % Hkv == 0.
  *   q         [T][Hq][D], tokens ldq elements apart (a multiple of 8).
- *   max_q     1..2^20, at least the most rows that a sequence has (rows past it are left out); 1
- *             where q_start is NULL.  max_q Hq / Hkv <= 2^26, and workgroups for max_q rows of all B
+ *   max_q     1..2^20, at least the most rows that a sequence has (of one with more the first max_q are
+ *             taken, at their positions among all, the others left out); 1 where q_start is
+ *             NULL.  max_q Hq / Hkv <= 2^26, and workgroups for max_q rows of all B
  *             sequences stay below 2^24: B Hq max_q <= 2^30 always does (SFX_E_SHAPE).
  *   starts    [B] int32 or NULL (0): left padding.  Nothing to attend to gives a zero row and
  *             lse = -inf.  Positions without a page are left out; what the cache holds in blocks
