@@ -215,8 +215,9 @@ __device__ __forceinline__ float attn8_lse(float ref, float sum) {
 struct Span8 {
   int start, end, t0, ntile, per, active;
 };
+// (The difference stays within 32 bits for rows in front of position 0 and any window too.)
 __device__ __forceinline__ int row8_lo(const Attn8Args& a, int start, int pos) {
-  return a.window ? max(start, pos + 1 - a.window) : start;
+  return a.window && pos >= a.window ? max(start, pos + 1 - a.window) : start;
 }
 // The same for `R` rows at a time, `step` positions to a tile and runs of at least `least` tiles.
 __device__ __forceinline__ Span8 span8(const Attn8Args& a, const Seq8& sq, int start, int rt, int R, int step, int least) {

@@ -116,3 +116,21 @@ def test_attention_fewer_rows_than_a_sequence_has(dt):
         cache = make_cache(pages, Hkv, 16, D, 4)
         check_rows(Hq, Hkv, D, dt, 16, table, cache, lens, counts, max_q=most, rows=9)
         check_rows(Hq, Hkv, D, dt, 16, table, cache, lens, counts, max_q=most, rows=9, window=30, starts=[2] * len(lens))
+
+
+def test_attention_windows_past_every_position():
+    """The longest window is none, also for calls with rows in front of position 0."""
+    D, page = 64, 16
+    lens, counts = [3, 40, 7, 0], [9, 5, 120, 6]
+    table, pages = make_table(lens, page, 3)
+    cache = make_cache(pages, 2, page, D, 4)
+    q_start = np.concatenate([[0], np.cumsum(counts)])
+    q = torch.randn(int(q_start[-1]), 4, D, generator=torch.Generator().manual_seed(1)).half().to(DEV)
+    ws = A.workspace(A.sfx_attn_q8_ws(4, 120, 4, 2, D, table.shape[1] * page))
+    outs = []
+    for window in (0, 2 ** 31 - 1, 2 ** 31 - 5, 1 << 20):
+        outs.append((torch.full_like(q, 7.0), torch.full((len(q), 4), 7.0, device=DEV)))
+        A.sfx_attn_q8(q, cache.to(DEV), table.to(DEV), i32(lens), outs[-1][0], ws, q_start=i32(q_start), max_q=120, window=window, lse=outs[-1][1])
+    assert (outs[0][0][6:9] != 0).any() and (outs[0][0][:6] == 0).all()
+    for o, l in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1])
