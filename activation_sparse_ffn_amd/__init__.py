@@ -14,6 +14,6 @@ from ._abi import sfx_hot_update, sfx_topk_now_update  # noqa: F401
 from ._abi import kv_cache_q4, sfx_attn_q4, sfx_attn_q4_ws, sfx_kv_append_q4, sfx_kv_lens_q4  # noqa: F401
 from ._abi import sfx_kv_read_q4, sfx_linear_q4  # noqa: F401
 from ._abi import kv_cache_q8, sfx_attn_q8, sfx_attn_q8_ws, sfx_kv_append_q8, sfx_kv_read_q8  # noqa: F401
-from ._abi import sfx_linear_q8, sfx_norm_q8  # noqa: F401
+from ._abi import sfx_kv_blank_q8, sfx_linear_q8, sfx_norm_q8  # noqa: F401
 from .step import AttnStep, AttnStep8, HotRegion, StackStep, StepBuffers, TamState, TopKNowState  # noqa: F401
 from .step import rows_q8, run_block, run_layer  # noqa: F401

@@ -28,7 +28,8 @@ EXPORTS = ("sfx_status_str", "sfx_abi_version", "sfx_predict_ws", "sfx_predict",
            "sfx_select_kth", "sfx_hot_first_order_ws", "sfx_hot_first_order", "sfx_gather_rows",
            "sfx_dense_ffn_ws", "sfx_dense_ffn", "sfx_linear_q4", "sfx_kv_cache_bytes", "sfx_kv_append_q4",
            "sfx_kv_read_q4", "sfx_kv_lens_q4", "sfx_attn_q4_ws", "sfx_attn_q4", "sfx_norm_q8", "sfx_linear_q8",
-           "sfx_kv_cache_q8_bytes", "sfx_kv_append_q8", "sfx_kv_read_q8", "sfx_attn_q8_ws", "sfx_attn_q8")
+           "sfx_kv_cache_q8_bytes", "sfx_kv_append_q8", "sfx_kv_blank_q8", "sfx_kv_read_q8", "sfx_attn_q8_ws",
+           "sfx_attn_q8")
 HOT_MAX_MATS = 8
 SFX_DOWN_SCRATCH_BYTES = 17 << 20
 
@@ -141,6 +142,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sfx_kv_cache_q8_bytes.argtypes = [I, I, I, I]
     lib.sfx_kv_append_q8.restype = I
     lib.sfx_kv_append_q8.argtypes = [P, I, I, I, I, I, I, P, Z, P, Z, P, Z, P, P, P, I, I, I, I, I, P, I, I, P, P]
+    lib.sfx_kv_blank_q8.restype = I
+    lib.sfx_kv_blank_q8.argtypes = [P, I, I, P, P, I, I, I, I, P, I, I, P]
     lib.sfx_kv_read_q8.restype = I
     lib.sfx_kv_read_q8.argtypes = [P, I, I, I, I, P, P, I, I, P, I, I, P, P, P]
     lib.sfx_attn_q8_ws.restype = Z
@@ -975,6 +978,27 @@ def sfx_kv_append_q8(q, k, v, lens, table, cache, q_out, q_start=None, cos_sin=N
              v.data_ptr(), Hkv * D if v.is_contiguous() else _head_rows(v, w, "v"),
              None if q_start is None else _tokens(q_start, B + 1, dev, w, "q_start"), lens.data_ptr(), pcs, rot, max_pos,
              1 if interleaved else 0, B, max_pages, table.data_ptr(), page, num_pages, cache.data_ptr(), pqo), w)
+
+
+def sfx_kv_blank_q8(x, lens, table, page: int, num_pages: int, q_start=None, max_q=1, max_pos=0, stream=None):
+    """Zeroes the rows of x [T][n] (fp16 / bf16) that are no token of a call: those that sfx_kv_append_q8 does not
+    store (with angles for `max_pos` positions; 0: no angles) and those past a sequence's first max_q."""
+    w = "sfx_kv_blank_q8"
+    if x.dim() != 2 or table.dim() != 2:
+        raise ValueError(f"{w}: x must be [T][n], table [B][max pages]")
+    if x.dtype is not _F16 and x.dtype is not _BF16:
+        raise TypeError(f"{w}: x must be fp16 or bf16")
+    if not x.is_contiguous():
+        _not_dense(w, x, "x", x.dtype)
+    if table.dtype is not _I32 or not table.is_contiguous():
+        _not_dense(w, table, "table", _I32)
+    B, max_pages = table.shape
+    dev = x.get_device()
+    if dev < 0 or table.get_device() != dev:
+        _device_error(w, x, table)
+    _run_on(dev, stream, (_lib or load()).sfx_kv_blank_q8,
+            (x.shape[0], x.shape[1], None if q_start is None else _tokens(q_start, B + 1, dev, w, "q_start"),
+             _tokens(lens, B, dev, w, "lens"), max_pos, max_q, B, max_pages, table.data_ptr(), page, num_pages, x.data_ptr()), w)
 
 
 def sfx_kv_read_q8(pos, table, cache, k_out, v_out, seq=None, stream=None):

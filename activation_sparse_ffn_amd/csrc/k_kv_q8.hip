@@ -194,26 +194,27 @@ __device__ __forceinline__ void append_block(const Append8Args& a, int x, int hg
   if (rest == 0) *(float2*)(blk + 32 * D) = make_float2(ks, vs);
 }
 
+// Position of row t where the append stores it (angles for max_pos positions; 0: no angles), else -1.  Each wave
+// finds it for itself, 64 sequences at a time.
+__device__ __forceinline__ int stored_pos(const KvCache& kv, const Rows8& rows, int max_pos, int t, int lane) {
+  for (int b0 = 0; b0 < kv.B; b0 += kWave) {
+    Seq8 s{};
+    if (b0 + lane < kv.B) s = rows8_seq(rows, b0 + lane);
+    const uint64_t in = __ballot(t >= s.first && t < s.first + s.n);
+    if (!in) continue;
+    const int l = __builtin_ctzll(in);
+    const int pos = __builtin_amdgcn_readlane(s.pos, l) + t - __builtin_amdgcn_readlane(s.first, l);
+    return pos < 0 || (max_pos && pos >= max_pos) || kv_page(kv, b0 + l, pos) < 0 ? -1 : pos;
+  }
+  return -1;
+}
+
 // Queries of one token.
 template <int DT, int QDT, bool VEC>
 __device__ __forceinline__ void append_query(const Append8Args& a, int t) {
-  const int D = a.kv.D, slices = D >> 3, lane = threadIdx.x & 63;
-  int b = -1;
-  Seq8 s{};
-  for (int b0 = 0; b0 < a.kv.B && b < 0; b0 += kWave) {
-    Seq8 m{};
-    if (b0 + lane < a.kv.B) m = rows8_seq(a.rows, b0 + lane);
-    const uint64_t in = __ballot(t >= m.first && t < m.first + m.n);
-    if (in) {
-      const int l = __builtin_ctzll(in);
-      b = b0 + l;
-      s.first = __builtin_amdgcn_readlane(m.first, l);
-      s.pos = __builtin_amdgcn_readlane(m.pos, l);
-    }
-  }
-  if (b < 0) return;
-  const int pos = s.pos + (t - s.first);
-  if (pos < 0 || (a.cs && pos >= a.max_pos) || kv_page(a.kv, b, pos) < 0) return;
+  const int D = a.kv.D, slices = D >> 3;
+  const int pos = stored_pos(a.kv, a.rows, a.cs ? a.max_pos : 0, t, threadIdx.x & 63);
+  if (pos < 0) return;
   const int step = kBlock / slices, slice = threadIdx.x % slices, d0 = 8 * slice;
   if ((int)threadIdx.x >= step * slices) return;
   Turn turn;
@@ -253,6 +254,20 @@ __global__ __launch_bounds__(kBlock) void k_kv_append8(Append8Args a) {
   const int kv_groups = a.blocks * a.hgroups;
   if ((int)blockIdx.x < kv_groups) append_block<DT, VEC>(a, blockIdx.x / a.hgroups, blockIdx.x % a.hgroups, codes, sh_max);
   else append_query<DT, QDT, VEC>(a, blockIdx.x - kv_groups);
+}
+
+struct Blank8Args {
+  KvCache kv;
+  Rows8 rows;
+  uint8_t* x;
+  int max_pos, bytes;       // bytes of a row
+};
+
+// A wave per row.  8192 rows of 16 KiB of one sequence: 5.9 us a call where all are tokens (the launch), 21 where none is.
+__global__ __launch_bounds__(kBlock) void k_kv_blank8(Blank8Args a) {
+  const int lane = threadIdx.x & 63, t = blockIdx.x * kWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= a.rows.T || stored_pos(a.kv, a.rows, a.max_pos, t, lane) >= 0) return;
+  for (int e = lane * 16; e < a.bytes; e += kWave * 16) *(Raw<16>*)(a.x + (size_t)t * a.bytes + e) = zero16();
 }
 
 struct Read8Args {
@@ -330,6 +345,14 @@ hipError_t launch_kv_append_q8(hipStream_t s, const KvGeom& g, int xdt, int qdt,
   if (xdt == DT_F32) run_append8<DT_F32>(s, a, grid, qdt, vec);
   else if (xdt == DT_F16) run_append8<DT_F16>(s, a, grid, qdt, vec);
   else run_append8<DT_BF16>(s, a, grid, qdt, vec);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_blank_q8(hipStream_t s, const KvGeom& g, int T, int n, void* x, const int32_t* q_start,
+                              const int32_t* lens, int max_pos, int max_q, const int32_t* table) {
+  const Blank8Args a{{nullptr, table, g.Hkv, g.D, g.page_shift, g.num_pages, g.max_pages, g.B}, {q_start, lens, T, max_q},
+                     (uint8_t*)x, max_pos, 2 * n};
+  k_kv_blank8<<<dim3((T + kWavesPerBlock - 1) / kWavesPerBlock), dim3(kBlock), 0, s>>>(a);
   return hipGetLastError();
 }
 

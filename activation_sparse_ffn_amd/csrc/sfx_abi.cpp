@@ -601,6 +601,18 @@ int sfx_kv_append_q8(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int
                                                 q_start, lens, cos_sin, rot, max_pos, interleaved != 0, table, cache, q_out));
 }
 
+int sfx_kv_blank_q8(void* stream, int T, int n, const int32_t* q_start, const int32_t* lens, int max_pos, int max_q, int B,
+                    int max_pages, const int32_t* table, int page, int num_pages, void* x) {
+  sfx::KvGeom g;
+  const int st = kv_geom8(B, 1, 32, page, num_pages, max_pages, &g);
+  if (st != SFX_OK) return st;
+  if (T < 1 || T > sfx::kQ8MaxTokens || (!q_start && T != B) || max_q < 1 || max_pos < 0) return SFX_E_SHAPE;
+  if (n < 8 || n > (1 << 24) || n % 8 != 0) return SFX_E_SHAPE;
+  if (!lens || !table || !x) return SFX_E_NULL;
+  if (!aligned16(x) || !aligned4(lens) || !aligned4(table) || (q_start && !aligned4(q_start))) return SFX_E_ALIGN;
+  return launch_status(sfx::launch_kv_blank_q8((hipStream_t)stream, g, T, n, x, q_start, lens, max_pos, max_q, table));
+}
+
 int sfx_kv_read_q8(void* stream, int odt, int T, int Hkv, int D, const int32_t* pos, const int32_t* seq, int B,
                    int max_pages, const int32_t* table, int page, int num_pages, const void* cache, void* k, void* v) {
   if (!dt16_or_32(odt)) return SFX_E_DTYPE;

@@ -124,6 +124,8 @@ hipError_t launch_kv_append_q8(hipStream_t s, const KvGeom& g, int xdt, int qdt,
                                const void* k, size_t ldk, const void* v, size_t ldv, const int32_t* q_start,
                                const int32_t* lens, const float* cos_sin, int rot, int max_pos, int pairs,
                                const int32_t* table, void* cache, void* q_out);
+hipError_t launch_kv_blank_q8(hipStream_t s, const KvGeom& g, int T, int n, void* x, const int32_t* q_start,
+                              const int32_t* lens, int max_pos, int max_q, const int32_t* table);
 hipError_t launch_kv_read_q8(hipStream_t s, const KvGeom& g, int odt, int T, const int32_t* pos, const int32_t* seq,
                              const int32_t* table, const void* cache, void* k, void* v);
 

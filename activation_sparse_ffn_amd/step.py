@@ -183,7 +183,8 @@ class AttnStep8:
                accumulate: bool = False, add: torch.Tensor = None, stream=None):
         """The same for rows q_start[b] .. q_start[b + 1] - 1 (at most max_q) of x [T][d], the last
         tokens of sequence b, which has lens[b] positions with them (int32 device tensors [B + 1] and
-        [B]).  Rows of no sequence hold no result."""
+        [B]).  A row of no sequence, past a sequence's first max_q or whose position has no page in `table` or
+        no row in `cos_sin` is no token: nothing of it is stored, and its output is the bias."""
         if x.dim() != 2 or x.shape[1] != self.d or y.shape != x.shape:
             raise ValueError(f"AttnStep8: x and y must be [rows][{self.d}]")
         if x.shape[0] > self.max_tokens or max_q > self.max_tokens:
@@ -203,7 +204,11 @@ class AttnStep8:
                            q_start=q_start, cos_sin=self.cos_sin, interleaved=self.interleaved, stream=stream)
         A.sfx_attn_q8(q, self.cache, self.table, lens, o, ws, q_start=q_start, max_q=max_q, window=self.window,
                       scale=self.scale, stream=stream)
-        A.sfx_norm_q8(o.view(T, a), oq, os, norm=False, stream=stream)
+        o = o.view(T, a)
+        if q_start is not None:                          # the queries of other rows are an earlier call's
+            A.sfx_kv_blank_q8(o, lens, self.table, self.cache.shape[2] * 16, self.cache.shape[0], q_start=q_start, max_q=max_q,
+                              max_pos=0 if self.cos_sin is None else self.cos_sin.shape[0], stream=stream)
+        A.sfx_norm_q8(o, oq, os, norm=False, stream=stream)
         A.sfx_linear_q8(oq, os, g("Wo"), g("Wo_s"), y, bias=g("bo"), accumulate=accumulate, stream=stream)
 
 

@@ -16,7 +16,7 @@
  *                    offline calibration: thresholds, frequencies, hot-first order
  *   sfx_linear_q4, sfx_kv_append_q4, sfx_kv_read_q4, sfx_kv_lens_q4, sfx_attn_q4
  *                    the attention half of a layer: int4 projections, paged int4 cache
- *   sfx_norm_q8, sfx_linear_q8, sfx_kv_append_q8, sfx_kv_read_q8, sfx_attn_q8
+ *   sfx_norm_q8, sfx_linear_q8, sfx_kv_append_q8, sfx_kv_blank_q8, sfx_kv_read_q8, sfx_attn_q8
  *                    the 8-bit layer half: norm to int8 rows, int8 projections, paged int8
  *                    cache, attention of one or many tokens per sequence
  *
@@ -657,6 +657,11 @@ int sfx_linear_q8(void* stream, int ydt, int T, int n, int d, const int8_t* x, s
  * sequences of a call.  T and Hkv / D are limited together: the blocks of all heads that T rows
  * of B sequences can touch stay below 2^24 (SFX_E_SHAPE).
  *
+ * sfx_kv_blank_q8 -- zeroes the rows of x [T][n] (16-bit numbers, dense, 16-byte aligned, n a multiple of 8 up to
+ *   2^24) that are no token: rows that an append with the same q_start, lens, table and max_pos (0: no
+ *   angles) does not store, and rows past the first max_q (>= 1) of their sequence.  Run on what
+ *   sfx_attn_q8 gave, it leaves nothing there of rows whose query no append has written.
+ *
  * sfx_kv_read_q8 -- values of T listed positions: k, v [T][Hkv][D] in odt (SFX_F32 rounded once,
  *   SFX_F16 / SFX_BF16 from there), written; zeros for a padding token (as in sfx_kv_read_q4).
  *
@@ -687,6 +692,8 @@ int sfx_kv_append_q8(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int
                      const int32_t* q_start, const int32_t* lens, const float* cos_sin, int rot, int max_pos,
                      int interleaved, int B, int max_pages, const int32_t* table, int page, int num_pages,
                      void* cache, void* q_out);
+int sfx_kv_blank_q8(void* stream, int T, int n, const int32_t* q_start, const int32_t* lens, int max_pos, int max_q,
+                    int B, int max_pages, const int32_t* table, int page, int num_pages, void* x);
 int sfx_kv_read_q8(void* stream, int odt, int T, int Hkv, int D, const int32_t* pos, const int32_t* seq,
                    int B, int max_pages, const int32_t* table, int page, int num_pages,
                    const void* cache, void* k, void* v);

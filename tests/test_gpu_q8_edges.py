@@ -6,7 +6,7 @@ import torch
 from activation_sparse_ffn_amd import _abi as A
 from gpu_helpers import say
 from oracle import q8_oracle as Q
-from test_gpu_q8 import DEV, DT, HALF_STEP, TINY, check_norm, logical, make_cache, make_table, np64
+from test_gpu_q8 import DEV, DT, HALF_STEP, TINY, check_norm, logical, make_cache, make_table, np64, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,135 @@ def test_attention_windows_past_every_position():
     assert (outs[0][0][6:9] != 0).any() and (outs[0][0][:6] == 0).all()
     for o, l in outs[1:]:
         assert torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1])
+
+
+# ------------------------------------------------------------------------------ AttnStep8
+
+def make_half(d, Hq, Hkv, D, B, dt, lens, page, max_pos, max_tokens, seed):
+    """A half on a cache of noise, its weights, and the position tensor."""
+    from activation_sparse_ffn_amd import AttnStep8, rows_q8
+    g = torch.Generator().manual_seed(seed)
+    table, pages = make_table(lens, page, seed)
+    pos = torch.full((B,), -1, dtype=torch.int32, device=DEV)
+    s = AttnStep8(d, Hq, Hkv, D, B, dt, table.to(DEV), pos, pages, page=page, max_tokens=max_tokens,
+                  cos_sin=torch.from_numpy(rope_table(max_pos, D)).to(DEV) if max_pos else None)
+    s.cache.copy_(torch.randint(0, 256, s.cache.shape, generator=g, dtype=torch.uint8))
+    w = {"wn": (1 + 0.2 * torch.randn(d, generator=g)).to(DEV), "bqkv": None, "bo": torch.randn(d, generator=g).to(DEV)}
+    w["Wqkv"], w["Wqkv_s"] = rows_q8((torch.randn((Hq + 2 * Hkv) * D, d, generator=g) * d ** -0.5).to(DEV))
+    w["Wo"], w["Wo_s"] = rows_q8((torch.randn(d, Hq * D, generator=g) * (Hq * D) ** -0.5).to(DEV))
+    return s, w, pos
+
+
+@pytest.mark.parametrize("case", [(8, 2, 64, "f16", 16, [40, 12, 60]), (4, 4, 32, "bf16", 32, [70, 5, 300]), (6, 1, 128, "f16", 16, [20, 31, 130])],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_prompt_rows_that_are_no_token(case):
+    """Rows past the table of angles, without a page, in front of position 0 or of no sequence: their y is the
+    output bias, whatever earlier calls left in the object, and the other rows do not see them."""
+    Hq, Hkv, D, dt, page, counts = case
+    d, max_pos, lead, tail = 256, 33, 2, 3
+    say(f"no token {case}")
+    g = torch.Generator().manual_seed(D)
+    lens = list(counts)
+    lens[1] -= 2                                         # two rows in front of position 0
+    q_start = np.concatenate([[0], np.cumsum(counts)]) + lead
+    T = int(q_start[-1]) + tail
+    s, w, _ = make_half(d, Hq, Hkv, D, 3, dt, counts, page, max_pos, T, D)
+    s.table[2, 0] = -1                                   # the third sequence's first page is missing
+    x = torch.randn(T, d, generator=g).to(DEV)
+    start, ys = s.cache.clone(), []
+    for junk in (0.0, 3.0, float("nan")):
+        s.cache.copy_(start)
+        for t in (s.q, s.o, s.qkv):
+            t.fill_(junk)
+        y = torch.full((T, d), 9.0, device=DEV)
+        s.prompt(w, x, y, i32(q_start), i32(lens), max(counts))
+        ys.append(y)
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+    is_token = np.zeros(T, bool)
+    for b in range(3):
+        p = np.arange(lens[b] - counts[b], lens[b])
+        is_token[q_start[b]:q_start[b + 1]] = (p >= 0) & (p < max_pos) & ((b != 2) | (p >= page))
+    is_token = torch.from_numpy(is_token).to(DEV)
+    assert torch.equal(ys[0][~is_token], w["bo"].expand(T, -1)[~is_token])
+    assert (ys[0][is_token] != w["bo"]).any(1).all()
+    # the tokens' attention over what the cache holds
+    got, q, cache, table = np64(s.o[:T]), np64(s.q[:T]), s.cache.cpu(), s.table.cpu().numpy()
+    for b in range(3):
+        k, v, has = logical(cache, table, page, b, min(lens[b], max_pos), D)
+        for i in range(counts[b]):
+            t, p = int(q_start[b]) + i, lens[b] - counts[b] + i
+            if not is_token[t]:
+                continue
+            keep = np.flatnonzero(has[:p + 1])
+            for h in range(Hkv):
+                hs = slice(h * (Hq // Hkv), (h + 1) * (Hq // Hkv))
+                o, _, ab, size = Q.attention(q[t, hs], k[keep, h], v[keep, h], D ** -0.5)
+                tol, _ = Q.attention_tolerance(o, _, ab, size, np.abs(v[keep, h]).max(), len(keep), D, HALF_STEP[dt])
+                assert (np.abs(got[t, hs] - o) <= tol + TINY[dt]).all(), (b, i, h)
+    y = torch.full((T, d), 9.0, device=DEV)              # added to y: the bias alone
+    s.cache.copy_(start)
+    s.prompt(w, x, y, i32(q_start), i32(lens), max(counts), accumulate=True)
+    assert torch.equal(y[~is_token], (w["bo"] + 9.0).expand(T, -1)[~is_token])
+    # rows past max_q are stored, and have no output
+    s.cache.copy_(start)
+    s.o.fill_(5.0)
+    s.prompt(w, x, y, i32(q_start), i32(lens), 8)
+    past = torch.cat([torch.arange(T)[int(q_start[b]) + 8:int(q_start[b + 1])] for b in range(3)])
+    assert len(past) and torch.equal(y[past.to(DEV)], w["bo"].expand(len(past), -1))
+
+
+def test_prompt_without_tokens_in_a_graph():
+    """The same captured: rows become tokens and stop being tokens between replays."""
+    d, Hq, Hkv, D, B, n = 256, 4, 2, 64, 2, 48
+    say("no token, captured")
+    s, w, _ = make_half(d, Hq, Hkv, D, B, "f16", [64, 64], 16, 64, 2 * n, 1)
+    e, _, _ = make_half(d, Hq, Hkv, D, B, "f16", [64, 64], 16, 64, 2 * n, 1)
+    x, y = torch.randn(2 * n, d, device=DEV), torch.zeros(2 * n, d, device=DEV)
+    q_start, lens = i32([0, n, 2 * n]), i32([n, n])
+    s.prompt(w, x, y, q_start, lens, n)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.prompt(w, x, y, q_start, lens, n)
+    for rep, (at, ln) in enumerate((([0, n, 2 * n], [n, n]), ([0, 5, 9], [5, 70]), ([3, 3, 40], [0, 20]), ([0, n, 2 * n], [64, 80]),
+                                    ([0, n, 2 * n], [n, n]))):
+        q_start.copy_(i32(at))
+        lens.copy_(i32(ln))
+        s.cache.zero_()
+        e.cache.zero_()
+        g.replay()
+        ye = torch.zeros_like(y)
+        e.prompt(w, x, ye, i32(at), i32(ln), n)
+        torch.cuda.synchronize()
+        assert torch.equal(y, ye) and torch.equal(s.cache, e.cache), rep
+        assert torch.equal(y[at[2]:], w["bo"].expand(2 * n - at[2], -1)), rep
+
+
+@pytest.mark.parametrize("case", [(1, 16, 70, 0), (3, 32, 5, 40), (70, 16, 200, 33), (200, 64, 3, 100)], ids=str)
+def test_blank_rows(case):
+    """Rows that the append does not store and rows past max_q become zeros, the others stay."""
+    B, page, most, max_pos = case
+    say(f"blank {case}")
+    rng = np.random.default_rng(B)
+    counts, lens = rng.integers(0, 2 * most // (1 + B // 50) + 2, B), rng.integers(-3, 150, B)
+    width = 8
+    table = rng.integers(-1, 12, (B, width)).astype(np.int32)              # -1 and 10, 11 are no pages
+    q_start = np.concatenate([[0], np.cumsum(counts)]) + 2
+    T = int(q_start[-1]) + 3
+    for n in (8, 520, 4096):
+        x = torch.randn(T, n, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16 if n == 520 else torch.float16)
+        for starts in (q_start, None):
+            rows = T if starts is not None else B
+            first = q_start if starts is not None else np.arange(B + 1)
+            got = x[:rows].clone().to(DEV) if rows <= T else x.repeat(-(-rows // T), 1)[:rows].to(DEV)
+            was = got.cpu()
+            A.sfx_kv_blank_q8(got, i32(lens), torch.from_numpy(table).to(DEV), page, 10, q_start=None if starts is None else i32(starts),
+                              max_q=most, max_pos=max_pos)
+            keep = np.zeros(rows, bool)
+            for b in range(B):
+                m = int(first[b + 1] - first[b])
+                for i in range(min(m, most)):
+                    p = int(lens[b]) - m + i if lens[b] > 0 else -1
+                    keep[first[b] + i] = (not max_pos or p < max_pos) and Q.pages_of(table, page, 10, b, p) >= 0
+            assert torch.equal(got.cpu()[keep], was[keep]) and (got.cpu()[~keep] == 0).all()
+            assert B == 1 or (keep.any() and not keep.all())
