@@ -139,8 +139,9 @@ class AttnStep8:
     each sequence's token in a decode step (-1: no token; its output is the bias of the output
     projection), are the caller's and may change between steps, also of a captured graph; the attention
     covers positions max(0, pos + 1 - window) .. pos (window 0: all).  A pos without a page in `table`
-    or a row in `cos_sin` is no token either.  Prompts of up to `max_tokens` rows together.  `ffn_dtype`: that of the
-    rows that run_block's FFN reads."""
+    or a row in `cos_sin` is no token either.  Prompts of up to `max_tokens` rows together.  A step and a
+    prompt of other sequences may overlap on two streams; two steps, two prompts and calls that touch the
+    same sequence may not.  `ffn_dtype`: that of the rows that run_block's FFN reads."""
 
     def __init__(self, d: int, Hq: int, Hkv: int, D: int, B: int, dtype: str, table: torch.Tensor, pos: torch.Tensor,
                  num_pages: int, page: int = 16, cos_sin: torch.Tensor = None, interleaved: bool = False,
@@ -151,20 +152,22 @@ class AttnStep8:
         self.table, self.pos, self.cos_sin, self.interleaved, self.scale = table, pos, cos_sin, interleaved, scale
         dev = torch.device(device)
         dt = TORCH_WDT[dtype]
-        rows = max(B, max_tokens)
         self.cache = A.kv_cache_q8(num_pages, Hkv, page, D, dev)
-        self.xq = torch.empty(rows, d, dtype=torch.int8, device=dev)
-        self.xs = torch.empty(rows, dtype=torch.float32, device=dev)
-        self.qkv = torch.empty(rows, (Hq + 2 * Hkv) * D, dtype=torch.float32, device=dev)
-        self.q = torch.zeros(rows, Hq, D, dtype=dt, device=dev)
-        self.o = torch.zeros(rows, Hq, D, dtype=dt, device=dev)
-        self.oq = torch.empty(rows, Hq * D, dtype=torch.int8, device=dev)
-        self.os = torch.empty(rows, dtype=torch.float32, device=dev)
+
+        def buffers(rows):
+            return (torch.empty(rows, d, dtype=torch.int8, device=dev), torch.empty(rows, dtype=torch.float32, device=dev),
+                    torch.empty(rows, (Hq + 2 * Hkv) * D, dtype=torch.float32, device=dev),
+                    torch.zeros(rows, Hq, D, dtype=dt, device=dev), torch.zeros(rows, Hq, D, dtype=dt, device=dev),
+                    torch.empty(rows, Hq * D, dtype=torch.int8, device=dev), torch.empty(rows, dtype=torch.float32, device=dev))
+        # decode steps and prompts (of other sequences) may overlap on different streams: each has buffers and a
+        # workspace of its own
+        self._step, self._prompt = buffers(B), buffers(max_tokens)
+        # those of the last call, for a look at what it left
+        self.xq, self.xs, self.qkv, self.q, self.o, self.oq, self.os = self._prompt if max_tokens else self._step
         self.xf = torch.empty(B, d, dtype=dt if ffn_dtype is None else TORCH_WDT[ffn_dtype], device=dev)
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
         self.max_tokens = max_tokens
-        # decode steps and prompts may run on different streams, each with its workspace; calls of more
-        # than 65536 tokens per sequence take none
+        # calls of more than 65536 tokens per sequence take no workspace
         need = [A.sfx_attn_q8_ws(B, n, Hq, Hkv, D, table.shape[1] * page) for n in range(1, min(max_tokens, 65536) + 1)]
         self.ws = A.workspace(A.sfx_attn_q8_ws(B, 1, Hq, Hkv, D, table.shape[1] * page), dev)
         self.ws_prompt = A.workspace(max(need, default=0), dev)
@@ -177,7 +180,7 @@ class AttnStep8:
             raise ValueError(f"AttnStep8: x and y must be [{self.B}][{self.d}]")
         A.sfx_kv_lens_q4(self.pos, self.table, self.cache.shape[2] * 16, self.cache.shape[0], self.lens,
                          max_pos=0 if self.cos_sin is None else self.cos_sin.shape[0], stream=stream)
-        self._half(layer, x, y, None, self.lens, 1, self.ws, accumulate, add, stream)
+        self._half(layer, x, y, None, self.lens, 1, self._step, self.ws, accumulate, add, stream)
 
     def prompt(self, layer, x: torch.Tensor, y: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor, max_q: int,
                accumulate: bool = False, add: torch.Tensor = None, stream=None):
@@ -189,13 +192,14 @@ class AttnStep8:
             raise ValueError(f"AttnStep8: x and y must be [rows][{self.d}]")
         if x.shape[0] > self.max_tokens or max_q > self.max_tokens:
             raise ValueError(f"AttnStep8: {x.shape[0]} rows, up to {max_q} of a sequence; room for {self.max_tokens}")
-        self._half(layer, x, y, q_start, lens, max_q, self.ws_prompt, accumulate, add, stream)
+        self._half(layer, x, y, q_start, lens, max_q, self._prompt, self.ws_prompt, accumulate, add, stream)
 
-    def _half(self, layer, x, y, q_start, lens, max_q, ws, accumulate, add, stream):
+    def _half(self, layer, x, y, q_start, lens, max_q, buffers, ws, accumulate, add, stream):
         g = layer.get if isinstance(layer, dict) else (lambda k: getattr(layer, k, None))
         T, a, b = x.shape[0], self.Hq * self.D, self.Hkv * self.D
         wn = g("wn")
-        xq, xs, qkv, q, o, oq, os = (t[:T] for t in (self.xq, self.xs, self.qkv, self.q, self.o, self.oq, self.os))
+        self.xq, self.xs, self.qkv, self.q, self.o, self.oq, self.os = buffers
+        xq, xs, qkv, q, o, oq, os = (t[:T] for t in buffers)
         A.sfx_norm_q8(x if add is None else add, xq, xs, weight=wn, eps=self.eps, residual=None if add is None else x,
                       norm=wn is not None, stream=stream)
         A.sfx_linear_q8(xq, xs, g("Wqkv"), g("Wqkv_s"), qkv, bias=g("bqkv"), stream=stream)

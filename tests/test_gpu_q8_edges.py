@@ -266,3 +266,53 @@ def test_blank_rows(case):
                     keep[first[b] + i] = (not max_pos or p < max_pos) and Q.pages_of(table, page, 10, b, p) >= 0
             assert torch.equal(got.cpu()[keep], was[keep]) and (got.cpu()[~keep] == 0).all()
             assert B == 1 or (keep.any() and not keep.all())
+
+
+def test_steps_and_prompts_of_one_object_overlap():
+    """A decode step of other sequences that runs while a prompt is between its calls, and a prompt that runs
+    while a step is: both give what they give alone, and so does the cache."""
+    d, Hq, Hkv, D, B, n = 256, 8, 2, 64, 3, 40
+    say("step within prompt, prompt within step")
+    g = torch.Generator().manual_seed(2)
+    x, xs = torch.randn(n, d, generator=g).to(DEV), torch.randn(B, d, generator=g).to(DEV)
+    q_start, lens = i32([0, 0, n, n]), i32([0, n, 0])
+    names = ("sfx_norm_q8", "sfx_linear_q8", "sfx_kv_append_q8", "sfx_attn_q8")
+
+    def run(inner, at, monkeypatch):
+        """The prompt of sequence 1 and a step of 0 and 2, one whole inside the other before its call `at`."""
+        s, w, pos = make_half(d, Hq, Hkv, D, B, "f16", [64] * 3, 16, 64, n, 5)
+        pos.copy_(i32([0, -1, 0]))
+        yp, ys = torch.zeros(n, d, device=DEV), torch.zeros(B, d, device=DEV)
+        other = torch.cuda.Stream()
+        calls = {"prompt": lambda st: s.prompt(w, x, yp, q_start, lens, n, stream=st), "step": lambda st: s.run(w, xs, ys, stream=st)}
+        if inner is None:
+            calls["prompt"](None)
+            calls["step"](None)
+        else:
+            outer = "step" if inner == "prompt" else "prompt"
+            seen, busy = [0], [False]
+            with monkeypatch.context() as m:
+                for name in names:
+                    def call(*a, f=getattr(A, name), **k):
+                        if not busy[0]:
+                            if seen[0] == at:
+                                busy[0] = True
+                                torch.cuda.synchronize()
+                                other.wait_stream(torch.cuda.current_stream())
+                                calls[inner](other)
+                                other.synchronize()
+                                busy[0] = False
+                            seen[0] += 1
+                        return f(*a, **k)
+                    m.setattr(A, name, call)
+                calls[outer](None)
+            assert seen[0] == 6
+        torch.cuda.synchronize()
+        return yp, ys, s.cache.clone()
+
+    with pytest.MonkeyPatch.context() as m:
+        alone = run(None, 0, m)
+        for inner in ("step", "prompt"):
+            for at in range(6):
+                for a, b in zip(run(inner, at, m), alone):
+                    assert torch.equal(a, b), (inner, at)
