@@ -12,7 +12,10 @@
 //   weights  P = 2^(s + log2 vs - ref + 9) in fp32, as one fp16 operand: the scale of a block's
 //            values rides in the exponent, so the second product takes the codes as they are
 //            and its precision is relative to the largest contribution.  The sum of weights
-//            takes P / vs in fp32;
+//            takes P / vs in fp32.  That holds every weight down to 2^-39 of the largest while the scales of
+//            a row's blocks lie within 2^-64 .. 2^32; from the first block outside on, a row's sum has a
+//            reference of its own, the largest score, and takes a second exponential (State8::wide;
+//            the test for it costs 1 to 4%);
 //   output   value codes as rows of 16 dims x 32 positions.
 // The lane that holds a score holds it in the place where the second product wants the weight.
 // 131072 positions of 8 kv heads of 128 for 64 query heads: 54 us (270 MB, 5.0 TB/s of a streaming 5.3), the
@@ -29,6 +32,9 @@ namespace {
 constexpr int kTile8 = 32;             // positions a wave takes at a time
 constexpr float kRefMin8 = -3.0e38f;
 constexpr float kNoScale = 0x1p-64f;   // stands for the scale 0 of values that are all 0
+constexpr float kNotWide = INFINITY;
+// (In whole numbers, which scales that all lanes hold alike are for the scalar unit.)
+__device__ __forceinline__ bool wide_scale8(uint32_t vs) { return vs != 0 && vs - 0x1F800000u > 0x4F800000u - 0x1F800000u; }
 constexpr int attn8_waves(int NG) { return NG <= 4 ? 8 : 4; }
 
 struct Attn8Args {
@@ -39,7 +45,7 @@ struct Attn8Args {
   const int32_t* starts;
   uint8_t* out;             // [T][Hq][D] 16 bit
   float* lse;               // [T][Hq] or null
-  float* parts;             // [B][Hkv][row tiles][S] x ([R][D] sums, [R][2] reference and weight sum), R rows a tile
+  float* parts;             // [B][Hkv][row tiles][S] x ([R][D] sums, [R][4] their reference, that of the weights' sum, that sum), R rows a tile
   float k2;                 // scale log2(e)
   int Hq, G, window, RT, S;
 };
@@ -84,6 +90,31 @@ __device__ __forceinline__ float quarters_sum8(float v, int lane) {
   v += __uint_as_float(lane_xor_u32<32>(__float_as_uint(v), lane));
   return v + __uint_as_float(lane_xor_u32<16>(__float_as_uint(v), lane));
 }
+__device__ __forceinline__ uint32_t quarters_or8(uint32_t v, int lane) {
+  v |= lane_xor_u32<32>(v, lane);
+  return v | lane_xor_u32<16>(v, lane);
+}
+
+// Adds weights of scores x (-inf: does not count) to a sum of weights 2^(x - wide + 9).
+template <int N>
+__device__ __forceinline__ void add_weights8(const float (&x)[N], float& wide, float& sum) {
+  float next = wide;
+#pragma unroll
+  for (int i = 0; i < N; ++i) next = fmaxf(next, x[i]);
+  sum *= __builtin_amdgcn_exp2f(wide - next);
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f(x[i] - next + 9.f);
+  wide = next;
+}
+// 2^x as f 2^e: results may lie below fp32's normal numbers.
+struct Power8 {
+  float f;
+  int e;
+};
+__device__ __forceinline__ Power8 power8(float x) {
+  const float i = floorf(x);
+  return Power8{__builtin_amdgcn_exp2f(x - i), (int)i};
+}
 
 // First of the eight dims that a lane of quarter c feeds to product g of the scores.
 template <int NG>
@@ -114,14 +145,16 @@ __device__ __forceinline__ void tile8_load(const uint8_t* const (&blk)[2], int n
 template <int NG>
 struct State8 {
   float ref, sum;           // reference (all quarters alike), sum of this quarter's weights
+  float wide;               // the sum's own reference, or kNotWide: ref
   f32x4 acc[2 * NG];        // of product m: dims (4 c + i) 2 NG + m
 };
 
 // NC tiles of 16 rows at once, so that codes are decoded once for them.  `on`: bit 4 u + i says that
 // position 4 c + i of block u counts for this lane's row (all ones where `full`).
+// `any_wide`: a row of the wave has a reference of its own for its sum.
 template <int NG, int NC>
 __device__ __forceinline__ void tile8_run(const Tile8<NG>& t, const Raw<16> (&qf)[NC][NG], float k2, const float (&qs)[NC],
-                                          bool full, const uint32_t (&on)[NC], int lane, State8<NG> (&st)[NC]) {
+                                          bool full, const uint32_t (&on)[NC], int lane, State8<NG> (&st)[NC], bool& any_wide) {
   float s[NC][8], lv[2], inv[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -142,6 +175,8 @@ __device__ __forceinline__ void tile8_run(const Tile8<NG>& t, const Raw<16> (&qf
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[j][4 * u + i] = fmaf(p[j][i], t.s[u].x * k2 * qs[j], lv[u]);
   }
+  const bool apart[2] = {wide_scale8(__builtin_amdgcn_readfirstlane(__float_as_uint(t.s[0].y))),
+                         wide_scale8(__builtin_amdgcn_readfirstlane(__float_as_uint(t.s[1].y)))};
   Raw<16> w[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
@@ -154,13 +189,25 @@ __device__ __forceinline__ void tile8_run(const Tile8<NG>& t, const Raw<16> (&qf
       if (!(on[j] & 0x0Fu)) iv[0] = 0.f;
       if (!(on[j] & 0xF0u)) iv[1] = 0.f;
     }
+    if (__builtin_expect(any_wide || apart[0] || apart[1], 0)) {
+      const uint32_t row = quarters_or8(on[j], lane);
+      if (st[j].wide == kNotWide && ((apart[0] && (row & 0x0Fu)) || (apart[1] && (row & 0xF0u)))) st[j].wide = st[j].ref;
+      if (__any(st[j].wide != kNotWide)) any_wide = true;
+      if (st[j].wide != kNotWide) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (on[j] >> i) & 1u ? s[j][i] - lv[i >> 2] : -INFINITY;
+        add_weights8(x, st[j].wide, st[j].sum);
+        iv[0] = iv[1] = 0.f;
+      }
+    }
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, s[j][i]);
     if (__any(top > st[j].ref + 6.f)) {
       const float next = fmaxf(quarters_max8(top, lane), st[j].ref), f = exp2f(st[j].ref - next);
       st[j].ref = next;
-      st[j].sum *= f;
+      st[j].sum *= st[j].wide == kNotWide ? f : 1.f;
 #pragma unroll
       for (int m = 0; m < 2 * NG; ++m)
 #pragma unroll
@@ -244,7 +291,8 @@ __device__ __forceinline__ const uint8_t* attn8_block(const KvCache& kv, int h, 
 template <class T, int NG, int NC>
 __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a) {
   constexpr int W = attn8_waves(NG), D = 32 * NG, kThreads = W * kWave, R = 16 * NC;
-  __shared__ float sh_ref[W][16], sh_sum[W][16];
+  __shared__ float sh_ref[W][16], sh_wide[W][16], sh_sum[W][16];
+  __shared__ __attribute__((aligned(8))) uint8_t sh_any[W];
   __shared__ __attribute__((aligned(16))) float sh_acc[W * 16 * (D + 4)];
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, c = lane >> 4;
@@ -275,9 +323,11 @@ __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a
   for (int j = 0; j < NC; ++j) {
     st[j].ref = kRefMin8;
     st[j].sum = 0.f;
+    st[j].wide = kNotWide;
 #pragma unroll
     for (int m = 0; m < 2 * NG; ++m) st[j].acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+  bool any_wide = false;
   int it = tb + wave;
   if (it < te) {
     const int todo = (te - it + W - 1) / W;
@@ -313,22 +363,30 @@ __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a
           }
         }
       }
-      tile8_run<NG, NC>(cur, qf, a.k2, qs, full, on, lane, st);
+      tile8_run<NG, NC>(cur, qf, a.k2, qs, full, on, lane, st, any_wide);
       cur = nxt;
       ids = next_ids;
     }
   }
 
-  // join the waves, 16 rows at a time
-  constexpr size_t run = R * (D + 2);
+  // join the waves, 16 rows at a time; without wide rows both references are the same
+  if (lane == 0) sh_any[wave] = any_wide;
+  constexpr size_t run = R * (D + 4);
   float* part = a.parts + ((((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S + split) * run;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     if (16 * j >= rows) break;
     if (j > 0) __syncthreads();
-    const float sum = quarters_sum8(st[j].sum, lane);
+    float base = st[j].ref, sum = st[j].sum;
+    if (any_wide) {                                            // quarters have references of their own
+      const float mine = st[j].wide == kNotWide ? base : st[j].wide;
+      base = quarters_max8(mine, lane);
+      sum *= exp2f(mine - base);
+    }
+    sum = quarters_sum8(sum, lane);
     if (c == 0) {
       sh_ref[wave][n] = st[j].ref;
+      sh_wide[wave][n] = base;
       sh_sum[wave][n] = sum;
     }
 #pragma unroll
@@ -336,6 +394,8 @@ __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a
 #pragma unroll
       for (int i = 0; i < 4; ++i) sh_acc[(wave * 16 + n) * (D + 4) + (4 * c + i) * 2 * NG + m] = st[j].acc[m][i];
     __syncthreads();
+    using Flags = std::conditional_t<W == 8, uint64_t, uint32_t>;
+    const bool apart = *(const Flags*)sh_any != 0;
     for (int e = threadIdx.x; e < min(16, rows - 16 * j) * (D / 2); e += kThreads) {
       const int rr = e / (D / 2), d = 2 * (e % (D / 2));
       float ref = sh_ref[0][rr];
@@ -350,15 +410,25 @@ __global__ __launch_bounds__(attn8_waves(NG) * kWave) void k_attn_q8(Attn8Args a
         v1 = fmaf(f, p[1], v1);
         l = fmaf(f, sh_sum[w][rr], l);
       }
+      float wide = ref;
+      if (apart) {
+        wide = sh_wide[0][rr];
+#pragma unroll
+        for (int w = 1; w < W; ++w) wide = fmaxf(wide, sh_wide[w][rr]);
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) l = fmaf(exp2f(sh_wide[w][rr] - wide), sh_sum[w][rr], l);
+      }
       if (sp.active == 1) {
         const int q = R * rt + 16 * j + rr;
         const size_t o = (size_t)(sq.first + q / a.G) * a.Hq + h * a.G + q % a.G;
-        const float inv = l != 0.f ? 1.0f / l : 0.f;
-        ((uint32_t*)a.out)[(o * D + d) >> 1] = (uint32_t)to_16(T{}, v0 * inv) | ((uint32_t)to_16(T{}, v1 * inv) << 16);
-        if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
+        const Power8 up = power8(ref - wide);
+        const float inv = l != 0.f ? up.f / l : 0.f;
+        ((uint32_t*)a.out)[(o * D + d) >> 1] = (uint32_t)to_16(T{}, ldexpf(v0 * inv, up.e)) | ((uint32_t)to_16(T{}, ldexpf(v1 * inv, up.e)) << 16);
+        if (a.lse && d == 0) a.lse[o] = attn8_lse(wide, l);
       } else {
         *reinterpret_cast<float2*>(part + (16 * j + rr) * D + d) = make_float2(v0, v1);
-        if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * (16 * j + rr)) = make_float2(ref, l);
+        if (d == 0) *reinterpret_cast<float4*>(part + R * D + 4 * (16 * j + rr)) = make_float4(ref, wide, l, 0.f);
       }
     }
   }
@@ -371,41 +441,51 @@ template <class T, int NG>
 __global__ __launch_bounds__(256) void k_attn8_join(Attn8Args a, int R, int step, int least) {
   constexpr int D = 32 * NG, kItems = D / 4, kGroups = 256 / kItems;
   __shared__ __attribute__((aligned(16))) float sh_v[kGroups][D];
-  __shared__ float sh_f[256], sh_l[256 / kWave], sh_r[256 / kWave];
+  __shared__ float sh_f[256], sh_l[256 / kWave], sh_r[256 / kWave], sh_w[256 / kWave];
   const int b = blockIdx.y, per_head = a.rows.most * a.G, h = blockIdx.x / per_head, q = blockIdx.x % per_head;
   const Seq8 sq = rows8_seq(a.rows, b);
   if (q >= sq.n * a.G) return;
   const int rt = q / R, rr = q % R;
   const Span8 sp = span8(a, sq, a.starts ? max(a.starts[b], 0) : 0, rt, R, step, least);
   if (sp.active == 1) return;                                   // the attention kernel wrote the row
-  const size_t run = (size_t)R * (D + 2);
+  const size_t run = (size_t)R * (D + 4);
   const float* part = a.parts + (((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S * run;
-  const float* rs = part + (size_t)R * D + 2 * rr;
+  const float* rs = part + (size_t)R * D + 4 * rr;
   const int grp = threadIdx.x / kItems, d = 4 * (threadIdx.x % kItems), wave = threadIdx.x >> 6;
-  float ref = kRefMin8, l = 0.f;
+  float ref = kRefMin8, wide = kRefMin8, l = 0.f;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   for (int k0 = 0; k0 < sp.active; k0 += 256) {                 // 256 runs at a time (there are hardly more)
     const int k = k0 + threadIdx.x;
-    const float2 rl = k < sp.active ? *reinterpret_cast<const float2*>(rs + k * run) : make_float2(kRefMin8, 0.f);
-    float top = rl.x;
+    const float4 rl = k < sp.active ? *reinterpret_cast<const float4*>(rs + k * run) : make_float4(kRefMin8, kRefMin8, 0.f, 0.f);
+    float top = rl.x, top_w = rl.y;
 #pragma unroll
-    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    if ((threadIdx.x & 63) == 0) sh_r[wave] = top;
+    for (int o = 32; o; o >>= 1) {
+      top = fmaxf(top, __shfl_xor(top, o));
+      top_w = fmaxf(top_w, __shfl_xor(top_w, o));
+    }
+    if ((threadIdx.x & 63) == 0) {
+      sh_r[wave] = top;
+      sh_w[wave] = top_w;
+    }
     __syncthreads();
-    float next = ref;
+    float next = ref, next_w = wide;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) next = fmaxf(next, sh_r[w]);
+    for (int w = 0; w < 4; ++w) {
+      next = fmaxf(next, sh_r[w]);
+      next_w = fmaxf(next_w, sh_w[w]);
+    }
     const float f = exp2f(rl.x - next), back = exp2f(ref - next);
     sh_f[threadIdx.x] = f;
-    float sum = f * rl.y;
+    float sum = exp2f(rl.y - next_w) * rl.z;
 #pragma unroll
     for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
     if ((threadIdx.x & 63) == 0) sh_l[wave] = sum;
     __syncthreads();
-    l = l * back + ((sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]));
+    l = l * exp2f(wide - next_w) + ((sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]));
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] *= back;
     ref = next;
+    wide = next_w;
     if (grp < kGroups) {
       const int n = min(256, sp.active - k0);
 #pragma unroll 8
@@ -429,11 +509,14 @@ __global__ __launch_bounds__(256) void k_attn8_join(Attn8Args a, int R, int step
       for (int i = 0; i < 4; ++i) v[i] += o[i];
     }
     const size_t o = (size_t)(sq.first + q / a.G) * a.Hq + h * a.G + q % a.G;
-    const float inv = l != 0.f ? 1.0f / l : 0.f;
+    const Power8 up = power8(ref - wide);
+    const float inv = l != 0.f ? up.f / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i] * inv, up.e);
     uint32_t* dst = (uint32_t*)a.out + ((o * D + d) >> 1);
-    dst[0] = (uint32_t)to_16(T{}, v[0] * inv) | ((uint32_t)to_16(T{}, v[1] * inv) << 16);
-    dst[1] = (uint32_t)to_16(T{}, v[2] * inv) | ((uint32_t)to_16(T{}, v[3] * inv) << 16);
-    if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
+    dst[0] = (uint32_t)to_16(T{}, v[0]) | ((uint32_t)to_16(T{}, v[1]) << 16);
+    dst[1] = (uint32_t)to_16(T{}, v[2]) | ((uint32_t)to_16(T{}, v[3]) << 16);
+    if (a.lse && d == 0) a.lse[o] = attn8_lse(wide, l);
   }
 }
 
@@ -450,15 +533,20 @@ __global__ __launch_bounds__(256) void k_attn8_join_few(Attn8Args a, int R, int 
   const int rt = q / R, rr = q % R;
   const Span8 sp = span8(a, sq, a.starts ? max(a.starts[b], 0) : 0, rt, R, step, least);
   if (sp.active == 1) return;                                   // the attention kernel wrote the row
-  const size_t run = (size_t)R * (D + 2);
+  const size_t run = (size_t)R * (D + 4);
   const float* part = a.parts + (((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S * run;
-  const float2 rl = lane < sp.active ? *reinterpret_cast<const float2*>(part + (size_t)R * D + 2 * rr + lane * run) : make_float2(kRefMin8, 0.f);
-  float ref = rl.x;
+  const float4 rl = lane < sp.active ? *reinterpret_cast<const float4*>(part + (size_t)R * D + 4 * rr + lane * run)
+                                     : make_float4(kRefMin8, kRefMin8, 0.f, 0.f);
+  float ref = rl.x, wide = rl.y;
 #pragma unroll
-  for (int o = 8; o; o >>= 1) ref = fmaxf(ref, __shfl_xor(ref, o));
+  for (int o = 8; o; o >>= 1) {
+    ref = fmaxf(ref, __shfl_xor(ref, o));
+    wide = fmaxf(wide, __shfl_xor(wide, o));
+  }
   ref = __shfl(ref, 0);
+  wide = __shfl(wide, 0);
   const float f = exp2f(rl.x - ref);
-  float l = f * rl.y;
+  float l = exp2f(rl.y - wide) * rl.z;
 #pragma unroll
   for (int o = 8; o; o >>= 1) l += __shfl_xor(l, o);
   l = __shfl(l, 0);
@@ -481,11 +569,14 @@ __global__ __launch_bounds__(256) void k_attn8_join_few(Attn8Args a, int R, int 
     for (int i = 0; i < 4; ++i) o4[i] += __shfl(v[i], (lane + k * kItems) & (kWave - 1));
   if (lane >= kItems) return;
   const size_t o = (size_t)(sq.first + q / a.G) * a.Hq + h * a.G + q % a.G;
-  const float inv = l != 0.f ? 1.0f / l : 0.f;
+  const Power8 up = power8(ref - wide);
+  const float inv = l != 0.f ? up.f / l : 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o4[i] = ldexpf(o4[i] * inv, up.e);
   uint32_t* dst = (uint32_t*)a.out + ((o * D + d) >> 1);
-  dst[0] = (uint32_t)to_16(T{}, o4[0] * inv) | ((uint32_t)to_16(T{}, o4[1] * inv) << 16);
-  dst[1] = (uint32_t)to_16(T{}, o4[2] * inv) | ((uint32_t)to_16(T{}, o4[3] * inv) << 16);
-  if (a.lse && d == 0) a.lse[o] = attn8_lse(ref, l);
+  dst[0] = (uint32_t)to_16(T{}, o4[0]) | ((uint32_t)to_16(T{}, o4[1]) << 16);
+  dst[1] = (uint32_t)to_16(T{}, o4[2]) | ((uint32_t)to_16(T{}, o4[3]) << 16);
+  if (a.lse && d == 0) a.lse[o] = attn8_lse(wide, l);
 }
 
 // ---- many rows of a sequence.  A workgroup takes 128 or 256 rows (attn8_rows), a wave 32 of them as the
@@ -505,7 +596,7 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
   constexpr int D = 32 * NG, kRow = 2 * D + 16, kK = kTileR8 * kRow, kV = kTileR8 * 2 * D, kPieces = 4 * D, PT = (kPieces + NTH - 1) / NTH;
   constexpr bool kWhole = D % 64 == 0;                         // a wave's pieces are of one block
   __shared__ __attribute__((aligned(16))) uint8_t mem[2][kK + kV];
-  __shared__ float4 consts[2][kTileR8 / kBlk8];                // of a block: ks k2, log2 vs, 1 / vs
+  __shared__ float4 consts[2][kTileR8 / kBlk8];                // of a block: ks k2, log2 vs, 1 / vs, 1 (0: no page, 2: wide_scale8)
   const int lane = opaque_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, c = lane >> 5;
   // a head's tiles on one XCD where heads are a multiple of 8; tiles with many positions first
   const int h = blockIdx.x % a.kv.Hkv, split = blockIdx.x / a.kv.Hkv % a.S, rt = a.RT - 1 - blockIdx.x / a.kv.Hkv / a.S, b = blockIdx.y;
@@ -547,7 +638,8 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
     }
     qs = ldexpf(1.f, e);
   }
-  float ref = kRefMin8, sum = 0.f;
+  float ref = kRefMin8, sum = 0.f, wide = kNotWide;            // see State8
+  bool any_wide = false;
   f32x16 acc[NG];
 #pragma unroll
   for (int m = 0; m < NG; ++m) acc[m] = f32x16{0.f};
@@ -611,7 +703,7 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
     if (threadIdx.x < kTileR8 / kBlk8) {
       const float vs = scales.y != 0.f ? scales.y : kNoScale;
       // a block without a page counts nowhere
-      consts[buf][threadIdx.x] = const_id >= 0 ? make_float4(scales.x * a.k2, log2f(vs), 1.0f / vs, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      consts[buf][threadIdx.x] = const_id >= 0 ? make_float4(scales.x * a.k2, log2f(vs), 1.0f / vs, wide_scale8(__float_as_uint(vs)) ? 2.f : 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
 
@@ -635,7 +727,7 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
       const float base = 9.f - ref;
 #pragma unroll
       for (int i = 0; i < 16; ++i) e[i] = fmaf(sc[i], kk[i >> 3], lv[i >> 3] + base);
-      if (!(p0 >= all_lo && p0 + 32 <= all_hi && k0.w != 0.f && k1.w != 0.f)) {
+      if (!(p0 >= all_lo && p0 + 32 <= all_hi && k0.w == 1.f && k1.w == 1.f && !any_wide)) {
         bool on[2] = {false, false};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -646,6 +738,21 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
         }
         iv[0] = on[0] ? iv[0] : 0.f;
         iv[1] = on[1] ? iv[1] : 0.f;
+        if (wide == kNotWide && ((k0.w > 1.f && p0 + kBlk8 > lo && p0 < hi) || (k1.w > 1.f && p0 + 2 * kBlk8 > lo && p0 + kBlk8 < hi)))
+          wide = ref;
+        if (__any(wide != kNotWide)) {
+          any_wide = true;
+          if (wide != kNotWide) {                              // eight at a time: registers
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = e[8 * u + i] == -INFINITY ? -INFINITY : sc[8 * u + i] * kk[u];
+              add_weights8(x, wide, sum);
+            }
+            iv[0] = iv[1] = 0.f;
+          }
+        }
       }
       float top = e[0];
 #pragma unroll
@@ -661,7 +768,7 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
         const float next = fmaxf(fmaxf(top, __uint_as_float(lane_xor_u32<32>(__float_as_uint(top), lane))), ref);
         const float f = exp2f(ref - next), off = 9.f - next;
         ref = next;
-        sum *= f;
+        sum *= wide == kNotWide ? f : 1.f;
 #pragma unroll
         for (int m = 0; m < NG; ++m)
 #pragma unroll
@@ -686,10 +793,16 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
   }
 
   if (n >= wrows) return;
+  float base = ref;
+  if (any_wide) {                                              // the row's halves have references of their own
+    const float mine = wide == kNotWide ? ref : wide;
+    base = fmaxf(mine, __uint_as_float(lane_xor_u32<32>(__float_as_uint(mine), lane)));
+    sum *= exp2f(mine - base);
+  }
   sum += __uint_as_float(lane_xor_u32<32>(__float_as_uint(sum), lane));
   if (sp.active > 1) {
     const int rr = 32 * wave + n;
-    float* part = a.parts + ((((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S + split) * (size_t)(kRows8 * (D + 2));
+    float* part = a.parts + ((((size_t)b * a.kv.Hkv + h) * a.RT + rt) * a.S + split) * (size_t)(kRows8 * (D + 4));
 #pragma unroll
     for (int m = 0; m < NG; ++m)
 #pragma unroll
@@ -697,10 +810,11 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
         const f32x4 v = {acc[m][4 * q], acc[m][4 * q + 1], acc[m][4 * q + 2], acc[m][4 * q + 3]};
         *reinterpret_cast<f32x4*>(part + rr * D + 32 * m + 8 * q + 4 * c) = v;
       }
-    if (c == 0) *reinterpret_cast<float2*>(part + kRows8 * D + 2 * rr) = make_float2(ref, sum);
+    if (c == 0) *reinterpret_cast<float4*>(part + kRows8 * D + 4 * rr) = make_float4(ref, base, sum, 0.f);
     return;
   }
-  const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+  const Power8 up = power8(ref - base);
+  const float inv = sum != 0.f ? up.f / sum : 0.f;
   const size_t o = (size_t)(sq.first + tok) * a.Hq + head;
 #pragma unroll
   for (int m = 0; m < NG; ++m)
@@ -709,10 +823,11 @@ __global__ __launch_bounds__(2 * attn8_rows(NG), 2) void k_attn_q8_rows(Attn8Arg
       Raw<8> w;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        w.w[j] = (uint32_t)to_16(T{}, acc[m][4 * q + 2 * j] * inv) | ((uint32_t)to_16(T{}, acc[m][4 * q + 2 * j + 1] * inv) << 16);
+        w.w[j] = (uint32_t)to_16(T{}, ldexpf(acc[m][4 * q + 2 * j] * inv, up.e)) |
+                 ((uint32_t)to_16(T{}, ldexpf(acc[m][4 * q + 2 * j + 1] * inv, up.e)) << 16);
       *(Raw<8>*)(a.out + (o * D + 32 * m + 8 * q + 4 * c) * 2) = w;
     }
-  if (a.lse && c == 0) a.lse[o] = attn8_lse(ref, sum);
+  if (a.lse && c == 0) a.lse[o] = attn8_lse(base, sum);
 }
 
 template <class T, int NG, int NC>

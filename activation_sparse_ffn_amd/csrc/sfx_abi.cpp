@@ -75,7 +75,7 @@ bool attn8_fits(const Attn8Plan& p, int B, int Hkv) { return (long long)B * Hkv 
 
 size_t attn8_ws_bytes(const Attn8Plan& p, int B, int Hkv, int D) {
   if (p.S <= 1) return 0;
-  return (size_t)B * Hkv * p.RT * p.S * p.R * (D + 2) * 4;
+  return (size_t)B * Hkv * p.RT * p.S * p.R * (D + 4) * 4;
 }
 
 }  // namespace sfx

@@ -100,10 +100,77 @@ def check_rows(Hq, Hkv, D, dt, page, table, cache, lens, counts, window=0, seed=
                     continue
                 tol, ltol = Q.attention_tolerance(o, l, ab, size, np.abs(v[keep, h]).max(), len(keep), D, HALF_STEP[dt])
                 top = {"f16": 65520, "bf16": 2.0 ** 128 * (1 - 2.0 ** -9)}[dt]       # what is rounded to an infinity
-                over = (np.abs(o) + tol >= top) & np.isinf(got[t, hs]) & (np.sign(got[t, hs]) == np.sign(o))
+                # any number within tol of o may be what is rounded: o = 1e25 made of cancelling terms with tol = 1e28
+                # gives an infinity of either sign in fp16
+                over = np.isinf(got[t, hs]) & (np.sign(got[t, hs]) * o + tol >= top)
                 err = np.where(over, 0.0, np.abs(got[t, hs] - o))
                 assert (err <= tol + TINY[dt]).all(), (b, i, h, err.max(), o, got[t, hs])
                 assert (np.abs(gl[t, hs] - l) <= ltol).all(), (b, i, h, gl[t, hs], l)
+
+
+SCALES = {  # values' scales by page, powers of two
+    "tiny": [-116], "tiniest": [-127], "subnormal": [-140, -149], "one tiny": [0, 0, 0, -127, 0], "one subnormal": [-145, 0, 0],
+    "small beside smaller": [-60, -70, -100, -130], "huge": [120], "huge and tiny": [110, -60, -127], "huge and zero": [100, None],
+    "apart": [100, 60, 30, 0, -30, -64, -90, -128, -149], "zero alone": [None], "tiny and zero": [-149, None]}
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("name", SCALES)
+def test_attention_value_scales_of_any_size(name, dt):
+    """Blocks whose values are tiny, subnormal, huge or zero, alone and beside others, few rows and many, in
+    one run and in several: weights count whatever the size of the values that they weigh."""
+    page = 16
+    for Hq, Hkv, D, lens, counts in ((2, 1, 64, [150, 33], [1, 1]), (2, 1, 64, [150, 20], [11, 3]), (4, 2, 96, [300], [60]),
+                                     (2, 2, 128, [1500], [1]), (2, 1, 32, [700, 200], [140, 70]), (1, 1, 256, [1100], [120]), (1, 1, 64, [9000], [1])):
+        say(f"value scales {name} {dt} {Hq}/{Hkv}x{D} {lens}")
+        table, pages = make_table(lens, page, 7)
+        cache = make_cache(pages, Hkv, page, D, 8, uneven=False)
+        s = cache[..., 32 * D:].contiguous().view(torch.float32)
+        for b in range(len(lens)):
+            for j in range(-(-lens[b] // page)):
+                e, pg = SCALES[name][j % len(SCALES[name])], int(table[b, j])
+                s[pg, ..., 1] = 0.0 if e is None else torch.ldexp(1 + (s[pg, ..., 1] * 30), torch.tensor(e)) if e > -126 else 2.0 ** e
+                if e is None:
+                    cache[pg, ..., 16 * D:32 * D] = 128
+        cache[..., 32 * D:] = s.view(torch.uint8)
+        for q_scale in (1.3, 20.0):
+            check_rows(Hq, Hkv, D, dt, page, table, cache, lens, counts, rows=6, q_scale=q_scale)
+        check_rows(Hq, Hkv, D, dt, page, table, cache, lens, counts, rows=6, window=50)
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [9, 3], [90, 40]], ids=str)
+def test_attention_blocks_not_covered_change_no_bit(counts):
+    """Whatever scales lie in blocks that a row does not cover (behind its window, past its position), its result
+    has the same bits; and so have rows beside one that does cover them."""
+    Hq, Hkv, D, page, lens = 4, 2, 64, 16, [400, 120]
+    table, pages = make_table([448, 192], page, 7)
+    plain = make_cache(pages, Hkv, page, D, 8)
+    q_start = np.concatenate([[0], np.cumsum(counts)])
+    q = torch.randn(int(q_start[-1]), Hq, D, generator=torch.Generator().manual_seed(1)).half().to(DEV)
+    ws = A.workspace(A.sfx_attn_q8_ws(2, max(counts), Hq, Hkv, D, table.shape[1] * page))
+
+    def run(cache, window):
+        out, lse = torch.empty_like(q), torch.empty(len(q), Hq, device=DEV)
+        A.sfx_attn_q8(q, cache.to(DEV), table.to(DEV), i32(lens), out, ws, q_start=i32(q_start), max_q=max(counts), window=window, lse=lse)
+        return out, lse
+    for window in (0, 40):
+        want = run(plain, window)
+        for scale in (float("nan"), 0.0, 2.0 ** -140, 2.0 ** -70, 2.0 ** 100):
+            for pos in (0, 300, 384, 400, 416):                # the block that takes this scale
+                cache = plain.clone()
+                for b in range(2):
+                    at = min(pos, 448 if b == 0 else 191) // page
+                    s = cache[int(table[b, at])][..., 32 * D:].contiguous().view(torch.float32)
+                    s[..., 1] = scale
+                    cache[int(table[b, at])][..., 32 * D:] = s.view(torch.uint8)
+                got = run(cache, window)
+                for b in range(2):
+                    first = min(pos, 448 if b == 0 else 191) // page * page
+                    p = torch.arange(lens[b] - counts[b], lens[b])
+                    sees = (first <= p) & ((first + 15 > p - window) if window else (first >= 0))
+                    rows = torch.arange(int(q_start[b]), int(q_start[b + 1]))[~sees]
+                    for g, w in zip(got, want):
+                        assert torch.equal(g[rows.to(DEV)], w[rows.to(DEV)]), (window, scale, pos, b)
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
