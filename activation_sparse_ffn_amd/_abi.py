@@ -780,7 +780,7 @@ def sfx_attn_q4(q, cache, table, lens, out, ws, starts=None, scale=None, lse=Non
             (SFX_F16 if qdt is _F16 else SFX_BF16, B, Hq, Hkv, D, q.data_ptr(),
              Hq * D if q.is_contiguous() else _head_rows(q, w, "q"), max_pages,
              table.data_ptr(), page, num_pages, cache.data_ptr(),
-             None if starts is None else _tokens(starts, B, dev, w, "starts"), _tokens(lens, B, dev, w, "lens"),
+             None if starts is None else _tokens(starts, B, dev, w, "starts"), lens.data_ptr(),
              D ** -0.5 if scale is None else float(scale), out.data_ptr(), pl, pw, nws), w)
 
 
