@@ -129,6 +129,19 @@ def rows_q8(w: torch.Tensor, stream=None):
     return q, s
 
 
+def _prompt_ws(B: int, Hq: int, Hkv: int, D: int, max_len: int, max_q: int) -> int:
+    """Largest workspace of sfx_attn_q8 calls with 1 .. max_q rows of a sequence.  Past 96 rows of a kv head it
+    goes by the number of tiles of 128 or 256, and once a call takes none, calls of more rows do not either."""
+    G, need, n = Hq // Hkv, 0, 1
+    while n <= max_q:
+        ws = A.sfx_attn_q8_ws(B, n, Hq, Hkv, D, max_len)
+        need = max(need, ws)
+        if n == max_q or (ws == 0 and n * G > 96):
+            break
+        n = n + 1 if n * G <= 96 else min(n + max(1, 128 // G), max_q)
+    return need
+
+
 class AttnStep8:
     """The attention half of one layer in int8, for decode steps and for prompts: rows to int8
     (normed first where the layer has the norm's weight `wn`), projection to queries, keys and
@@ -167,10 +180,8 @@ class AttnStep8:
         self.xf = torch.empty(B, d, dtype=dt if ffn_dtype is None else TORCH_WDT[ffn_dtype], device=dev)
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
         self.max_tokens = max_tokens
-        # calls of more than 65536 tokens per sequence take no workspace
-        need = [A.sfx_attn_q8_ws(B, n, Hq, Hkv, D, table.shape[1] * page) for n in range(1, min(max_tokens, 65536) + 1)]
         self.ws = A.workspace(A.sfx_attn_q8_ws(B, 1, Hq, Hkv, D, table.shape[1] * page), dev)
-        self.ws_prompt = A.workspace(max(need, default=0), dev)
+        self.ws_prompt = A.workspace(_prompt_ws(B, Hq, Hkv, D, table.shape[1] * page, max_tokens), dev)
 
     def run(self, layer, x: torch.Tensor, y: torch.Tensor, accumulate: bool = False, add: torch.Tensor = None,
             stream=None):

@@ -35,3 +35,50 @@ def test_blank_binding_refusals():
     for bad in (dict(x=x.float()), dict(table=table.long())):
         with pytest.raises(TypeError):
             A.sfx_kv_blank_q8(**{**args, **bad})
+
+
+PROMPT_WS = [  # B, Hq, Hkv, D, max_len, max_q
+    (1, 1, 1, 64, 1 << 17, 40000), (1, 64, 8, 128, 131072, 5000), (3, 6, 2, 96, 5000, 5000), (16, 128, 8, 64, 4096, 3000),
+    (1, 256, 1, 256, 1 << 20, 600), (2, 7, 7, 160, 700, 3000), (64, 32, 32, 128, 8192, 200), (1, 4, 4, 32, 256, 3000), (1, 20, 1, 224, 3000, 97),
+    (5, 40, 8, 128, 100000, 1), (1, 96, 1, 128, 9000, 2), (1, 1, 1, 128, 1 << 20, 33000)]
+
+
+@pytest.mark.parametrize("case", PROMPT_WS, ids=str)
+def test_prompt_workspace_fits_every_row_count(case, monkeypatch):
+    """The largest of all row counts' workspaces, from a few hundred calls."""
+    from activation_sparse_ffn_amd import step
+    B, Hq, Hkv, D, max_len, max_q = case
+    want = max(A.sfx_attn_q8_ws(B, n, Hq, Hkv, D, max_len) for n in range(1, max_q + 1))
+    calls, ask = [0], A.sfx_attn_q8_ws
+
+    def counted(*a):
+        calls[0] += 1
+        return ask(*a)
+    monkeypatch.setattr(A, "sfx_attn_q8_ws", counted)
+    assert step._prompt_ws(*case) == want
+    assert calls[0] <= 96 + 500
+    assert step._prompt_ws(B, Hq, Hkv, D, max_len, 0) == 0
+
+
+def test_half_asks_for_few_workspaces(monkeypatch):
+    from activation_sparse_ffn_amd import AttnStep8
+    calls, ask = [0], A.sfx_attn_q8_ws
+
+    def counted(*a):
+        calls[0] += 1
+        return ask(*a)
+    monkeypatch.setattr(A, "sfx_attn_q8_ws", counted)
+    table, pos = torch.zeros(1, 64, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    s = AttnStep8(64, 8, 2, 64, 1, "f16", table, pos, 64, max_tokens=1024, device="cpu")
+    assert calls[0] < 100
+    assert s.ws_prompt.numel() >= max(ask(1, n, 8, 2, 64, 1024) for n in range(1, 1025))
+
+
+def test_half_keeps_steps_and_prompts_apart():
+    """No buffer that a decode step writes is one that a prompt writes."""
+    from activation_sparse_ffn_amd import AttnStep8
+    table, pos = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    s = AttnStep8(64, 8, 2, 64, 2, "f16", table, pos, 8, max_tokens=20, device="cpu")
+    spans = [[(t.data_ptr(), t.data_ptr() + t.nbytes) for t in side] for side in (s._step, s._prompt)]
+    for a0, a1 in spans[0]:
+        assert a1 > a0 and all(b1 <= a0 or a1 <= b0 for b0, b1 in spans[1])
