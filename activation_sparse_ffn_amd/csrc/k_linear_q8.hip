@@ -422,6 +422,8 @@ void few_run(hipStream_t st, const Linear8Args& a, int rt) {
 //   128 x 128     4.8 + 5.4e-3 d with four stages, 1024 x 4096 x 4096 27.9 (few 39.6, 256 x 256 59)
 //                 5.5 + 8.2e-3 d with two, two workgroups per unit: 512 x 11008 x 4096 44 (256 x 256 64)
 //   256 x 256     13 + 11.5e-3 d    4096 x 4096 x 4096 60 (128 x 128 78)
+// Not in the costs: pieces of 128 columns that do not divide by a workgroup's waves (1056 columns are nine for
+// the eight waves of `few`: the ninth is a round of its own).
 enum { kFew, kTile64, kTile128x4, kTile128x2, kTile256 };
 struct Choice8 {
   int kind, nt, rt;
@@ -454,7 +456,9 @@ hipError_t launch_linear_q8(hipStream_t st, int ydt, int T, int n, int d, const 
                             const int8_t* W, const float* sw, const float* bias, int accumulate, void* y, size_t ldy) {
   const Linear8Args a{x, ldx, sx, W, sw, bias, y, ldy, T, n, d, accumulate, ydt};
   if (T <= 4 && n <= 8192) {
-    // 1 x 4096 x 4096: 5.2 us, 6.0 with lines through LDS; 1 x 11008 x 4096: 10.6 and 10.9
+    // here and with lines through LDS, us: 1 x 4096 x 4096 5.5 and 5.9, 1 x 8192 x 4096 7.8 and 9.1, 4 x 8192 x 4096 8.4
+    // and 9.2.  With more rows it goes by the columns: 1 x 11008 x 4096 10.7 and 11.1, 4 x 11008 x 4096 11.6 and 11.0,
+    // 9000 x 1024 6.9 and 4.8, 28672 x 7168 41.4 and 40.0, 32768 x 8192 46.9 and 56.8
     k_linear_q8_one<16, 4><<<dim3((n + 15) / 16), dim3(16 * kWave), 0, st>>>(a);
     return hipGetLastError();
   }

@@ -49,10 +49,13 @@ size_t attn_ws_bytes(const AttnPlan& p, int B, int Hkv, int D) {
 }
 
 // Rows of a tile and runs of its positions.  Up to 96 rows of a sequence and kv head: 16 or 32 at a time,
-// waves deal the positions among themselves, two workgroups of eight waves per compute unit and no run
-// shorter than a tile of positions per wave; 256 units are left whole.  More rows: 128 or 256 at a time,
-// one or two workgroups per compute unit, no run shorter than 256 positions, and a workspace of at most 64
-// MiB.  16 sequences of 4096 with 8 kv heads of 64, 48, 80 and 112 rows: 32, 58 and 61 us by 32 rows, 48,
+// waves deal the positions among themselves, at least 512 workgroups and no run shorter than a tile of
+// positions per wave; 256 units are left whole.  By registers one workgroup of eight waves fits a compute unit at
+// heads of 96 and 128 and with two tiles of heads of 64, two or three fit below: 512 are two rounds there, and
+// whether one round of 256 is better goes by how runs fill it.  8 kv heads of 128, one token, by 512 and 256: 1 x
+// 131072 64.7 and 60.4 us, 8 x 4096 24.7 and 21.2, 17 x 4096 43 and 46, 20 x 4096 52 and 53, 28 x 4096 64 and 61
+// (by 768: 70, 28, 46, 56, 67).  More rows: 128 or 256 at a time, no run shorter than 256 positions, and a
+// workspace of at most 64 MiB.  16 sequences of 4096 with 8 kv heads of 64, 48, 80 and 112 rows: 32, 58 and 61 us by 32 rows, 48,
 // 51 and 55 by 128; 80 rows of lengths up to 4096 behind a window of 1500: 16 and 26; 131072 positions, 8
 // kv heads of 128, 64 and 120 rows: 100 and 161, 124 and 134.
 Attn8Plan attn8_plan(int B, int max_q, int Hq, int Hkv, int D, int max_len) {

@@ -683,8 +683,9 @@ int sfx_linear_q8(void* stream, int ydt, int T, int n, int d, const int8_t* x, s
  *   ws        >= sfx_attn_q8_ws(B, max_q, Hq, Hkv, D, max_pages * page) bytes, any contents.  A
  *             workspace used with several B or max_q has the largest size that any of them needs.
  * Scores, sums and results are fp32, a weight is rounded once to fp16, down to 2^-33 of the largest
- * contribution of a block's values; codes are exact.  Bitwise reproducible for the same shapes, lens and
- * q_start.
+ * contribution of a row's values, whatever their scales (fp16 results are off by 2.7e-4 of themselves, root mean
+ * square, 2.1e-4 of it their own rounding); codes are exact.  Bitwise reproducible for the same shapes, lens
+ * and q_start.
  * ------------------------------------------------------------------------------- */
 size_t sfx_kv_cache_q8_bytes(int Hkv, int D, int page, int num_pages);
 int sfx_kv_append_q8(void* stream, int xdt, int qdt, int T, int Hq, int Hkv, int D,
