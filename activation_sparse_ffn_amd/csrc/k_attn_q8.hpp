@@ -21,8 +21,8 @@
 //            instead of 53, eight 115 instead of 103, 8192 tokens in one sequence 769 instead of 566;
 //   output   value codes as rows of 16 dims x 32 positions.
 // The lane that holds a score holds it in the place where the second product wants the weight.
-// 131072 positions of 8 kv heads of 128 for 64 query heads: 54 us (270 MB, 5.0 TB/s of a streaming 5.3), the
-// join 4.8.  8192 tokens of 32 / 8 heads of 128 in one sequence: 581 us (946 TFLOP/s).
+// 131072 positions of 8 kv heads of 128 for 64 query heads: 56-58 us (270 MB, 4.7 TB/s of a streaming 5.3), the
+// join 4.3.  8192 tokens of 32 / 8 heads of 128 in one sequence: 566 us (971 TFLOP/s).
 // The reference is raised only when an exponent passes it by 6, so P stays below 2^15.
 #pragma once
 #include "sfx_kv8.hpp"

@@ -130,7 +130,7 @@ hipError_t launch_kv_read_q8(hipStream_t s, const KvGeom& g, int odt, int T, con
                              const int32_t* table, const void* cache, void* k, void* v);
 
 // Rows of a workgroup of the kernel for many of them, D = 32 NG.  256 share the decoding (8192 tokens
-// of 32/8 heads of 128: 581 us, 621 by 128).  Where that is little, at heads of 32 and 64, three workgroups of 128
+// of 32/8 heads of 128: 581 us and 621 by 128 when both were there, 566 now).  Where that is little, at heads of 32 and 64, three workgroups of 128
 // fit a compute unit and do not hold each other up (heads of 64, 4096 tokens: 201 us, 217 by 256).  From heads of 160 on a
 // wave needs the registers of a SIMD for itself and the two buffers most of the LDS: one workgroup of four waves
 // (heads of 256, 4096 tokens: 249 us, 323 by 256).
