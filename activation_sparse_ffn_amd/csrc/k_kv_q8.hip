@@ -8,8 +8,9 @@
 // border, where it is taken in 64 bits: codes are those of the exact quotient.
 //
 // 4095 tokens of 64 query and 8 kv heads of 128 dims, bf16: 34-40 us (160 MB, 4.0-4.7 TB/s); 8 single tokens of 32
-// heads: 6.0 us, offsets, page, rows, scale and kept codes one behind the other.  Reading 4109 positions of
-// 8 heads back: 8 us (25 MB).
+// heads: 6.0 us, offsets, page, rows, scale and kept codes one behind the other.  Where a half of the rotated
+// dims is no whole slice of 8, or rows are not aligned, elements are loaded one by one: 40 of 128 dims rotated 53 us (64
+// of them 36), 24 of 96 50 (32 of them 34), single tokens 7.0.  Reading 4109 positions of 8 heads back: 8 us (25 MB).
 //
 // A workgroup takes one block of one head (several heads of fewer than 128 dims): the scale needs
 // all of a block's new rows.  Sequences' blocks are numbered one behind the other, so no
