@@ -100,8 +100,8 @@ def check_rows(Hq, Hkv, D, dt, page, table, cache, lens, counts, window=0, seed=
                     continue
                 tol, ltol = Q.attention_tolerance(o, l, ab, size, np.abs(v[keep, h]).max(), len(keep), D, HALF_STEP[dt])
                 top = {"f16": 65520, "bf16": 2.0 ** 128 * (1 - 2.0 ** -9)}[dt]       # what is rounded to an infinity
-                # any number within tol of o may be what is rounded: o = 1e25 made of cancelling terms with tol = 1e28
-                # gives an infinity of either sign in fp16
+                # any number of [o - tol, o + tol] may be what is rounded, and both ends round to infinities where tol is
+                # past the top: of terms that cancel, either sign
                 over = np.isinf(got[t, hs]) & (np.sign(got[t, hs]) * o + tol >= top)
                 err = np.where(over, 0.0, np.abs(got[t, hs] - o))
                 assert (err <= tol + TINY[dt]).all(), (b, i, h, err.max(), o, got[t, hs])
